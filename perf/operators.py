@@ -8,7 +8,8 @@
 
 `own` False computes them in their plain form (elementary torch operations in fp32); True makes the calls of the package.
 8-bit moments: 256-element blocks of a tensor hold m / s_m and sqrt(v) / s_v in e4m3, with s = (largest magnitude in the
-block) / 448 in fp32 and s = 0 for a block whose largest magnitude is below 2^-100.
+block) / 448 in fp32 and s = 0 for a block whose largest magnitude is below 2^-100; a positive sqrt(v) keeps at least the
+smallest code.
 """
 import math
 
@@ -19,6 +20,7 @@ own = False
 
 BLOCK = 256           # elements that share one scale of an 8-bit moment
 TOP = 448.0           # largest e4m3 value
+LEAST = 2.0 ** -9     # smallest positive one
 TINY = 2.0 ** -100    # a block whose largest magnitude is below this is held as zeros
 LR, B1, B2, EPS, WD, STEP = 1e-3, 0.9, 0.999, 1e-8, 0.1, 100
 
@@ -111,14 +113,16 @@ def _spans(case):
     return spans, split, at
 
 
-def _to_e4m3(x):
-    """(codes, scales) of a flat fp32 buffer of whole blocks."""
+def _to_e4m3(x, least=0.0):
+    """(codes, scales) of a flat fp32 buffer of whole blocks; positive values are held as at least `least`."""
     b = x.view(-1, BLOCK)
     top = b.abs().amax(1)
     zero = top < TINY
     scale = torch.where(zero, torch.zeros_like(top), top * (1.0 / TOP))
     inv = torch.where(zero, torch.zeros_like(top), torch.full_like(top, TOP) / top)
-    return (b * inv[:, None]).to(torch.float8_e4m3fn).view(-1), scale
+    near = b * inv[:, None]
+    near = torch.where(near > 0, near.clamp(min=least), near)
+    return near.to(torch.float8_e4m3fn).view(-1), scale
 
 
 def _from_e4m3(code, scale):
@@ -175,7 +179,7 @@ def prepare(case, seed):
                  g_scale=torch.tensor([0.5], device="cuda"))
         if case["bits"] == 8:
             s["m"], s["ms"] = _to_e4m3(flat["m"])
-            s["v"], s["vs"] = _to_e4m3(flat["r"])
+            s["v"], s["vs"] = _to_e4m3(flat["r"], LEAST)
         else:
             s["m"], s["v"] = flat["m"], flat["r"].square_()
         if own:
@@ -265,8 +269,8 @@ def _adam(s):
     w -= (m / (1 - B1 ** STEP)) / (r / math.sqrt(1 - B2 ** STEP) + EPS) * LR
     s["Wb"].copy_(w)
     if eight:
-        for name, x in (("m", m), ("v", r)):
-            code, scale = _to_e4m3(x)
+        for name, x, least in (("m", m, 0.0), ("v", r, LEAST)):
+            code, scale = _to_e4m3(x, least)
             s[name].copy_(code)
             s[name + "s"].copy_(scale)
     else:
@@ -392,12 +396,12 @@ def exact(case, seed):
     if case["bits"] == 32:
         return {"W": w, "Wb": w, "m": m, "v": v}
     held = {"W": w, "Wb": w}
-    for name, x in (("m", m), ("v", v.sqrt())):
+    for name, x, least in (("m", m, 0.0), ("v", v.sqrt(), LEAST)):
         top = x.view(-1, BLOCK).abs().max(1).values
         scale = torch.where(top < TINY, 0.0, top / TOP)
         near = x.view(-1, BLOCK) / torch.where(scale > 0, scale, 1.0)[:, None]
         # e4m3: three bits after the leading one down to 2^-6, steps of 2^-9 below
         step = torch.exp2(torch.floor(torch.log2(near.abs().clamp(min=2.0 ** -6))) - 3)
-        held[name] = (torch.round(near / step) * step).view(-1)
+        held[name] = (torch.round(torch.where(near > 0, near.clamp(min=least), near) / step) * step).view(-1)
         held[name + "s"] = scale
     return held
