@@ -59,7 +59,9 @@ typedef enum {
     DUST_OP_CREDIT = 1,
     DUST_OP_WEIGHT_GRAD = 2,
     DUST_OP_LOGITS_CE = 3, /* d_in = vocabulary size V, d_out = slab size S */
-    DUST_OP_SPSA_PROBE = 4 /* K = number of probes P */
+    DUST_OP_SPSA_PROBE = 4, /* K = number of probes P */
+    DUST_OP_LINEAR_BACKWARD = 5,
+    DUST_OP_EMBEDDING_GRAD = 6 /* d_in = table rows V, d_out = d; dt = type of g */
 } dust_op;
 
 /* Identifies the noise of one call.  seed: generator key; layer_id: fourth counter word, so
@@ -110,6 +112,78 @@ dust_status dust_noisy_linear_output(const void* x, const void* W, dust_dtype dt
                                      int32_t d_in, int32_t d_out, int32_t K, float sigma,
                                      dust_noise_key key, void* y_out, dust_dtype out_dt,
                                      int64_t ld_out, void* stream);
+
+/*
+ * The linear layer itself with its epilogue: the clean forward of a block's layer, and the
+ * recomputation of the layers behind a perturbed one.
+ *   z_t = W x_t + bias,   y_t = act(z_t) + residual_t
+ * x: bf16 [N, ld_x], W: bf16 [d_out, d_in] (d_in, d_out multiples of 16); bias: fp32 [d_out] or
+ * NULL; residual: [N, ld_res] of type out_dt or NULL; y: [N, ld_y] of type out_dt (fp32 or bf16);
+ * z: optional bf16 [N, ld_z], the pre-activation for dust_linear_backward (NULL to skip).
+ * Row strides (elements) at least the row and a multiple of 16 bytes; all pointers 16-byte
+ * aligned.  y may be the residual's buffer (with the same stride); other overlaps are undefined.
+ * Sums in fp32; each output is rounded once.  Rows behind N and columns behind d_out are not
+ * written.  Up to 8 tokens stream W through the CUDA cores, more go to the tensor cores, so the
+ * last bit of a sum can depend on which.  Deterministic.
+ *   DUST_ACT_GELU: z Phi(z);  DUST_ACT_GELU_TANH: z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2;
+ *   DUST_ACT_SILU: z / (1 + exp(-z));  DUST_ACT_RELU: max(z, 0).
+ */
+typedef enum {
+    DUST_ACT_NONE = 0,
+    DUST_ACT_RELU = 1,
+    DUST_ACT_GELU = 2,
+    DUST_ACT_GELU_TANH = 3,
+    DUST_ACT_SILU = 4
+} dust_act;
+
+dust_status dust_linear(const void* x, int64_t ld_x, const void* W, const float* bias, dust_act act,
+                        const void* residual, int64_t ld_res, dust_dtype dt, int64_t N, int32_t d_in,
+                        int32_t d_out, void* y, dust_dtype out_dt, int64_t ld_y, void* z, int64_t ld_z,
+                        void* stream);
+
+/*
+ * The layer's exact gradients from the gradient dy at its output (the residual's gradient is dy
+ * itself): to carry an output-error estimate g back through the layers of a block, and to compare
+ * the estimate G_W with the true gradient.
+ *   dz_t = dy_t act'(z_t);   dx_t = W^T dz_t;   dW (+)= sum_t dz_t x_t^T;   db (+)= sum_t dz_t
+ * dy: [N, ld_dy] of type dy_dt (fp32 or bf16); z: bf16 [N, ld_z] as dust_linear left it (ignored
+ * and may be NULL for DUST_ACT_NONE); x, W as in dust_linear.  dx: [N, ld_dx] of type dx_dt; dW:
+ * fp32 [d_out, d_in]; db: fp32 [d_out]; each NULL to skip, not all three.  accumulate != 0 adds to
+ * dW and db (dx is always overwritten).
+ * dz enters the tensor cores as g_terms bf16 terms (as g in dust_weight_grad) in dW and in an fp32
+ * dx; a bf16 dx takes one term.  A bf16 dy without an activation is exact in one.  dx may not
+ * overlap an input.  N <= 8388607.
+ * workspace: dust_workspace_size(DUST_OP_LINEAR_BACKWARD, DUST_BF16, N, d_in, d_out, 0) bytes.
+ * Deterministic.
+ */
+dust_status dust_linear_backward(const void* dy, dust_dtype dy_dt, int64_t ld_dy, const void* z, int64_t ld_z,
+                                 const void* x, int64_t ld_x, const void* W, dust_act act, dust_dtype dt,
+                                 int64_t N, int32_t d_in, int32_t d_out, int32_t g_terms, void* dx,
+                                 dust_dtype dx_dt, int64_t ld_dx, float* dW, float* db, int accumulate,
+                                 void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Token embedding: out_t = scale E[ids_t].  ids: DEVICE int32 [N]; E: [V, ld_E] of type dt, out:
+ * [N, ld_out] of type out_dt, both with d valid columns (any d >= 1; columns behind d are not
+ * written).  A negative id is padding and gives a zero row; an id >= V gives a NaN row (as an
+ * invalid target does in dust_noisy_logits_ce).  Row strides at least d and a multiple of 16 bytes.
+ */
+dust_status dust_embedding(const int32_t* ids, const void* E, dust_dtype dt, int64_t ld_E, int64_t N, int32_t V,
+                           int32_t d, float scale, void* out, dust_dtype out_dt, int64_t ld_out, void* stream);
+
+/*
+ * The gradient of the embedding table, the weight estimate of a layer whose input is one-hot:
+ *   G[v] (+)= scale sum_{t: ids_t = v} g_t
+ * g: [N, ld_g] of type dt, the gradient (or output-error estimate) at the embedding's output; G: fp32
+ * [V, ld_G].  accumulate == 0 overwrites all V rows (rows without tokens with zeros), accumulate != 0
+ * adds to the rows that have tokens and leaves the others (for a table shared with the output layer).
+ * Tokens whose id is outside [0, V) add nothing.  Sums in fp32, in token order within runs of sorted
+ * tokens: deterministic.  N and V below 2^31 - 1.
+ * workspace: dust_workspace_size(DUST_OP_EMBEDDING_GRAD, dt, N, V, d, 0) bytes.
+ */
+dust_status dust_embedding_grad(const int32_t* ids, const void* g, dust_dtype dt, int64_t ld_g, int64_t N,
+                                int32_t V, int32_t d, float scale, float* G, int64_t ld_G, int accumulate,
+                                void* workspace, size_t ws_bytes, void* stream);
 
 /*
  * LM-head perturbation on cached logits (Dust page, section "간섭(interference) 줄이기": the
@@ -292,6 +366,46 @@ typedef struct {
  * receives the updated W rounded to bf16 (for the next forward).  `opt` is a HOST pointer. */
 dust_status dust_optimizer_step(const dust_opt_params* opt, const float* G, float* W,
                                 void* W_bf16, float* m, float* v, int64_t n, void* stream);
+
+/*
+ * dust_optimizer_step over many tensors in one launch (up to 256 tensors; more take more
+ * launches): the update of a whole stack, embedding and biases included.  With DUST_STATE_E4M3
+ * (Adam only) the moments are held in 8 bits: for each block of DUST_STATE_BLOCK consecutive
+ * elements of a tensor (the last one may be shorter), m holds e4m3 codes of m_i / s and v holds
+ * e4m3 codes of sqrt(v_i) / s, s = (largest magnitude in the block) / 448 in m_scale / v_scale
+ * (a block whose largest magnitude is below 2^-100 is held as zeros).  All-zero codes and
+ * scales are the initial state.  Codes are rounded to nearest even from the step's fp32
+ * moments; the weights use the unrounded ones.
+ * tensors: HOST array of descriptors; the pointers inside are DEVICE pointers, all 16-byte
+ *   aligned, and no tensor may overlap another (or be listed twice).  n = 0 tensors are skipped.
+ * g_dt: type of every G.  g_scale: optional DEVICE fp32 scalar that multiplies every G (a batch
+ *   normalisation or clipping factor computed on the device); NULL is 1.
+ * step: optional DEVICE int32 scalar with Adam's step count t, read by the kernels (values
+ *   below 1 are taken as 1), so that a captured graph can be replayed over the steps; NULL takes
+ *   opt->step.  opt->step must be >= 1 in either case.
+ * A non-finite gradient makes its element's weight and moments non-finite (with 8-bit moments,
+ * its block's moments).  Deterministic.
+ */
+#define DUST_STATE_BLOCK 256
+
+typedef enum { DUST_STATE_F32 = 0, DUST_STATE_E4M3 = 1 } dust_state_dtype;
+
+typedef struct {
+    const void* G;     /* [n], read; of type g_dt */
+    float* W;          /* [n] fp32 master weights, updated */
+    void* W_bf16;      /* [n] bf16 copy of the updated weights, or NULL */
+    void* m;           /* [n] fp32, or e4m3 codes */
+    void* v;           /* [n] fp32, or e4m3 codes of sqrt(v); NULL for SGD */
+    float* m_scale;    /* [ceil(n / 256)] with 8-bit moments, else NULL */
+    float* v_scale;    /* the same */
+    int64_t n;
+    float lr_scale;    /* >= 0, multiplies opt->lr for this tensor */
+    float decay_scale; /* >= 0, multiplies opt->weight_decay for this tensor (0: no decay) */
+} dust_opt_tensor;
+
+dust_status dust_optimizer_step_grouped(const dust_opt_params* opt, const dust_opt_tensor* tensors,
+                                        int32_t n_tensors, dust_dtype g_dt, dust_state_dtype state,
+                                        const float* g_scale, const int32_t* step, void* stream);
 
 /* dust_weight_grad with the optimizer step fused into the pass that finishes G_W (the
  * contraction's epilogue, or the split-K reduction): the weight estimate is not written and

@@ -10,6 +10,10 @@ Function names follow the C ABI:
   dust_noisy_linear_fwd  per-draw loss change of the noisy layer (noise equation)
   dust_credit            centred loss and discounted credit (centred-loss, credit equations)
   dust_weight_grad       output-error estimate g and weight estimate G_W
+and around the estimator, for the rest of a training step:
+  dust_linear, dust_linear_backward      the clean layer with its epilogue, and its exact gradients
+  dust_embedding, dust_embedding_grad    the token embedding and the gradient of its table
+  DustOptimizer (dust_optimizer_step_grouped)   one step over all tensors, moments in 32 or 8 bits
 """
 from __future__ import annotations
 
@@ -35,6 +39,14 @@ DUST_OP_CREDIT = 1
 DUST_OP_WEIGHT_GRAD = 2
 DUST_OP_LOGITS_CE = 3
 DUST_OP_SPSA_PROBE = 4
+DUST_OP_LINEAR_BACKWARD = 5
+DUST_OP_EMBEDDING_GRAD = 6
+
+DUST_ACTS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+
+DUST_STATE_F32 = 0
+DUST_STATE_E4M3 = 1
+DUST_STATE_BLOCK = 256
 
 EXPORTED_SYMBOLS = (
     "dust_noisy_linear_fwd", "dust_credit", "dust_weight_grad", "dust_workspace_size",
@@ -45,6 +57,8 @@ EXPORTED_SYMBOLS = (
     "dust_optimizer_step", "dust_weight_grad_step", "dust_noisy_logits_ce",
     "dust_debug_normal_sum", "dust_debug_fwd_plan", "dust_attn_reward", "dust_discounted_credit",
     "dust_spsa_probe", "dust_spsa_estimate", "dust_noisy_linear_output", "dust_debug_word_sum",
+    "dust_linear", "dust_linear_backward", "dust_embedding", "dust_embedding_grad",
+    "dust_optimizer_step_grouped",
 )
 
 DUST_OPT_SGD_MOMENTUM = 1
@@ -75,6 +89,13 @@ class dust_opt_params(ctypes.Structure):
     _fields_ = [("kind", ctypes.c_int32), ("step", ctypes.c_int32), ("lr", ctypes.c_float),
                 ("momentum", ctypes.c_float), ("beta1", ctypes.c_float), ("beta2", ctypes.c_float),
                 ("eps", ctypes.c_float), ("weight_decay", ctypes.c_float)]
+
+
+class dust_opt_tensor(ctypes.Structure):
+    _fields_ = [("G", ctypes.c_void_p), ("W", ctypes.c_void_p), ("W_bf16", ctypes.c_void_p),
+                ("m", ctypes.c_void_p), ("v", ctypes.c_void_p), ("m_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("n", ctypes.c_int64), ("lr_scale", ctypes.c_float),
+                ("decay_scale", ctypes.c_float)]
 
 
 def sgd_momentum(lr: float, momentum: float, weight_decay: float = 0.0) -> dust_opt_params:
@@ -164,6 +185,19 @@ def lib() -> ctypes.CDLL:
         L.dust_debug_normal_sum.restype = ctypes.c_int
         L.dust_debug_word_sum.argtypes = [dust_noise_key, i64, i32, vp, vp]
         L.dust_debug_word_sum.restype = ctypes.c_int
+        L.dust_linear.argtypes = [vp, i64, vp, vp, ctypes.c_int, vp, i64, ctypes.c_int, i64, i32, i32, vp,
+                                  ctypes.c_int, i64, vp, i64, vp]
+        L.dust_linear_backward.argtypes = [vp, ctypes.c_int, i64, vp, i64, vp, i64, vp, ctypes.c_int,
+                                           ctypes.c_int, i64, i32, i32, i32, vp, ctypes.c_int, i64, vp, vp,
+                                           ctypes.c_int, vp, sz, vp]
+        L.dust_embedding.argtypes = [vp, vp, ctypes.c_int, i64, i64, i32, i32, f32, vp, ctypes.c_int, i64, vp]
+        L.dust_embedding_grad.argtypes = [vp, vp, ctypes.c_int, i64, i64, i32, i32, f32, vp, i64,
+                                          ctypes.c_int, vp, sz, vp]
+        L.dust_optimizer_step_grouped.argtypes = [op, ctypes.POINTER(dust_opt_tensor), i32, ctypes.c_int,
+                                                  ctypes.c_int, vp, vp, vp]
+        for name in ("dust_linear", "dust_linear_backward", "dust_embedding", "dust_embedding_grad",
+                     "dust_optimizer_step_grouped"):
+            getattr(L, name).restype = ctypes.c_int
         L.dust_debug_credit_skip_publish.argtypes = [i32]
         L.dust_debug_credit_skip_publish.restype = None
         L.dust_debug_fwd_plan.argtypes = [i64, i32, i32, vp, i32, ctypes.POINTER(i32),
@@ -495,6 +529,302 @@ def dust_weight_grad_step(r, x, d_out: int, K_total: int, sigma: float, key: Noi
                                      _stream(x.device, stream))
     _check(st, "dust_weight_grad_step")
     return W
+
+
+# ------------------------------------------------------------------ around the estimator
+
+class _NoScope:
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *exc):
+        return False
+
+
+_NO_SCOPE = _NoScope()
+
+
+def _scope(device, stream):
+    """What a call runs under: its tensors' device, and its stream, so that outputs and workspaces
+    that the call allocates belong to the stream that uses them."""
+    torch = _torch()
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
+        return torch.cuda.stream(stream)
+    if device.index != torch.cuda.current_device():
+        return torch.cuda.device(device)
+    return _NO_SCOPE
+
+
+def _rows(t, name: str, rows: int, cols: int, device, dtypes) -> int:
+    """Checks a CUDA matrix [rows, cols] with contiguous rows and returns its row stride."""
+    if t.device != device or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor on {device}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be one of {dtypes}, not {t.dtype}")
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols or (cols > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be [{rows}, {cols}] with contiguous rows, got {tuple(t.shape)}, "
+                         f"strides {t.stride()}")
+    return t.stride(0) if rows > 1 else -(-cols // 8) * 8
+
+
+def _flat(t, name: str, n: int, device, dtype):
+    if t.device != device or not t.is_cuda or t.dtype != dtype or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of {n} elements on {device}")
+    return t
+
+
+def _new_rows(rows: int, cols: int, dtype, device, vec: int):
+    """A new [rows, cols] matrix whose rows begin at multiples of `vec` elements."""
+    torch = _torch()
+    if cols % vec == 0:
+        return torch.empty((rows, cols), dtype=dtype, device=device)
+    return torch.empty((rows, -(-cols // vec) * vec), dtype=dtype, device=device)[:, :cols]
+
+
+def _act_code(act: str) -> int:
+    code = DUST_ACTS.get(act)
+    if code is None:
+        raise ValueError(f"unknown activation {act!r}; one of {sorted(DUST_ACTS)}")
+    return code
+
+
+def dust_linear(x, W, bias=None, act: str = "none", residual=None, y=None, z=None, out_dtype=None, stream=None):
+    """y[N, d_out] = act(x W^T + bias) + residual for bf16 x [N, d_in] and W [d_out, d_in]; bias fp32
+    [d_out]; y (and residual) bf16 by default, or out_dtype=torch.float32.  z=True (or a bf16
+    tensor) also keeps the pre-activation for dust_linear_backward and returns (y, z).  Rows of
+    x, residual, y and z may be further apart than their length."""
+    torch = _torch()
+    bf, f32 = torch.bfloat16, torch.float32
+    dev = x.device
+    if x.dim() != 2 or W.dim() != 2:
+        raise ValueError("x must be [N, d_in] and W [d_out, d_in]")
+    N, d_in = x.shape
+    d_out = W.shape[0]
+    ld_x = _rows(x, "x", N, d_in, dev, (bf,))
+    _flat(W, "W", d_out * d_in, dev, bf)
+    if W.shape[1] != d_in:
+        raise ValueError("x must be [N, d_in] and W [d_out, d_in]")
+    if bias is not None:
+        _flat(bias, "bias", d_out, dev, f32)
+    code = _act_code(act)
+    with _scope(dev, stream):
+        if y is None:
+            y = torch.empty((N, d_out), dtype=out_dtype or bf, device=dev)
+        elif out_dtype is not None and y.dtype != out_dtype:
+            raise TypeError(f"y is {y.dtype}, out_dtype {out_dtype}")
+        ld_y = _rows(y, "y", N, d_out, dev, (bf, f32))
+        ld_res = _rows(residual, "residual", N, d_out, dev, (y.dtype,)) if residual is not None else 0
+        keep = z is not None and z is not False
+        if z is True:
+            z = torch.empty((N, d_out), dtype=bf, device=dev)
+        ld_z = _rows(z, "z", N, d_out, dev, (bf,)) if keep else 0
+        st = lib().dust_linear(x.data_ptr(), ld_x, W.data_ptr(), _ptr(bias), code, _ptr(residual), ld_res,
+                               DUST_BF16, N, d_in, d_out, y.data_ptr(),
+                               DUST_BF16 if y.dtype == bf else DUST_F32, ld_y,
+                               z.data_ptr() if keep else None, ld_z, torch.cuda.current_stream().cuda_stream)
+    _check(st, "dust_linear")
+    return (y, z) if keep else y
+
+
+def dust_linear_backward(dy, x, W, act: str = "none", z=None, dx=True, dW=True, db=True, accumulate: bool = False,
+                         dx_dtype=None, workspace=None, stream=None, g_terms: int = G_TERMS):
+    """(dx, dW, db) of dust_linear from dy [N, d_out] (bf16 or fp32) and the pre-activation z that it
+    kept (not needed for act="none"): dx [N, d_in] bf16 (or dx_dtype=torch.float32), dW fp32
+    [d_out, d_in], db fp32 [d_out].  Each output is True (allocated), a tensor, or None (skipped);
+    accumulate=True adds to the given dW and db."""
+    torch = _torch()
+    bf, f32 = torch.bfloat16, torch.float32
+    dev = dy.device
+    if dy.dim() != 2 or x.dim() != 2 or W.dim() != 2:
+        raise ValueError("dy must be [N, d_out], x [N, d_in], W [d_out, d_in]")
+    N, d_out = dy.shape
+    d_in = x.shape[1]
+    ld_dy = _rows(dy, "dy", N, d_out, dev, (bf, f32))
+    ld_x = _rows(x, "x", N, d_in, dev, (bf,))
+    _flat(W, "W", d_out * d_in, dev, bf)
+    if tuple(W.shape) != (d_out, d_in):
+        raise ValueError("dy must be [N, d_out], x [N, d_in], W [d_out, d_in]")
+    code = _act_code(act)
+    if code and z is None:
+        raise ValueError(f"act={act!r} needs the pre-activation z that dust_linear kept")
+    ld_z = _rows(z, "z", N, d_out, dev, (bf,)) if code else 0
+    if accumulate and (dW is True or db is True):
+        raise ValueError("accumulate adds to given dW and db tensors; pass them, or None to skip them")
+    with _scope(dev, stream):
+        if dx is True:
+            dx = torch.empty((N, d_in), dtype=dx_dtype or bf, device=dev)
+        if dW is True:
+            dW = torch.empty((d_out, d_in), dtype=f32, device=dev)
+        if db is True:
+            db = torch.empty(d_out, dtype=f32, device=dev)
+        dx, dW, db = (None if t is False else t for t in (dx, dW, db))
+        if dx is not None and dx_dtype is not None and dx.dtype != dx_dtype:
+            raise TypeError(f"dx is {dx.dtype}, dx_dtype {dx_dtype}")
+        ld_dx = _rows(dx, "dx", N, d_in, dev, (bf, f32)) if dx is not None else 0
+        if dW is not None:
+            _flat(dW, "dW", d_out * d_in, dev, f32)
+        if db is not None:
+            _flat(db, "db", d_out, dev, f32)
+        ws, nb = _workspace(workspace, dust_workspace_size(DUST_OP_LINEAR_BACKWARD, DUST_BF16, N, d_in, d_out, 0),
+                            dev)
+        st = lib().dust_linear_backward(dy.data_ptr(), _dtype_code(dy), ld_dy, z.data_ptr() if code else None, ld_z,
+                                        x.data_ptr(), ld_x, W.data_ptr(), code, DUST_BF16, N, d_in, d_out,
+                                        int(g_terms), _ptr(dx),
+                                        DUST_F32 if dx is not None and dx.dtype == f32 else DUST_BF16, ld_dx,
+                                        _ptr(dW), _ptr(db), 1 if accumulate else 0, _ptr(ws), nb,
+                                        torch.cuda.current_stream().cuda_stream)
+    _check(st, "dust_linear_backward")
+    return dx, dW, db
+
+
+def _check_ids(ids):
+    torch = _torch()
+    if ids.dtype != torch.int32:
+        raise TypeError("ids must be int32")
+    if not ids.is_cuda or ids.dim() != 1 or not ids.is_contiguous():
+        raise ValueError("ids must be a contiguous CUDA vector")
+    return ids.numel()
+
+
+def dust_embedding(ids, E, scale: float = 1.0, out=None, out_dtype=None, stream=None):
+    """out[N, d] = scale E[ids] for int32 ids [N] and a bf16 or fp32 table E [V, d] (out of E's type, or
+    out_dtype).  A negative id gives a zero row, an id >= V a NaN row."""
+    torch = _torch()
+    both = (torch.bfloat16, torch.float32)
+    N = _check_ids(ids)
+    dev = ids.device
+    if E.dim() != 2:
+        raise ValueError("E must be [V, d]")
+    V, d = E.shape
+    ld_E = _rows(E, "E", V, d, dev, both)
+    with _scope(dev, stream):
+        if out is None:
+            out = _new_rows(N, d, out_dtype or E.dtype, dev, 8)
+        elif out_dtype is not None and out.dtype != out_dtype:
+            raise TypeError(f"out is {out.dtype}, out_dtype {out_dtype}")
+        ld_out = _rows(out, "out", N, d, dev, both)
+        st = lib().dust_embedding(ids.data_ptr(), E.data_ptr(), _dtype_code(E), ld_E, N, V, d, float(scale),
+                                  out.data_ptr(), _dtype_code(out), ld_out, torch.cuda.current_stream().cuda_stream)
+    _check(st, "dust_embedding")
+    return out
+
+
+def dust_embedding_grad(ids, g, V: int, scale: float = 1.0, G=None, accumulate: bool = False, workspace=None,
+                        stream=None):
+    """The table's gradient G[v] (+)= scale sum of g[t] over the tokens with ids[t] = v, fp32 [V, d], from g
+    [N, d] (bf16 or fp32).  accumulate=True adds to the rows of the given G that have tokens."""
+    torch = _torch()
+    N = _check_ids(ids)
+    dev = ids.device
+    if g.dim() != 2:
+        raise ValueError("g must be [N, d]")
+    d = g.shape[1]
+    ld_g = _rows(g, "g", N, d, dev, (torch.bfloat16, torch.float32))
+    if accumulate and G is None:
+        raise ValueError("accumulate adds to a given G")
+    with _scope(dev, stream):
+        if G is None:
+            G = _new_rows(V, d, torch.float32, dev, 4)
+        ld_G = _rows(G, "G", V, d, dev, (torch.float32,))
+        dt = _dtype_code(g)
+        ws, nb = _workspace(workspace, dust_workspace_size(DUST_OP_EMBEDDING_GRAD, dt, N, V, d, 0), dev)
+        st = lib().dust_embedding_grad(ids.data_ptr(), g.data_ptr(), dt, ld_g, N, V, d, float(scale), G.data_ptr(),
+                                       ld_G, 1 if accumulate else 0, _ptr(ws), nb,
+                                       torch.cuda.current_stream().cuda_stream)
+    _check(st, "dust_embedding_grad")
+    return G
+
+
+class DustOptimizer:
+    """One optimizer step over many tensors in one launch (dust_optimizer_step_grouped), with the moments
+    in fp32 (bits=32) or e4m3 codes with a scale for each block of 256 elements (bits=8, Adam only).
+
+    W: list of fp32 master weights (any shapes, contiguous); G: list of their gradients (all fp32 or
+    all bf16); W_bf16: optional list of bf16 copies to refresh (entries may be None).  lr_scale and
+    decay multiply the learning rate and the weight decay tensor by tensor (decay=False: none).
+    The moments are the lists ``m`` and ``v`` (bits=8: torch.float8_e4m3fn codes of m and of sqrt(v), with
+    ``m_scale`` and ``v_scale``), created as zeros or taken over from m=, v=, m_scale=, v_scale=."""
+
+    def __init__(self, W, G, W_bf16=None, bits: int = 32, lr_scale=None, decay=None, m=None, v=None, m_scale=None,
+                 v_scale=None):
+        torch = _torch()
+        if bits not in (32, 8):
+            raise ValueError("bits must be 32 or 8")
+        self.W, self.bits = list(W), bits
+        k = len(self.W)
+        if k == 0:
+            raise ValueError("no tensors")
+        self.device = self.W[0].device
+        dev, f32 = self.device, torch.float32
+        sizes = [t.numel() for t in self.W]
+        state = f32 if bits == 32 else torch.float8_e4m3fn
+
+        def take(given, what, dtype, counts, may_skip=False, zeros=False):
+            if given is None:
+                return [torch.zeros(n, dtype=dtype, device=dev) if zeros else None for n in counts]
+            given = list(given)
+            if len(given) != k:
+                raise ValueError(f"{what} must have one entry for each of the {k} tensors")
+            for i, (t, n) in enumerate(zip(given, counts)):
+                if t is not None or not may_skip:
+                    _flat(t, f"{what}[{i}]", n, dev, dtype)
+            return given
+
+        take(self.W, "W", f32, sizes)
+        self.W_bf16 = take(W_bf16, "W_bf16", torch.bfloat16, sizes, may_skip=True)
+        self.m = take(m, "m", state, sizes, zeros=True)
+        self.v = take(v, "v", state, sizes, zeros=True)
+        blocks = [-(-n // DUST_STATE_BLOCK) for n in sizes]
+        self.m_scale = take(m_scale, "m_scale", f32, blocks, zeros=True) if bits == 8 else None
+        self.v_scale = take(v_scale, "v_scale", f32, blocks, zeros=True) if bits == 8 else None
+        held = [t for ts in (self.W, self.W_bf16, self.m, self.v, self.m_scale, self.v_scale) if ts is not None
+                for t in ts if t is not None and t.numel()]
+        spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in held)
+        if any(b[0] < a[1] for a, b in zip(spans, spans[1:])):
+            raise ValueError("weights and moments must not share memory")
+        self._desc = (dust_opt_tensor * k)()
+        for i, d in enumerate(self._desc):
+            d.W, d.W_bf16, d.m, d.v = (_ptr(t) for t in (self.W[i], self.W_bf16[i], self.m[i], self.v[i]))
+            if bits == 8:
+                d.m_scale, d.v_scale = self.m_scale[i].data_ptr(), self.v_scale[i].data_ptr()
+            d.n = sizes[i]
+            d.lr_scale = 1.0 if lr_scale is None else float(lr_scale[i])
+            d.decay_scale = 1.0 if decay is None else float(decay[i])
+        self.set_gradients(G)
+
+    def set_gradients(self, G) -> None:
+        """Takes other gradient tensors for the steps that follow."""
+        torch = _torch()
+        G = list(G)
+        if len(G) != len(self.W):
+            raise ValueError(f"G must have one entry for each of the {len(self.W)} tensors")
+        dtype = G[0].dtype
+        if dtype not in (torch.float32, torch.bfloat16):
+            raise TypeError(f"gradients are fp32 or bf16, not {dtype}")
+        for i, (g, w) in enumerate(zip(G, self.W)):
+            _flat(g, f"G[{i}]", w.numel(), self.device, dtype)
+        self.G, self._g_dt = G, DUST_F32 if dtype == torch.float32 else DUST_BF16
+        for d, g in zip(self._desc, G):
+            d.G = g.data_ptr()
+
+    def step(self, opt: dust_opt_params, g_scale=None, step=None, stream=None):
+        """One step with the hyper-parameters of sgd_momentum(...) or adam(...).  g_scale: optional fp32
+        CUDA scalar that multiplies every gradient.  step: optional int32 CUDA scalar with Adam's
+        step count, read when the step runs (for captured graphs); None takes opt.step."""
+        torch = _torch()
+        if g_scale is not None:
+            _flat(g_scale, "g_scale", 1, self.device, torch.float32)
+        if step is not None:
+            _flat(step, "step", 1, self.device, torch.int32)
+        with _scope(self.device, stream):
+            st = lib().dust_optimizer_step_grouped(ctypes.byref(opt), self._desc, len(self.W), self._g_dt,
+                                                   DUST_STATE_F32 if self.bits == 32 else DUST_STATE_E4M3,
+                                                   _ptr(g_scale), _ptr(step),
+                                                   torch.cuda.current_stream().cuda_stream)
+        _check(st, "dust_optimizer_step_grouped")
+        return self.W
 
 
 def dust_last_device_error(stream=None, device=None) -> Tuple[int, int]:

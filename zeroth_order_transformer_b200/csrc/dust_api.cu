@@ -140,10 +140,15 @@ int num_sms() {
 
 bool make_tmap_bf16_2d(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols,
                        uint32_t box_rows, uint32_t box_cols) {
+    return make_tmap_bf16_2d_ld(map, base, rows, cols, cols, box_rows, box_cols);
+}
+
+bool make_tmap_bf16_2d_ld(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint64_t ld,
+                          uint32_t box_rows, uint32_t box_cols) {
     auto fn = get_encode_fn();
     if (!fn) return false;
     cuuint64_t dims[2] = {cols, rows};
-    cuuint64_t strides[1] = {cols * 2};
+    cuuint64_t strides[1] = {ld * 2};
     cuuint32_t box[2] = {box_cols, box_rows};
     cuuint32_t estr[2] = {1, 1};
     return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides,
@@ -252,6 +257,13 @@ dust_status check_layer(const void* x, dust_dtype dt, int64_t N, int32_t d_in, i
     return DUST_OK;
 }
 
+bool valid_act(dust_act a) { return a >= DUST_ACT_NONE && a <= DUST_ACT_SILU; }
+
+// A row stride: at least the row, and whole 16-byte vectors.
+bool valid_ld(int64_t ld, int64_t cols, int64_t vec) {
+    return ld >= cols && ld % vec == 0 && ld < (1LL << 38);
+}
+
 dust_status check_ws(void* ws, size_t have, size_t need) {
     if (need == 0) return DUST_OK;
     if (!ws || !aligned256(ws) || have < need) return DUST_ERR_WORKSPACE;
@@ -283,6 +295,10 @@ size_t dust_workspace_size(dust_op op, dust_dtype dt, int64_t N, int32_t d_in, i
         case DUST_OP_WEIGHT_GRAD: return wgrad_workspace_bytes(dt, N, d_in, d_out);
         case DUST_OP_LOGITS_CE: return lmhead_workspace_bytes(N, d_out, K);
         case DUST_OP_SPSA_PROBE: return spsa_workspace_bytes(N, d_in, d_out, K);
+        case DUST_OP_LINEAR_BACKWARD:
+            return d_in < 1 || d_out < 1 ? 0 : linear_backward_workspace_bytes(N, d_in, d_out);
+        case DUST_OP_EMBEDDING_GRAD:
+            return d_in < 1 || d_out < 1 ? 0 : embedding_grad_workspace_bytes(dt, N, d_in, d_out);
     }
     return 0;
 }
@@ -359,6 +375,74 @@ dust_status dust_noisy_linear_output(const void* x, const void* W, dust_dtype dt
     return noisy_output_launch(x, W, N, d_in, d_out, K, sigma, make_key(key), y_out,
                                out_dt == DUST_BF16 ? 1 : 0, ld_out,
                                static_cast<cudaStream_t>(stream));
+}
+
+dust_status dust_linear(const void* x, int64_t ld_x, const void* W, const float* bias, dust_act act,
+                        const void* residual, int64_t ld_res, dust_dtype dt, int64_t N, int32_t d_in,
+                        int32_t d_out, void* y, dust_dtype out_dt, int64_t ld_y, void* z, int64_t ld_z,
+                        void* stream) {
+    if (!valid_dtype(dt) || !valid_dtype(out_dt) || !valid_act(act) || !x || !W || !y || N < 1 || d_in < 1 ||
+        d_out < 1)
+        return DUST_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(W) || !aligned16(bias) || !aligned16(residual) || !aligned16(y) ||
+        !aligned16(z))
+        return DUST_ERR_INVALID_ARG;
+    const int64_t out_vec = out_dt == DUST_BF16 ? 8 : 4;
+    if (!valid_ld(ld_x, d_in, 8) || !valid_ld(ld_y, d_out, out_vec) ||
+        (residual && !valid_ld(ld_res, d_out, out_vec)) || (z && !valid_ld(ld_z, d_out, 8)))
+        return DUST_ERR_INVALID_ARG;
+    if (dt != DUST_BF16 || d_in % 16 != 0 || d_out % 16 != 0 || N > 1073741823LL) return DUST_ERR_UNSUPPORTED;
+    return linear_launch(x, ld_x, W, bias, act, residual, ld_res, N, d_in, d_out, y, out_dt == DUST_BF16 ? 1 : 0,
+                         ld_y, z, ld_z, static_cast<cudaStream_t>(stream));
+}
+
+dust_status dust_linear_backward(const void* dy, dust_dtype dy_dt, int64_t ld_dy, const void* z, int64_t ld_z,
+                                 const void* x, int64_t ld_x, const void* W, dust_act act, dust_dtype dt,
+                                 int64_t N, int32_t d_in, int32_t d_out, int32_t g_terms, void* dx,
+                                 dust_dtype dx_dt, int64_t ld_dx, float* dW, float* db, int accumulate,
+                                 void* workspace, size_t ws_bytes, void* stream) {
+    if (!valid_dtype(dt) || !valid_dtype(dy_dt) || !valid_dtype(dx_dt) || !valid_act(act) || !dy || N < 1 ||
+        d_in < 1 || d_out < 1 || (g_terms != 1 && g_terms != 2))
+        return DUST_ERR_INVALID_ARG;
+    if ((!dx && !dW && !db) || (dx && !W) || (dW && !x) || (act != DUST_ACT_NONE && !z)) return DUST_ERR_INVALID_ARG;
+    if (!aligned16(dy) || !aligned16(z) || !aligned16(x) || !aligned16(W) || !aligned16(dx) || !aligned16(dW) ||
+        !aligned16(db))
+        return DUST_ERR_INVALID_ARG;
+    if (!valid_ld(ld_dy, d_out, dy_dt == DUST_BF16 ? 8 : 4) || (act != DUST_ACT_NONE && !valid_ld(ld_z, d_out, 8)) ||
+        (dW && !valid_ld(ld_x, d_in, 8)) || (dx && !valid_ld(ld_dx, d_in, dx_dt == DUST_BF16 ? 8 : 4)))
+        return DUST_ERR_INVALID_ARG;
+    if (dt != DUST_BF16 || d_in % 16 != 0 || d_out % 16 != 0 || N > 8388607LL) return DUST_ERR_UNSUPPORTED;
+    const dust_status st = check_ws(workspace, ws_bytes, linear_backward_workspace_bytes(N, d_in, d_out));
+    if (st != DUST_OK) return st;
+    return linear_backward_launch(dy, dy_dt == DUST_BF16 ? 1 : 0, ld_dy, z, ld_z, x, ld_x, W, act, N, d_in, d_out,
+                                  g_terms, dx, dx_dt == DUST_BF16 ? 1 : 0, ld_dx, dW, db, accumulate, workspace,
+                                  static_cast<cudaStream_t>(stream));
+}
+
+dust_status dust_embedding(const int32_t* ids, const void* E, dust_dtype dt, int64_t ld_E, int64_t N, int32_t V,
+                           int32_t d, float scale, void* out, dust_dtype out_dt, int64_t ld_out, void* stream) {
+    if (!valid_dtype(dt) || !valid_dtype(out_dt) || !ids || !E || !out || N < 1 || V < 1 || d < 1)
+        return DUST_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(ids) & 3u) || !aligned16(E) || !aligned16(out) ||
+        !valid_ld(ld_E, d, dt == DUST_BF16 ? 8 : 4) || !valid_ld(ld_out, d, out_dt == DUST_BF16 ? 8 : 4))
+        return DUST_ERR_INVALID_ARG;
+    if (N > 2147483647LL) return DUST_ERR_UNSUPPORTED;
+    return embedding_launch(ids, E, dt, ld_E, N, V, d, scale, out, out_dt, ld_out,
+                            static_cast<cudaStream_t>(stream));
+}
+
+dust_status dust_embedding_grad(const int32_t* ids, const void* g, dust_dtype dt, int64_t ld_g, int64_t N,
+                                int32_t V, int32_t d, float scale, float* G, int64_t ld_G, int accumulate,
+                                void* workspace, size_t ws_bytes, void* stream) {
+    if (!valid_dtype(dt) || !ids || !g || !G || N < 1 || V < 1 || d < 1) return DUST_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(ids) & 3u) || !aligned16(g) || !aligned16(G) ||
+        !valid_ld(ld_g, d, dt == DUST_BF16 ? 8 : 4) || !valid_ld(ld_G, d, 4))
+        return DUST_ERR_INVALID_ARG;
+    if (N > 2147483647LL || V > 2147483646) return DUST_ERR_UNSUPPORTED;
+    const dust_status st = check_ws(workspace, ws_bytes, embedding_grad_workspace_bytes(dt, N, V, d));
+    if (st != DUST_OK) return st;
+    return embedding_grad_launch(ids, g, dt, ld_g, N, V, d, scale, G, ld_G, accumulate, workspace,
+                                 static_cast<cudaStream_t>(stream));
 }
 
 dust_status dust_spsa_probe(const void* x, const void* W, const void* u, dust_dtype dt, int64_t N,
@@ -458,6 +542,35 @@ dust_status dust_optimizer_step(const dust_opt_params* opt, const float* G, floa
         (W_bf16 && (reinterpret_cast<uintptr_t>(W_bf16) & 7u) != 0))
         return DUST_ERR_INVALID_ARG;
     return opt_launch(o, G, OptTargets{W, W_bf16, m, v}, n, static_cast<cudaStream_t>(stream));
+}
+
+dust_status dust_optimizer_step_grouped(const dust_opt_params* opt, const dust_opt_tensor* tensors,
+                                        int32_t n_tensors, dust_dtype g_dt, dust_state_dtype state,
+                                        const float* g_scale, const int32_t* step, void* stream) {
+    OptParams o;
+    if (!make_opt(opt, &o) || !std::isfinite(opt->weight_decay) || !valid_dtype(g_dt) ||
+        (state != DUST_STATE_F32 && state != DUST_STATE_E4M3) || n_tensors < 0 ||
+        (n_tensors > 0 && !tensors))
+        return DUST_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(g_scale) & 3u) || (reinterpret_cast<uintptr_t>(step) & 3u))
+        return DUST_ERR_INVALID_ARG;
+    const bool adam = o.kind == DUST_OPT_ADAM, eight = state == DUST_STATE_E4M3;
+    for (int32_t i = 0; i < n_tensors; ++i) {
+        const dust_opt_tensor& t = tensors[i];
+        if (t.n < 0 || !(t.lr_scale >= 0.f) || !std::isfinite(t.lr_scale) || !(t.decay_scale >= 0.f) ||
+            !std::isfinite(t.decay_scale))
+            return DUST_ERR_INVALID_ARG;
+        if (t.n == 0) continue;
+        if (!t.G || !t.W || !t.m || (adam && !t.v) || (eight && (!t.m_scale || !t.v_scale)))
+            return DUST_ERR_INVALID_ARG;
+        if (!aligned16(t.G) || !aligned16(t.W) || !aligned16(t.W_bf16) || !aligned16(t.m) ||
+            !aligned16(t.v) || (reinterpret_cast<uintptr_t>(t.m_scale) & 3u) ||
+            (reinterpret_cast<uintptr_t>(t.v_scale) & 3u))
+            return DUST_ERR_INVALID_ARG;
+    }
+    if (eight && !adam) return DUST_ERR_UNSUPPORTED;
+    return opt_grouped_launch(o, opt, tensors, n_tensors, g_dt == DUST_BF16, eight, g_scale, step,
+                              static_cast<cudaStream_t>(stream));
 }
 
 dust_status dust_weight_grad_step(const float* r, int64_t ld_r, const void* x, dust_dtype dt,

@@ -1,0 +1,694 @@
+// Token embedding: the lookup with its scaling, and the gradient of the table.
+//
+//   out_t = scale E[ids_t]                 (a zero row for ids_t < 0, a NaN row for ids_t >= V)
+//   G[v] (+)= scale sum_{t: ids_t = v} g_t (tokens with ids outside [0, V) add nothing)
+//
+// The lookup is one pass: a thread moves eight elements of a row, four such items at a time, so
+// that every thread has four loads in flight.
+//
+// The gradient is a sum over the tokens of each row, and the tokens of a row are scattered over
+// the batch.  They are brought together by a stable radix sort of the token indices by id
+// (least significant digit first, up to nine bits a pass: a vocabulary of 2^18 takes two), which
+// moves 8 bytes a token where a row is hundreds to thousands.  The sorted positions are cut into
+// chunks of equal length; one warp sums a chunk's rows over 128 (fp32) or 256 (bf16) columns,
+// sixteen bytes a lane, eight rows in flight, and writes a table row whenever the id changes.  An id
+// that crosses a chunk border leaves partial sums, which a last kernel adds in chunk order: no
+// atomics on floats, and the same result on every run.  Rows that no token names are cleared in the
+// same launch by CTAs that look for their ids in the sorted list, so every row is written once.
+//
+// Both are HBM-bound: the rows read and written once.
+#include <algorithm>
+
+#include "dust_device.cuh"
+#include "dust_internal.h"
+
+namespace dust {
+namespace {
+
+// ------------------------------------------------------------------ rows of eight elements
+struct V8 {
+    float v[8];
+};
+
+__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// Elements [0, n) of the eight at p (16-byte aligned); the others are 0.
+__device__ __forceinline__ V8 load8(const float* p, int n) {
+    V8 r;
+    if (n >= 8) {
+        const float4 a = __ldg(reinterpret_cast<const float4*>(p));
+        const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+        r = V8{{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) r.v[j] = j < n ? __ldg(p + j) : 0.f;
+    }
+    return r;
+}
+__device__ __forceinline__ V8 load8(const __nv_bfloat16* p, int n) {
+    V8 r;
+    if (n >= 8) {
+        const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
+        r = V8{{bf_lo(a.x), bf_hi(a.x), bf_lo(a.y), bf_hi(a.y), bf_lo(a.z), bf_hi(a.z), bf_lo(a.w),
+                bf_hi(a.w)}};
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) r.v[j] = j < n ? __bfloat162float(p[j]) : 0.f;
+    }
+    return r;
+}
+__device__ __forceinline__ void store8(float* p, const V8& r, int n) {
+    if (n >= 8) {
+        reinterpret_cast<float4*>(p)[0] = make_float4(r.v[0], r.v[1], r.v[2], r.v[3]);
+        reinterpret_cast<float4*>(p)[1] = make_float4(r.v[4], r.v[5], r.v[6], r.v[7]);
+    } else {
+        for (int j = 0; j < n; ++j) p[j] = r.v[j];
+    }
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const V8& r, int n) {
+    if (n >= 8) {
+        uint4 w;
+        uint32_t* wp = &w.x;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(r.v[2 * j], r.v[2 * j + 1]);
+            wp[j] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+        *reinterpret_cast<uint4*>(p) = w;
+    } else {
+        for (int j = 0; j < n; ++j) p[j] = __float2bfloat16_rn(r.v[j]);
+    }
+}
+
+// ------------------------------------------------------------------ the lookup
+constexpr int kFThreads = 256;
+constexpr int kFItems = 4;  // items of eight elements a thread holds at once
+
+template <typename TE, typename TO>
+__global__ void __launch_bounds__(kFThreads) embedding_kernel(const int32_t* __restrict__ ids,
+                                                              const TE* __restrict__ E, int64_t ld_E,
+                                                              int64_t N, int32_t V, int32_t d, int32_t nv,
+                                                              uint64_t nv_magic, float scale, TO* out,
+                                                              int64_t ld_out) {
+    const int64_t total = N * nv;
+    const int64_t base = static_cast<int64_t>(blockIdx.x) * (kFThreads * kFItems) + threadIdx.x;
+    V8 r[kFItems];
+    int64_t at[kFItems];
+    int left[kFItems];
+#pragma unroll
+    for (int j = 0; j < kFItems; ++j) {
+        const int64_t f = base + j * kFThreads;
+        left[j] = 0;
+        if (f < total) {
+            const int64_t t = div_by_magic(f, nv, nv_magic);
+            const int c = 8 * static_cast<int>(f - t * nv);
+            const int32_t id = __ldg(ids + t);
+            left[j] = d - c;
+            at[j] = t * ld_out + c;
+            if (id >= 0 && id < V) {
+                r[j] = load8(E + static_cast<int64_t>(id) * ld_E + c, left[j]);
+            } else {
+                const float fill = id < 0 ? 0.f : __uint_as_float(0x7FC00000u);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) r[j].v[k] = fill;
+            }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < kFItems; ++j)
+        if (left[j] > 0) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) r[j].v[k] *= scale;
+            store8(out + at[j], r[j], left[j]);
+        }
+}
+
+// ------------------------------------------------------------------ stable radix sort by id
+constexpr int kBinBits = 9;
+constexpr int kBins = 1 << kBinBits;
+constexpr int kSThreads = 512;  // one thread per bin in the prefix sums
+constexpr int kSWarps = kSThreads / 32;
+constexpr int kSRounds = 8;     // keys per lane
+constexpr int kTile = kSThreads * kSRounds;
+static_assert(kSThreads == kBins, "one thread per bin");
+
+__device__ __forceinline__ uint32_t key_of(int32_t id, int32_t V) {
+    return id >= 0 && id < V ? static_cast<uint32_t>(id) : static_cast<uint32_t>(V);  // no row: last
+}
+
+// Digit counts of each tile: hist[tile][bin].
+__global__ void __launch_bounds__(kSThreads) embed_hist_kernel(const int32_t* __restrict__ ids,
+                                                               const uint32_t* __restrict__ keys, int64_t N,
+                                                               int32_t V, int shift, uint32_t mask,
+                                                               int32_t* hist) {
+    __shared__ int32_t cnt[kBins];
+    cnt[threadIdx.x] = 0;
+    __syncthreads();
+    const int64_t p0 = static_cast<int64_t>(blockIdx.x) * kTile;
+#pragma unroll
+    for (int r = 0; r < kSRounds; ++r) {
+        const int64_t p = p0 + r * kSThreads + threadIdx.x;
+        if (p < N) {
+            const uint32_t k = ids ? key_of(ids[p], V) : keys[p];
+            atomicAdd(&cnt[(k >> shift) & mask], 1);
+        }
+    }
+    __syncthreads();
+    hist[static_cast<int64_t>(blockIdx.x) * kBins + threadIdx.x] = cnt[threadIdx.x];
+}
+
+// Where each of this thread's keys goes within a stable order of the tile by digit, on top of
+// base[bin].  Keys are taken warp by warp, round by round, lane by lane: their order in the tile.
+// `n` keys are valid.  All threads of the CTA call it; wh [kSWarps][kBins] is scratch.
+__device__ __forceinline__ void tile_ranks(const uint32_t (&digit)[kSRounds], int n, int32_t base,
+                                           int32_t (*wh)[kBins], int32_t (&pos)[kSRounds]) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int w = 0; w < kSWarps; ++w) wh[w][threadIdx.x] = 0;
+    __syncthreads();
+    const uint32_t below = (1u << lane) - 1u;
+#pragma unroll
+    for (int r = 0; r < kSRounds; ++r) {
+        const int at = (warp * kSRounds + r) * 32 + lane;
+        const uint32_t dg = at < n ? digit[r] : 0xFFFFFFFFu;
+        const uint32_t same = __match_any_sync(0xFFFFFFFFu, dg);
+        int before = 0;
+        if (at < n) before = wh[warp][dg];
+        __syncwarp();
+        pos[r] = before + __popc(same & below);
+        if (at < n && (same & below) == 0) wh[warp][dg] = before + __popc(same);
+        __syncwarp();
+    }
+    __syncthreads();
+    int32_t run = base;  // of bin threadIdx.x
+    for (int w = 0; w < kSWarps; ++w) {
+        const int32_t c = wh[w][threadIdx.x];
+        wh[w][threadIdx.x] = run;
+        run += c;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < kSRounds; ++r) {
+        const int at = (warp * kSRounds + r) * 32 + lane;
+        if (at < n) pos[r] += wh[warp][digit[r]];
+    }
+    __syncthreads();
+}
+
+// Exclusive prefix sum over the kBins threads of the CTA.
+__device__ __forceinline__ int32_t scan_bins(int32_t x, int32_t* sh) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int32_t s = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int32_t y = __shfl_up_sync(0xFFFFFFFFu, s, o);
+        if (lane >= o) s += y;
+    }
+    if (lane == 31) sh[warp] = s;
+    __syncthreads();
+    if (warp == 0) {
+        int32_t w = lane < kSWarps ? sh[lane] : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int32_t y = __shfl_up_sync(0xFFFFFFFFu, w, o);
+            if (lane >= o) w += y;
+        }
+        if (lane < kSWarps) sh[lane] = w;
+    }
+    __syncthreads();
+    const int32_t r = s - x + (warp > 0 ? sh[warp - 1] : 0);
+    __syncthreads();
+    return r;
+}
+
+// One pass over a tile: reads its keys (ids in the first pass), writes keys and token indices in
+// the order of the pass's digit.  Each CTA sums the other tiles' counts itself.
+__global__ void __launch_bounds__(kSThreads) embed_scatter_kernel(
+    const int32_t* __restrict__ ids, const uint32_t* __restrict__ keys, const int32_t* __restrict__ idx,
+    int64_t N, int32_t V, int shift, uint32_t mask, const int32_t* __restrict__ hist, int tiles,
+    uint32_t* keys_out, int32_t* idx_out) {
+    __shared__ int32_t wh[kSWarps][kBins];
+    __shared__ int32_t sh[32];
+    int32_t all = 0, earlier = 0;
+    const int tile = blockIdx.x;
+#pragma unroll 8
+    for (int t = 0; t < tiles; ++t) {
+        const int32_t c = __ldg(hist + static_cast<int64_t>(t) * kBins + threadIdx.x);
+        all += c;
+        if (t < tile) earlier += c;
+    }
+    const int32_t base = scan_bins(all, sh) + earlier;
+    const int64_t p0 = static_cast<int64_t>(tile) * kTile;
+    const int n = static_cast<int>(min(static_cast<int64_t>(kTile), N - p0));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint32_t key[kSRounds], digit[kSRounds];
+    int32_t val[kSRounds], pos[kSRounds];
+#pragma unroll
+    for (int r = 0; r < kSRounds; ++r) {
+        const int at = (warp * kSRounds + r) * 32 + lane;
+        key[r] = 0;
+        val[r] = 0;
+        if (at < n) {
+            key[r] = ids ? key_of(ids[p0 + at], V) : keys[p0 + at];
+            val[r] = ids ? static_cast<int32_t>(p0 + at) : idx[p0 + at];
+        }
+        digit[r] = (key[r] >> shift) & mask;
+    }
+    tile_ranks(digit, n, base, wh, pos);
+#pragma unroll
+    for (int r = 0; r < kSRounds; ++r) {
+        const int at = (warp * kSRounds + r) * 32 + lane;
+        if (at < n) {
+            keys_out[pos[r]] = key[r];
+            idx_out[pos[r]] = val[r];
+        }
+    }
+}
+
+// A batch of at most one tile: all passes in one CTA, through shared memory.
+__global__ void __launch_bounds__(kSThreads) embed_sort_tile_kernel(const int32_t* __restrict__ ids, int N,
+                                                                    int32_t V, int passes, int bits,
+                                                                    uint32_t* keys_out, int32_t* idx_out) {
+    extern __shared__ int32_t dyn[];
+    int32_t(*wh)[kBins] = reinterpret_cast<int32_t(*)[kBins]>(dyn);
+    uint32_t* skey = reinterpret_cast<uint32_t*>(dyn + kSWarps * kBins);  // [kTile]
+    int32_t* sval = reinterpret_cast<int32_t*>(skey + kTile);             // [kTile]
+    int32_t* cnt = sval + kTile;                                          // [kBins]
+    int32_t* sh = cnt + kBins;                                            // [32]
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint32_t key[kSRounds], digit[kSRounds];
+    int32_t val[kSRounds], pos[kSRounds];
+#pragma unroll
+    for (int r = 0; r < kSRounds; ++r) {
+        const int at = (warp * kSRounds + r) * 32 + lane;
+        key[r] = at < N ? key_of(ids[at], V) : 0u;
+        val[r] = at;
+    }
+    const uint32_t mask = (1u << bits) - 1u;
+    for (int pass = 0; pass < passes; ++pass) {
+        cnt[threadIdx.x] = 0;
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < kSRounds; ++r) {
+            const int at = (warp * kSRounds + r) * 32 + lane;
+            digit[r] = (key[r] >> (pass * bits)) & mask;
+            if (at < N) atomicAdd(&cnt[digit[r]], 1);
+        }
+        __syncthreads();
+        const int32_t base = scan_bins(cnt[threadIdx.x], sh);
+        tile_ranks(digit, N, base, wh, pos);
+        if (pass + 1 == passes) break;
+#pragma unroll
+        for (int r = 0; r < kSRounds; ++r) {
+            const int at = (warp * kSRounds + r) * 32 + lane;
+            if (at < N) {
+                skey[pos[r]] = key[r];
+                sval[pos[r]] = val[r];
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < kSRounds; ++r) {
+            const int at = (warp * kSRounds + r) * 32 + lane;
+            if (at < N) {
+                key[r] = skey[at];
+                val[r] = sval[at];
+            }
+        }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int r = 0; r < kSRounds; ++r) {
+        const int at = (warp * kSRounds + r) * 32 + lane;
+        if (at < N) {
+            keys_out[pos[r]] = key[r];
+            idx_out[pos[r]] = val[r];
+        }
+    }
+}
+constexpr int kSortTileSmem = (kSWarps * kBins + 2 * kTile + kBins + 32) * 4;
+
+// ------------------------------------------------------------------ the sums
+constexpr int kGThreads = 256;
+constexpr int kGWarps = kGThreads / 32;
+constexpr int kZeroRows = 64;  // table rows that one clearing CTA looks after
+
+struct GradArgs {
+    const uint32_t* key;  // sorted
+    const int32_t* idx;
+    const void* g;
+    float* G;
+    float* head;  // [chunks, dpad]: sums of ids that began in an earlier chunk
+    float* tail;  // [chunks, dpad]: sums of ids that begin in the chunk and go on past its end
+    int64_t ld_g, ld_G, N, units;
+    int32_t V, d, dpad, slabs, chunk, chunks, zero_blocks, accumulate;
+    float scale;
+};
+
+template <typename T>
+struct Lane;  // what one lane sums: 16 bytes of a row
+template <>
+struct Lane<float> {
+    static constexpr int kN = 4;
+    using Raw = float4;
+    static __device__ __forceinline__ void add(float (&a)[4], const Raw& r) {
+        a[0] += r.x;
+        a[1] += r.y;
+        a[2] += r.z;
+        a[3] += r.w;
+    }
+    static __device__ __forceinline__ Raw tail(const float* p, int n) {
+        return make_float4(n > 0 ? p[0] : 0.f, n > 1 ? p[1] : 0.f, n > 2 ? p[2] : 0.f, 0.f);
+    }
+};
+template <>
+struct Lane<__nv_bfloat16> {
+    static constexpr int kN = 8;
+    using Raw = uint4;
+    static __device__ __forceinline__ void add(float (&a)[8], const Raw& r) {
+        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            a[2 * j] += bf_lo(w[j]);
+            a[2 * j + 1] += bf_hi(w[j]);
+        }
+    }
+    static __device__ __forceinline__ Raw tail(const __nv_bfloat16* p, int n) {
+        uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int j = 0; j < 7; ++j)
+            if (j < n) w[j >> 1] |= static_cast<uint32_t>(__bfloat16_as_ushort(p[j])) << (16 * (j & 1));
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+};
+
+template <int kN>
+__device__ __forceinline__ void put_row(float* row, const float (&a)[kN], int n, float scale, bool accumulate) {
+    if (n >= kN) {
+        float4* r4 = reinterpret_cast<float4*>(row);
+#pragma unroll
+        for (int j = 0; j < kN / 4; ++j) {
+            float4 w = make_float4(a[4 * j] * scale, a[4 * j + 1] * scale, a[4 * j + 2] * scale,
+                                   a[4 * j + 3] * scale);
+            if (accumulate) {
+                const float4 o = r4[j];
+                w = make_float4(o.x + w.x, o.y + w.y, o.z + w.z, o.w + w.w);
+            }
+            r4[j] = w;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < kN; ++j)
+            if (j < n) row[j] = accumulate ? row[j] + a[j] * scale : a[j] * scale;
+    }
+}
+template <int kN>
+__device__ __forceinline__ void put_partial(float* row, const float (&a)[kN]) {
+#pragma unroll
+    for (int j = 0; j < kN / 4; ++j)
+        reinterpret_cast<float4*>(row)[j] = make_float4(a[4 * j], a[4 * j + 1], a[4 * j + 2], a[4 * j + 3]);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kGThreads) embed_grad_kernel(const __grid_constant__ GradArgs A) {
+    constexpr int kN = Lane<T>::kN;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t sum_blocks = (A.units + kGWarps - 1) / kGWarps;
+    if (static_cast<int64_t>(blockIdx.x) >= sum_blocks) {
+        // clear the rows of [r0, r0 + kZeroRows) that no token names
+        __shared__ bool absent[kZeroRows];
+        const int64_t r0 = (static_cast<int64_t>(blockIdx.x) - sum_blocks) * kZeroRows;
+        if (threadIdx.x < kZeroRows) {
+            const uint32_t v = static_cast<uint32_t>(r0 + threadIdx.x);
+            int64_t lo = 0, hi = A.N;  // first position whose key is >= v
+            while (lo < hi) {
+                const int64_t mid = (lo + hi) >> 1;
+                if (__ldg(A.key + mid) < v)
+                    lo = mid + 1;
+                else
+                    hi = mid;
+            }
+            absent[threadIdx.x] = r0 + threadIdx.x < A.V && (lo == A.N || __ldg(A.key + lo) != v);
+        }
+        __syncthreads();
+        for (int r = warp; r < kZeroRows; r += kGWarps) {
+            if (!absent[r]) continue;
+            float* row = A.G + (r0 + r) * A.ld_G;
+            for (int c = 4 * lane; c < A.d; c += 128) {
+                if (c + 4 <= A.d)
+                    *reinterpret_cast<float4*>(row + c) = make_float4(0.f, 0.f, 0.f, 0.f);
+                else
+                    for (int j = c; j < A.d; ++j) row[j] = 0.f;
+            }
+        }
+        return;
+    }
+    const int64_t unit = static_cast<int64_t>(blockIdx.x) * kGWarps + warp;
+    if (unit >= A.units) return;
+    const int64_t c = unit / A.slabs;
+    const int col = static_cast<int>(unit - c * A.slabs) * (32 * kN) + kN * lane;
+    const int n = A.d - col;  // columns left, this lane's own among them
+    const int64_t p0 = c * A.chunk, p1 = min(A.N, p0 + A.chunk);
+    const uint32_t none = static_cast<uint32_t>(A.V);
+    uint32_t cur = __ldg(A.key + p0);
+    bool began_before = p0 > 0 && __ldg(A.key + p0 - 1) == cur;
+    const T* g = static_cast<const T*>(A.g) + col;
+    float acc[kN] = {};
+    for (int64_t q = p0; q < p1 && cur != none; q += 32) {
+        const int cnt = static_cast<int>(min(static_cast<int64_t>(32), p1 - q));
+        uint32_t my_key = none;
+        int32_t my_idx = 0;
+        if (lane < cnt) {
+            my_key = __ldg(A.key + q + lane);
+            my_idx = __ldg(A.idx + q + lane);
+        }
+        for (int b = 0; b < cnt; b += 8) {
+            typename Lane<T>::Raw raw[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t k = __shfl_sync(0xFFFFFFFFu, my_key, b + j);
+                const int64_t t = __shfl_sync(0xFFFFFFFFu, my_idx, b + j);
+                raw[j] = typename Lane<T>::Raw{};
+                if (k != none) {
+                    if (n >= kN)
+                        raw[j] = __ldcs(reinterpret_cast<const typename Lane<T>::Raw*>(g + t * A.ld_g));
+                    else if (n > 0)
+                        raw[j] = Lane<T>::tail(g + t * A.ld_g, n);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t k = __shfl_sync(0xFFFFFFFFu, my_key, b + j);
+                if (b + j >= cnt || cur == none) break;  // uniform over the warp
+                if (k != cur) {
+                    if (n > 0) {
+                        if (began_before)
+                            put_partial(A.head + c * A.dpad + col, acc);
+                        else
+                            put_row(A.G + static_cast<int64_t>(cur) * A.ld_G + col, acc, n, A.scale, A.accumulate != 0);
+                    }
+                    began_before = false;
+                    cur = k;
+#pragma unroll
+                    for (int i = 0; i < kN; ++i) acc[i] = 0.f;
+                    if (cur == none) break;
+                }
+                Lane<T>::add(acc, raw[j]);
+            }
+        }
+    }
+    if (cur == none || n <= 0) return;
+    const bool goes_on = p1 < A.N && __ldg(A.key + p1) == cur;
+    if (began_before)
+        put_partial(A.head + c * A.dpad + col, acc);
+    else if (goes_on)
+        put_partial(A.tail + c * A.dpad + col, acc);
+    else
+        put_row(A.G + static_cast<int64_t>(cur) * A.ld_G + col, acc, n, A.scale, A.accumulate != 0);
+}
+
+// CTA (chunk, 128 columns): if an id begins in the chunk and goes on past its end, adds its partial
+// sums.  The eight warps take consecutive runs of chunks, summed in order and then warp by warp.
+__global__ void __launch_bounds__(kGThreads) embed_join_kernel(const __grid_constant__ GradArgs A, int32_t slabs) {
+    const int64_t c = blockIdx.x / slabs;
+    const int64_t p1 = (c + 1) * A.chunk;
+    if (p1 >= A.N) return;
+    const uint32_t cur = __ldg(A.key + p1 - 1);
+    if (cur == static_cast<uint32_t>(A.V) || __ldg(A.key + p1) != cur) return;
+    const int64_t p0 = c * A.chunk;
+    if (p0 > 0 && __ldg(A.key + p0 - 1) == cur) return;  // it began earlier
+    __shared__ float4 part[kGWarps][32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int col = static_cast<int>(blockIdx.x - c * slabs) * 128 + 4 * lane;
+    // chunks c + 1 .. end - 1 begin with this id
+    int64_t lo = c + 1, hi = A.chunks;
+    while (lo < hi) {
+        const int64_t mid = (lo + hi) >> 1;
+        if (__ldg(A.key + mid * A.chunk) == cur)
+            lo = mid + 1;
+        else
+            hi = mid;
+    }
+    const int64_t cnt = lo - (c + 1), per = (cnt + kGWarps - 1) / kGWarps;
+    const int64_t a = c + 1 + warp * per, b = min(lo, a + per);
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (col < A.dpad) {
+        if (warp == 0) s = *reinterpret_cast<const float4*>(A.tail + c * A.dpad + col);
+#pragma unroll 8
+        for (int64_t k = a; k < b; ++k) {
+            const float4 h = *reinterpret_cast<const float4*>(A.head + k * A.dpad + col);
+            s = make_float4(s.x + h.x, s.y + h.y, s.z + h.z, s.w + h.w);
+        }
+    }
+    part[warp][lane] = s;
+    __syncthreads();
+    if (warp == 0 && col < A.d) {
+        for (int w = 1; w < kGWarps; ++w) {
+            const float4 h = part[w][lane];
+            s = make_float4(s.x + h.x, s.y + h.y, s.z + h.z, s.w + h.w);
+        }
+        const float acc[4] = {s.x, s.y, s.z, s.w};
+        put_row(A.G + static_cast<int64_t>(cur) * A.ld_G + col, acc, A.d - col, A.scale, A.accumulate != 0);
+    }
+}
+
+struct GradPlan {
+    int64_t N;
+    int slabs, chunk, chunks, tiles, dpad, passes, bits;
+    size_t keys, hist, part;  // bytes of one array of each kind
+};
+
+// Chunk length: about 24 warps for each SM, between 32 and 1024 positions.
+GradPlan grad_plan(dust_dtype dt, int64_t N, int32_t V, int32_t d) {
+    GradPlan p{};
+    p.N = N;
+    const int cols = dt == DUST_BF16 ? 256 : 128;
+    p.slabs = (d + cols - 1) / cols;
+    const int64_t want = std::max<int64_t>(1, static_cast<int64_t>(num_sms()) * 24 / p.slabs);
+    int64_t c = 32;
+    while (c < 1024 && N / (2 * c) >= want) c *= 2;
+    p.chunk = static_cast<int>(c);
+    p.chunks = static_cast<int>((N + c - 1) / c);
+    p.tiles = static_cast<int>((N + kTile - 1) / kTile);
+    p.dpad = (d + 7) / 8 * 8;
+    int bits = 1;  // of the keys 0 .. V
+    while (bits < 31 && (static_cast<int64_t>(V) >> bits) != 0) ++bits;
+    p.passes = (bits + kBinBits - 1) / kBinBits;
+    p.bits = (bits + p.passes - 1) / p.passes;
+    p.keys = align_up(static_cast<size_t>(N) * 4, 256);
+    p.hist = align_up(static_cast<size_t>(p.tiles) * kBins * 4, 256);
+    p.part = align_up(static_cast<size_t>(p.chunks) * p.dpad * 4, 256);
+    return p;
+}
+
+template <typename TE, typename TO>
+void launch_lookup(const int32_t* ids, const void* E, int64_t ld_E, int64_t N, int32_t V, int32_t d, float scale,
+                   void* out, int64_t ld_out, unsigned blocks, int32_t nv, cudaStream_t s) {
+    embedding_kernel<TE, TO><<<blocks, kFThreads, 0, s>>>(ids, static_cast<const TE*>(E), ld_E, N, V, d, nv,
+                                                          div_magic(nv), scale, static_cast<TO*>(out), ld_out);
+}
+
+}  // namespace
+
+dust_status embedding_launch(const int32_t* ids, const void* E, dust_dtype dt, int64_t ld_E, int64_t N, int32_t V,
+                             int32_t d, float scale, void* out, dust_dtype out_dt, int64_t ld_out,
+                             cudaStream_t s) {
+    const int32_t nv = (d + 7) / 8;
+    const int64_t blocks = (N * nv + kFThreads * kFItems - 1) / (kFThreads * kFItems);
+    if (blocks > 2147483647LL) return DUST_ERR_UNSUPPORTED;
+    const unsigned nb = static_cast<unsigned>(blocks);
+    prof_begin(s);
+    if (dt == DUST_BF16 && out_dt == DUST_BF16)
+        launch_lookup<__nv_bfloat16, __nv_bfloat16>(ids, E, ld_E, N, V, d, scale, out, ld_out, nb, nv, s);
+    else if (dt == DUST_BF16)
+        launch_lookup<__nv_bfloat16, float>(ids, E, ld_E, N, V, d, scale, out, ld_out, nb, nv, s);
+    else if (out_dt == DUST_BF16)
+        launch_lookup<float, __nv_bfloat16>(ids, E, ld_E, N, V, d, scale, out, ld_out, nb, nv, s);
+    else
+        launch_lookup<float, float>(ids, E, ld_E, N, V, d, scale, out, ld_out, nb, nv, s);
+    prof_end(s, "embedding");
+    return cudaGetLastError() == cudaSuccess ? DUST_OK : DUST_ERR_CUDA;
+}
+
+size_t embedding_grad_workspace_bytes(dust_dtype dt, int64_t N, int32_t V, int32_t d) {
+    const GradPlan p = grad_plan(dt, N, V, d);
+    return 4 * p.keys + p.hist + 2 * p.part;
+}
+
+dust_status embedding_grad_launch(const int32_t* ids, const void* g, dust_dtype dt, int64_t ld_g, int64_t N,
+                                  int32_t V, int32_t d, float scale, float* G, int64_t ld_G, int accumulate,
+                                  void* ws, cudaStream_t s) {
+    const GradPlan p = grad_plan(dt, N, V, d);
+    char* w = static_cast<char*>(ws);
+    uint32_t* key[2] = {reinterpret_cast<uint32_t*>(w), reinterpret_cast<uint32_t*>(w + p.keys)};
+    int32_t* idx[2] = {reinterpret_cast<int32_t*>(w + 2 * p.keys), reinterpret_cast<int32_t*>(w + 3 * p.keys)};
+    int32_t* hist = reinterpret_cast<int32_t*>(w + 4 * p.keys);
+    float* head = reinterpret_cast<float*>(w + 4 * p.keys + p.hist);
+    float* tail = reinterpret_cast<float*>(w + 4 * p.keys + p.hist + p.part);
+    int at = 0;  // where the sorted list ends up
+    if (p.tiles == 1) {
+        static PerContextOnce attr;
+        if (!attr.run([] {
+                return cudaFuncSetAttribute(embed_sort_tile_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                            kSortTileSmem) == cudaSuccess;
+            }))
+            return DUST_ERR_CUDA;
+        prof_begin(s);
+        embed_sort_tile_kernel<<<1, kSThreads, kSortTileSmem, s>>>(ids, static_cast<int>(N), V, p.passes, p.bits,
+                                                                  key[0], idx[0]);
+        prof_end(s, "embedding_sort");
+    } else {
+        const uint32_t mask = (1u << p.bits) - 1u;
+        at = 1;
+        for (int pass = 0; pass < p.passes; ++pass) {
+            const int32_t* first = pass == 0 ? ids : nullptr;
+            const int to = at ^ 1;
+            prof_begin(s);
+            embed_hist_kernel<<<p.tiles, kSThreads, 0, s>>>(first, key[at], N, V, pass * p.bits, mask, hist);
+            prof_end(s, "embedding_sort_count");
+            prof_begin(s);
+            embed_scatter_kernel<<<p.tiles, kSThreads, 0, s>>>(first, key[at], idx[at], N, V, pass * p.bits, mask,
+                                                              hist, p.tiles, key[to], idx[to]);
+            prof_end(s, "embedding_sort");
+            at = to;
+        }
+    }
+    GradArgs A{};
+    A.key = key[at];
+    A.idx = idx[at];
+    A.g = g;
+    A.G = G;
+    A.head = head;
+    A.tail = tail;
+    A.ld_g = ld_g;
+    A.ld_G = ld_G;
+    A.N = N;
+    A.V = V;
+    A.d = d;
+    A.dpad = p.dpad;
+    A.slabs = p.slabs;
+    A.chunk = p.chunk;
+    A.chunks = p.chunks;
+    A.units = static_cast<int64_t>(p.chunks) * p.slabs;
+    A.accumulate = accumulate;
+    A.scale = scale;
+    A.zero_blocks = accumulate ? 0 : (V + kZeroRows - 1) / kZeroRows;
+    const int64_t blocks = (A.units + kGWarps - 1) / kGWarps + A.zero_blocks;
+    const int join_slabs = (d + 127) / 128;
+    if (blocks > 2147483647LL || static_cast<int64_t>(p.chunks) * join_slabs > 2147483647LL)
+        return DUST_ERR_UNSUPPORTED;
+    prof_begin(s);
+    if (dt == DUST_BF16)
+        embed_grad_kernel<__nv_bfloat16><<<static_cast<unsigned>(blocks), kGThreads, 0, s>>>(A);
+    else
+        embed_grad_kernel<float><<<static_cast<unsigned>(blocks), kGThreads, 0, s>>>(A);
+    prof_end(s, "embedding_grad");
+    if (p.chunks > 1) {
+        prof_begin(s);
+        embed_join_kernel<<<static_cast<unsigned>(p.chunks * join_slabs), kGThreads, 0, s>>>(A, join_slabs);
+        prof_end(s, "embedding_grad_join");
+    }
+    return cudaGetLastError() == cudaSuccess ? DUST_OK : DUST_ERR_CUDA;
+}
+
+}  // namespace dust

@@ -107,6 +107,10 @@ class PerContextOnce {
 bool make_tmap_bf16_2d(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols,
                        uint32_t box_rows, uint32_t box_cols);
 
+// The same with rows ld elements apart (ld a multiple of 8).
+bool make_tmap_bf16_2d_ld(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint64_t ld,
+                          uint32_t box_rows, uint32_t box_cols);
+
 // Encodes a 2-D row-major fp32 tensor [rows, cols] with leading dimension ld (elements) for
 // TMA with a (32 x box_rows) box and 128-byte swizzle: 32 floats make one 128-byte line.
 bool make_tmap_f32_2d_sw128(CUtensorMap* map, const float* base, uint64_t rows, uint64_t cols,
@@ -191,6 +195,11 @@ bool make_opt(const dust_opt_params* p, OptParams* o);
 dust_status opt_launch(const OptParams& o, const float* G, const OptTargets& t, int64_t n,
                        cudaStream_t s);
 
+// The same over many tensors (dust_opt_grouped.cu).
+dust_status opt_grouped_launch(const OptParams& o, const dust_opt_params* p, const dust_opt_tensor* ts,
+                               int n, bool g_bf16, bool eight, const float* g_scale,
+                               const int32_t* step, cudaStream_t s);
+
 // ---- weight estimate (dust_wgrad.cu)
 struct WgradLayerArgs {
     const float* r;
@@ -212,6 +221,30 @@ dust_status wgrad_launch(const float* r, int64_t ld_r, const void* x, dust_dtype
                          float sigma, NoiseKey key, float* G_W, int accumulate, float* g_out,
                          int g_terms, void* ws, cudaStream_t s, const OptParams* opt = nullptr,
                          const OptTargets* targets = nullptr);
+
+// The contraction alone on a given operand g [terms N, d_out]: out (+)= g^T x.
+size_t contract_workspace_bytes(int64_t N, int32_t d_in, int32_t d_out);
+dust_status contract_launch(const void* g, int64_t ld_g, int terms, const void* x, int64_t ld_x, int64_t N,
+                            int32_t d_in, int32_t d_out, float* out, int accumulate, void* ws, cudaStream_t s);
+
+// ---- linear layer with its epilogue, and its backward pass (dust_linear.cu)
+dust_status linear_launch(const void* x, int64_t ld_x, const void* W, const float* bias, int act, const void* res,
+                          int64_t ld_res, int64_t N, int32_t d_in, int32_t d_out, void* y, int out_bf16,
+                          int64_t ld_y, void* z, int64_t ld_z, cudaStream_t s);
+size_t linear_backward_workspace_bytes(int64_t N, int32_t d_in, int32_t d_out);
+dust_status linear_backward_launch(const void* dy, int dy_bf16, int64_t ld_dy, const void* z, int64_t ld_z,
+                                   const void* x, int64_t ld_x, const void* W, int act, int64_t N, int32_t d_in,
+                                   int32_t d_out, int terms, void* dx, int dx_bf16, int64_t ld_dx, float* dW,
+                                   float* db, int accumulate, void* ws, cudaStream_t s);
+
+// ---- token embedding and the gradient of its table (dust_embed.cu)
+dust_status embedding_launch(const int32_t* ids, const void* E, dust_dtype dt, int64_t ld_E, int64_t N, int32_t V,
+                             int32_t d, float scale, void* out, dust_dtype out_dt, int64_t ld_out,
+                             cudaStream_t s);
+size_t embedding_grad_workspace_bytes(dust_dtype dt, int64_t N, int32_t V, int32_t d);
+dust_status embedding_grad_launch(const int32_t* ids, const void* g, dust_dtype dt, int64_t ld_g, int64_t N,
+                                  int32_t V, int32_t d, float scale, float* G, int64_t ld_G, int accumulate,
+                                  void* ws, cudaStream_t s);
 
 // ---- generator test export (dust_api.cu)
 dust_status philox_debug_launch(const uint32_t* ctr, int64_t n, NoiseKey key, uint32_t* words,

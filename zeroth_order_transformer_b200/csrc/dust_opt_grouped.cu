@@ -1,0 +1,386 @@
+// Optimizer step over many tensors at once (dust_optimizer_step_grouped): the elementwise step of
+// dust_opt.cu for up to kMaxTensors tensors in one launch, with the moments in fp32 or, for Adam,
+// in 8 bits.
+//
+//   m' = b1 m + (1 - b1) g,  v' = b2 v + (1 - b2) g^2,  g = g_scale G
+//   w' = w - lr wd w;  w'' = w' - lr (m' / c1) / (sqrt(v') / sqrt(c2) + eps),  c = 1 - beta^t
+//
+// 8-bit moments: a block of 256 consecutive elements of a tensor (the last one may be shorter)
+// holds m / s_m and r / s_r, r = sqrt(v), as e4m3 codes with fp32 scales s = max / 448.  Choices:
+//   - sqrt(v) and not v: e4m3 spans 2^18 from its largest value to its smallest, which for v
+//     itself would be 2^9 in gradient size; an element whose v rounded to 0 while its m did not
+//     would take a step of m / eps.  For the same reason a positive r never gets code 0.
+//   - An fp32 scale and not a power of two: 1 - b2 = 0.001 is far below the codes' half step of
+//     2^-4, so a single element's code cannot follow a slow decay; the block's exact largest
+//     value does, and carries the others with it (with gradients cut tenfold after 3000 steps
+//     the median of the held sqrt(v) stays within 1.5% of the exact average's, scatter 15%).
+//   - Round to nearest even: no random numbers, the same result on every run.
+// All arithmetic is fp32; the codes are rounded from the fp32 moments after the weights have
+// used them.
+//
+// HBM-bound: per element 4 (G) + 8 (w) + 2 (bf16 copy) + 16 bytes with fp32 moments, + 4.06 with
+// 8-bit ones.
+#include <cuda_fp8.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "dust_device.cuh"
+#include "dust_internal.h"
+
+namespace dust {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kUnit = 4096;  // elements of one work unit: 16 blocks of an 8-bit tensor
+constexpr int kBlock = DUST_STATE_BLOCK;
+constexpr float kTop = 448.0f;  // largest e4m3 value
+// A block whose largest magnitude is below this is held as zeros: 448 / max stays finite.
+constexpr float kTiny = 7.888609052210118e-31f;  // 2^-100
+constexpr int kCtasPerSm = 32;
+
+struct OptTensor {
+    const void* G;
+    float* W;
+    __nv_bfloat16* Wb;
+    void* m;
+    void* v;
+    float* ms;
+    float* vs;
+    int64_t n;
+    int64_t unit_begin;
+    float lr, lr_wd;
+};
+
+template <int kMax>
+struct OptTable {
+    OptTensor t[kMax];
+    OptParams o;
+    const float* g_scale;
+    const int32_t* step;
+    float beta1, beta2;
+    int64_t units;
+    int n;
+};
+
+__device__ __forceinline__ float sqrt_approx(float x) {
+    float y;
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// 1 / c1 and 1 / sqrt(c2) of this step.
+struct Bias {
+    float i1, i2;
+};
+
+template <bool kGbf16>
+__device__ __forceinline__ float4 load_g4(const void* G, int64_t e) {
+    if (kGbf16) {
+        const uint2 w = __ldcs(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(G) + e));
+        return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u),
+                           __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xFFFF0000u));
+    }
+    return __ldcs(reinterpret_cast<const float4*>(static_cast<const float*>(G) + e));
+}
+template <bool kGbf16>
+__device__ __forceinline__ float load_g1(const void* G, int64_t e) {
+    return kGbf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(G)[e])
+                  : static_cast<const float*>(G)[e];
+}
+
+__device__ __forceinline__ void store_b4(__nv_bfloat16* p, float4 w) {
+    __nv_bfloat162 lo = __floats2bfloat162_rn(w.x, w.y);
+    __nv_bfloat162 hi = __floats2bfloat162_rn(w.z, w.w);
+    uint2 b;
+    b.x = *reinterpret_cast<uint32_t*>(&lo);
+    b.y = *reinterpret_cast<uint32_t*>(&hi);
+    *reinterpret_cast<uint2*>(p) = b;
+}
+
+// One element: the new moments and weight; `r` returns sqrt(v').
+template <bool kAdam>
+__device__ __forceinline__ void update(const OptParams& o, const OptTensor& t, Bias b, float g,
+                                       float& w, float& m, float& v, float& r) {
+    w = fmaf(-t.lr_wd, w, w);
+    if (kAdam) {
+        m = fmaf(o.b1, m, o.omb1 * g);
+        v = fmaf(o.b2, v, o.omb2 * (g * g));
+        r = sqrt_approx(v);
+        w = fmaf(-t.lr, __fdividef(m * b.i1, fmaf(r, b.i2, o.eps)), w);
+    } else {
+        m = fmaf(o.mu, m, g);
+        w = fmaf(-t.lr, m, w);
+    }
+}
+
+template <int kMax>
+__device__ __forceinline__ int find_tensor(const OptTable<kMax>& T, int64_t u) {
+    int lo = 0, hi = T.n;  // the last tensor whose first unit is <= u
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (T.t[mid].unit_begin <= u)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    return lo;
+}
+
+template <int kMax>
+__device__ __forceinline__ Bias bias_of(const OptTable<kMax>& T, float* sh) {
+    if (T.step == nullptr) return Bias{T.o.c1, T.o.c2};
+    // the step count on the device (a captured graph replays with the count it finds)
+    if (threadIdx.x == 0) {
+        const double t = static_cast<double>(max(*T.step, 1));
+        sh[0] = static_cast<float>(1.0 / (1.0 - pow(static_cast<double>(T.beta1), t)));
+        sh[1] = static_cast<float>(1.0 / sqrt(1.0 - pow(static_cast<double>(T.beta2), t)));
+    }
+    __syncthreads();
+    return Bias{sh[0], sh[1]};
+}
+
+template <int kMax, bool kAdam, bool kGbf16>
+__global__ void __launch_bounds__(kThreads) opt_grouped_f32_kernel(const __grid_constant__ OptTable<kMax> T) {
+    __shared__ float sh[2];
+    const Bias b = kAdam ? bias_of(T, sh) : Bias{1.f, 1.f};
+    const float gs = T.g_scale ? __ldg(T.g_scale) : 1.0f;
+    for (int64_t u = blockIdx.x; u < T.units; u += gridDim.x) {
+        const OptTensor& t = T.t[find_tensor(T, u)];
+        const int64_t e0 = (u - t.unit_begin) * kUnit;
+        float* const tm = static_cast<float*>(t.m);
+        float* const tv = static_cast<float*>(t.v);
+        const int64_t left = t.n - e0;
+        const int n = left < kUnit ? static_cast<int>(left) : kUnit;
+        const int n4 = n >> 2;
+#pragma unroll 2
+        for (int q = threadIdx.x; q < n4; q += kThreads) {
+            const int64_t e = e0 + 4 * q;
+            float4 g = load_g4<kGbf16>(t.G, e);
+            float4 w = *reinterpret_cast<const float4*>(t.W + e);
+            float4 m = *reinterpret_cast<const float4*>(tm + e);
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (kAdam) v = *reinterpret_cast<const float4*>(tv + e);
+            float r;
+            update<kAdam>(T.o, t, b, g.x * gs, w.x, m.x, v.x, r);
+            update<kAdam>(T.o, t, b, g.y * gs, w.y, m.y, v.y, r);
+            update<kAdam>(T.o, t, b, g.z * gs, w.z, m.z, v.z, r);
+            update<kAdam>(T.o, t, b, g.w * gs, w.w, m.w, v.w, r);
+            *reinterpret_cast<float4*>(t.W + e) = w;
+            *reinterpret_cast<float4*>(tm + e) = m;
+            if (kAdam) *reinterpret_cast<float4*>(tv + e) = v;
+            if (t.Wb) store_b4(t.Wb + e, w);
+        }
+        const int e1 = 4 * n4 + static_cast<int>(threadIdx.x);  // a tensor's last, partial quad
+        if (e1 < n) {
+            const int64_t e = e0 + e1;
+            float w = t.W[e], m = tm[e], v = kAdam ? tv[e] : 0.f, r;
+            update<kAdam>(T.o, t, b, load_g1<kGbf16>(t.G, e) * gs, w, m, v, r);
+            t.W[e] = w;
+            tm[e] = m;
+            if (kAdam) tv[e] = v;
+            if (t.Wb) t.Wb[e] = __float2bfloat16_rn(w);
+        }
+    }
+}
+
+// Four e4m3 codes to fp32 and back (the hardware's conversions; rounding to nearest even).
+__device__ __forceinline__ float4 from_e4m3(uint32_t c) {
+    const __half2_raw lo = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c & 0xFFFFu), __NV_E4M3);
+    const __half2_raw hi = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c >> 16), __NV_E4M3);
+    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+    const float2 d = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+    return make_float4(a.x, a.y, d.x, d.y);
+}
+__device__ __forceinline__ uint32_t to_e4m3(float4 y) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y.x, y.y), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y.z, y.w), __NV_SATFINITE, __NV_E4M3);
+    return lo | (hi << 16);
+}
+// The largest magnitude over the warp, as bits: magnitudes order like their bit patterns, with
+// infinity above every number and NaN above infinity, so neither is lost.
+__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
+__device__ __forceinline__ uint32_t max_bits(uint32_t a, float4 x) {
+    return max(max(max(a, abs_bits(x.x)), abs_bits(x.y)), max(abs_bits(x.z), abs_bits(x.w)));
+}
+
+// A warp takes one block at a time: lane l holds elements 4 l .. 4 l + 3 and 128 + 4 l .. + 3, so
+// every access of the warp is contiguous; the block's largest magnitudes are two warp reductions.
+template <int kMax, bool kGbf16>
+__global__ void __launch_bounds__(kThreads) opt_grouped_e4m3_kernel(const __grid_constant__ OptTable<kMax> T) {
+    __shared__ float sh[2];
+    const Bias b = bias_of(T, sh);
+    const float gs = T.g_scale ? __ldg(T.g_scale) : 1.0f;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int kWarps = kThreads / 32;
+    for (int64_t u = blockIdx.x; u < T.units; u += gridDim.x) {
+        const OptTensor& t = T.t[find_tensor(T, u)];
+        uint8_t* const tm = static_cast<uint8_t*>(t.m);
+        uint8_t* const tv = static_cast<uint8_t*>(t.v);
+        for (int k = warp; k < kUnit / kBlock; k += kWarps) {
+            const int64_t blk = (u - t.unit_begin) * (kUnit / kBlock) + k;
+            const int64_t e0 = blk * kBlock;
+            if (e0 >= t.n) break;
+            const float sm = t.ms[blk], sr = t.vs[blk];
+            float4 w[2], m[2], r[2];
+            const bool whole = e0 + kBlock <= t.n;
+            if (whole) {
+                float4 g[2];
+                uint32_t cm[2], cr[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int64_t e = e0 + 128 * h + 4 * lane;
+                    g[h] = load_g4<kGbf16>(t.G, e);
+                    w[h] = *reinterpret_cast<const float4*>(t.W + e);
+                    cm[h] = *reinterpret_cast<const uint32_t*>(tm + e);
+                    cr[h] = *reinterpret_cast<const uint32_t*>(tv + e);
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    m[h] = from_e4m3(cm[h]);
+                    r[h] = from_e4m3(cr[h]);
+                    float* gp = &g[h].x;
+                    float* wp = &w[h].x;
+                    float* mp = &m[h].x;
+                    float* rp = &r[h].x;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float r0 = rp[j] * sr;
+                        float mj = mp[j] * sm, vj = r0 * r0;
+                        update<true>(T.o, t, b, gp[j] * gs, wp[j], mj, vj, rp[j]);
+                        mp[j] = mj;
+                    }
+                }
+            } else {  // the tensor's last, shorter block: elements past its end count as zeros
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float* wp = &w[h].x;
+                    float* mp = &m[h].x;
+                    float* rp = &r[h].x;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int64_t e = e0 + 128 * h + 4 * lane + j;
+                        wp[j] = mp[j] = rp[j] = 0.f;
+                        if (e < t.n) {
+                            wp[j] = t.W[e];
+                            const float r0 = from_e4m3(tv[e]).x * sr;
+                            float mj = from_e4m3(tm[e]).x * sm, vj = r0 * r0;
+                            update<true>(T.o, t, b, load_g1<kGbf16>(t.G, e) * gs, wp[j], mj, vj, rp[j]);
+                            mp[j] = mj;
+                        }
+                    }
+                }
+            }
+            const float top_m = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, max_bits(max_bits(0u, m[0]), m[1])));
+            const float top_r = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, max_bits(max_bits(0u, r[0]), r[1])));
+            const bool zm = top_m < kTiny, zr = top_r < kTiny;  // false for NaN
+            const float im = zm ? 0.f : kTop / top_m, ir = zr ? 0.f : kTop / top_r;
+            if (lane == 0) {
+                t.ms[blk] = zm ? 0.f : top_m * (1.0f / kTop);
+                t.vs[blk] = zr ? 0.f : top_r * (1.0f / kTop);
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int64_t e = e0 + 128 * h + 4 * lane;
+                const uint32_t cm = to_e4m3(make_float4(m[h].x * im, m[h].y * im, m[h].z * im, m[h].w * im));
+                uint32_t cr = to_e4m3(make_float4(r[h].x * ir, r[h].y * ir, r[h].z * ir, r[h].w * ir));
+                // a positive r keeps at least the smallest code
+                const float* rp = &r[h].x;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (!zr && rp[j] > 0.f && ((cr >> (8 * j)) & 0xFFu) == 0u) cr |= 1u << (8 * j);
+                if (whole) {
+                    *reinterpret_cast<float4*>(t.W + e) = w[h];
+                    *reinterpret_cast<uint32_t*>(tm + e) = cm;
+                    *reinterpret_cast<uint32_t*>(tv + e) = cr;
+                    if (t.Wb) store_b4(t.Wb + e, w[h]);
+                } else {
+                    const float* wp = &w[h].x;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (e + j < t.n) {
+                            t.W[e + j] = wp[j];
+                            tm[e + j] = static_cast<uint8_t>(cm >> (8 * j));
+                            tv[e + j] = static_cast<uint8_t>(cr >> (8 * j));
+                            if (t.Wb) t.Wb[e + j] = __float2bfloat16_rn(wp[j]);
+                        }
+                }
+            }
+        }
+    }
+}
+
+// Tensors of one launch: a table of 32 is 2.6 KB of kernel parameters, one of 256 20 KB.
+constexpr int kFew = 32;
+constexpr int kMany = 256;
+
+template <int kMax>
+dust_status launch(const OptParams& o, const dust_opt_params* p, const dust_opt_tensor* ts, int n,
+                   bool g_bf16, bool eight, const float* g_scale, const int32_t* step, cudaStream_t s) {
+    OptTable<kMax> T;
+    T.o = o;
+    // the kernels multiply by the inverse corrections
+    T.o.c1 = 1.0f / o.c1;
+    T.o.c2 = static_cast<float>(1.0 / std::sqrt(static_cast<double>(o.c2)));
+    T.g_scale = g_scale;
+    T.step = o.kind == DUST_OPT_ADAM ? step : nullptr;
+    T.beta1 = p->beta1;
+    T.beta2 = p->beta2;
+    T.n = 0;
+    int64_t units = 0;
+    for (int i = 0; i < n; ++i) {
+        if (ts[i].n == 0) continue;
+        OptTensor& t = T.t[T.n++];
+        t.G = ts[i].G;
+        t.W = ts[i].W;
+        t.Wb = static_cast<__nv_bfloat16*>(ts[i].W_bf16);
+        t.m = ts[i].m;
+        t.v = ts[i].v;
+        t.ms = ts[i].m_scale;
+        t.vs = ts[i].v_scale;
+        t.n = ts[i].n;
+        t.unit_begin = units;
+        t.lr = o.lr * ts[i].lr_scale;
+        t.lr_wd = t.lr * p->weight_decay * ts[i].decay_scale;
+        units += (t.n + kUnit - 1) / kUnit;
+    }
+    if (units == 0) return DUST_OK;
+    T.units = units;
+    const unsigned blocks = static_cast<unsigned>(std::min<int64_t>(units, static_cast<int64_t>(num_sms()) * kCtasPerSm));
+    prof_begin(s);
+    if (eight) {
+        if (g_bf16)
+            opt_grouped_e4m3_kernel<kMax, true><<<blocks, kThreads, 0, s>>>(T);
+        else
+            opt_grouped_e4m3_kernel<kMax, false><<<blocks, kThreads, 0, s>>>(T);
+    } else if (o.kind == DUST_OPT_ADAM) {
+        if (g_bf16)
+            opt_grouped_f32_kernel<kMax, true, true><<<blocks, kThreads, 0, s>>>(T);
+        else
+            opt_grouped_f32_kernel<kMax, true, false><<<blocks, kThreads, 0, s>>>(T);
+    } else {
+        if (g_bf16)
+            opt_grouped_f32_kernel<kMax, false, true><<<blocks, kThreads, 0, s>>>(T);
+        else
+            opt_grouped_f32_kernel<kMax, false, false><<<blocks, kThreads, 0, s>>>(T);
+    }
+    prof_end(s, "optimizer_step_grouped");
+    return cudaGetLastError() == cudaSuccess ? DUST_OK : DUST_ERR_CUDA;
+}
+
+}  // namespace
+
+dust_status opt_grouped_launch(const OptParams& o, const dust_opt_params* p, const dust_opt_tensor* ts,
+                               int n, bool g_bf16, bool eight, const float* g_scale,
+                               const int32_t* step, cudaStream_t s) {
+    for (int i = 0; i < n; i += kMany) {
+        const int cnt = std::min(kMany, n - i);
+        const dust_status st = cnt <= kFew
+                                   ? launch<kFew>(o, p, ts + i, cnt, g_bf16, eight, g_scale, step, s)
+                                   : launch<kMany>(o, p, ts + i, cnt, g_bf16, eight, g_scale, step, s);
+        if (st != DUST_OK) return st;
+    }
+    return DUST_OK;
+}
+
+}  // namespace dust
