@@ -383,6 +383,8 @@ dust_status dust_optimizer_step(const dust_opt_params* opt, const float* G, floa
  * step: optional DEVICE int32 scalar with Adam's step count t, read by the kernels (values
  *   below 1 are taken as 1), so that a captured graph can be replayed over the steps; NULL takes
  *   opt->step.  opt->step must be >= 1 in either case.
+ * 1 - beta is formed from the decimal that the fp32 beta stands for (0.001 for 0.999f, where the fp32
+ * difference that dust_optimizer_step takes is off by 1.3e-5 of it).
  * A non-finite gradient makes its element's weight and moments non-finite (with 8-bit moments,
  * its block's moments).  Deterministic.
  */

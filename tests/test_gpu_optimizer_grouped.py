@@ -1,7 +1,7 @@
 """DustOptimizer (dust_optimizer_step_grouped) against the formulas in 64 bits.
 
-fp32 moments: m and v are each a product and a multiply-add of two terms (three half steps, 2^-24, of the
-terms' magnitudes, with (1 - beta) taken from the fp32 beta); w loses half a step for the decay and half for
+fp32 moments: m and v are each a product and a multiply-add of two terms with fp32 factors beta and 1 - beta
+(four half steps, 2^-24, of the terms' magnitudes; one and a half more for the square); w loses half a step for the decay and half for
 the update, and the update itself is right to 2^-19 relative (square root, quotient, bias corrections).
 8-bit moments: the held value is the moment rounded to e4m3 of its block's scale: off by at most half a step,
 2^-4 of the value or 2^-10 of the scale where that is larger, on top of the fp32 error; the weights use the moments
@@ -57,7 +57,7 @@ def held(opt, i, what):
 def steps(z, opt, decay, lrs, n_steps, kind, gs, seed, dev_step=False):
     import torch
     g = torch.Generator(device="cuda").manual_seed(seed)
-    b1, b2, lr, wd, eps, mu = f32(B1), f32(B2), f32(LR), f32(WD), f32(EPS), f32(0.8)
+    b1, b2, lr, wd, eps, mu = B1, B2, f32(LR), f32(WD), f32(EPS), f32(0.8)
     scale = torch.tensor([gs], device="cuda") if gs != 1.0 else None
     count = torch.zeros(1, dtype=torch.int32, device="cuda")
     for t in range(1, n_steps + 1):
@@ -139,7 +139,9 @@ def test_step_count_on_the_device(z, bits):
 
 
 def test_same_as_one_tensor_at_a_time(z):
-    """The step of dust_optimizer_step, within the two kernels' rounding."""
+    """The step of dust_optimizer_step, within the two kernels' rounding; v also within 1.3e-5, since that call takes
+    1 - beta2 from the fp32 beta2: |fl(0.999) - 0.999| = 1.29e-8, 1.29e-5 of 0.001.  (The bias correction
+    1 - beta2^t carries the same factor at small t, so the weights agree to rounding.)"""
     import torch
     opt, _, _ = make(z, [10000, 77], 32, torch.float32, 7)
     opt = z.DustOptimizer(opt.W, opt.G)
@@ -151,7 +153,7 @@ def test_same_as_one_tensor_at_a_time(z):
             z.dust_optimizer_step(z.adam(1e-3, t, weight_decay=0.01), opt.G[i], W[i], m[i], v[i])
     for i in range(2):
         assert torch.allclose(opt.W[i], W[i], rtol=1e-6, atol=1e-7)
-        assert torch.allclose(opt.m[i], m[i], rtol=1e-6, atol=0) and torch.allclose(opt.v[i], v[i], rtol=1e-6, atol=0)
+        assert torch.allclose(opt.m[i], m[i], rtol=1e-6, atol=0) and torch.allclose(opt.v[i], v[i], rtol=1.4e-5, atol=0)
 
 
 @pytest.mark.parametrize("bits", [32, 8])

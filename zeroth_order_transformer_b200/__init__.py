@@ -533,6 +533,11 @@ def dust_weight_grad_step(r, x, d_out: int, K_total: int, sigma: float, key: Noi
 
 # ------------------------------------------------------------------ around the estimator
 
+def _raw_stream(device) -> int:
+    """The handle of the current stream (without the Stream object around it, 3 us of host time)."""
+    return _torch()._C._cuda_getCurrentRawStream(device.index)
+
+
 class _NoScope:
     def __enter__(self):
         return None
@@ -623,7 +628,7 @@ def dust_linear(x, W, bias=None, act: str = "none", residual=None, y=None, z=Non
         st = lib().dust_linear(x.data_ptr(), ld_x, W.data_ptr(), _ptr(bias), code, _ptr(residual), ld_res,
                                DUST_BF16, N, d_in, d_out, y.data_ptr(),
                                DUST_BF16 if y.dtype == bf else DUST_F32, ld_y,
-                               z.data_ptr() if keep else None, ld_z, torch.cuda.current_stream().cuda_stream)
+                               z.data_ptr() if keep else None, ld_z, _raw_stream(dev))
     _check(st, "dust_linear")
     return (y, z) if keep else y
 
@@ -674,7 +679,7 @@ def dust_linear_backward(dy, x, W, act: str = "none", z=None, dx=True, dW=True, 
                                         int(g_terms), _ptr(dx),
                                         DUST_F32 if dx is not None and dx.dtype == f32 else DUST_BF16, ld_dx,
                                         _ptr(dW), _ptr(db), 1 if accumulate else 0, _ptr(ws), nb,
-                                        torch.cuda.current_stream().cuda_stream)
+                                        _raw_stream(dev))
     _check(st, "dust_linear_backward")
     return dx, dW, db
 
@@ -706,7 +711,7 @@ def dust_embedding(ids, E, scale: float = 1.0, out=None, out_dtype=None, stream=
             raise TypeError(f"out is {out.dtype}, out_dtype {out_dtype}")
         ld_out = _rows(out, "out", N, d, dev, both)
         st = lib().dust_embedding(ids.data_ptr(), E.data_ptr(), _dtype_code(E), ld_E, N, V, d, float(scale),
-                                  out.data_ptr(), _dtype_code(out), ld_out, torch.cuda.current_stream().cuda_stream)
+                                  out.data_ptr(), _dtype_code(out), ld_out, _raw_stream(dev))
     _check(st, "dust_embedding")
     return out
 
@@ -732,7 +737,7 @@ def dust_embedding_grad(ids, g, V: int, scale: float = 1.0, G=None, accumulate: 
         ws, nb = _workspace(workspace, dust_workspace_size(DUST_OP_EMBEDDING_GRAD, dt, N, V, d, 0), dev)
         st = lib().dust_embedding_grad(ids.data_ptr(), g.data_ptr(), dt, ld_g, N, V, d, float(scale), G.data_ptr(),
                                        ld_G, 1 if accumulate else 0, _ptr(ws), nb,
-                                       torch.cuda.current_stream().cuda_stream)
+                                       _raw_stream(dev))
     _check(st, "dust_embedding_grad")
     return G
 
@@ -822,7 +827,7 @@ class DustOptimizer:
             st = lib().dust_optimizer_step_grouped(ctypes.byref(opt), self._desc, len(self.W), self._g_dt,
                                                    DUST_STATE_F32 if self.bits == 32 else DUST_STATE_E4M3,
                                                    _ptr(g_scale), _ptr(step),
-                                                   torch.cuda.current_stream().cuda_stream)
+                                                   _raw_stream(self.device))
         _check(st, "dust_optimizer_step_grouped")
         return self.W
 

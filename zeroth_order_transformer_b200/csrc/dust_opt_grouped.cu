@@ -37,6 +37,7 @@ constexpr int kBlock = DUST_STATE_BLOCK;
 constexpr float kTop = 448.0f;  // largest e4m3 value
 // A block whose largest magnitude is below this is held as zeros: 448 / max stays finite.
 constexpr float kTiny = 7.888609052210118e-31f;  // 2^-100
+constexpr float kLeast = 1.0f / 512.0f;  // smallest positive e4m3 value
 constexpr int kCtasPerSm = 32;
 
 struct OptTensor {
@@ -58,7 +59,7 @@ struct OptTable {
     OptParams o;
     const float* g_scale;
     const int32_t* step;
-    float beta1, beta2;
+    double beta1, beta2;
     int64_t units;
     int n;
 };
@@ -98,6 +99,17 @@ __device__ __forceinline__ void store_b4(__nv_bfloat16* p, float4 w) {
     *reinterpret_cast<uint2*>(p) = b;
 }
 
+// One element of an 8-bit tensor: m and r = sqrt(v) in, m' and r' out.  The moments are formed with
+// one rounding for each product, sum and root, so that the codes are those of the formulas evaluated
+// step by step in fp32 (a contraction into a multiply-add moves one code in a million by a step).
+__device__ __forceinline__ void update8(const OptParams& o, const OptTensor& t, Bias b, float g, float& w,
+                                        float& m, float& r) {
+    m = __fadd_rn(__fmul_rn(m, o.b1), __fmul_rn(g, o.omb1));
+    r = __fsqrt_rn(__fadd_rn(__fmul_rn(__fmul_rn(r, r), o.b2), __fmul_rn(__fmul_rn(g, g), o.omb2)));
+    w = fmaf(-t.lr_wd, w, w);
+    w = fmaf(-t.lr, __fdividef(m * b.i1, fmaf(r, b.i2, o.eps)), w);
+}
+
 // One element: the new moments and weight; `r` returns sqrt(v').
 template <bool kAdam>
 __device__ __forceinline__ void update(const OptParams& o, const OptTensor& t, Bias b, float g,
@@ -133,8 +145,8 @@ __device__ __forceinline__ Bias bias_of(const OptTable<kMax>& T, float* sh) {
     // the step count on the device (a captured graph replays with the count it finds)
     if (threadIdx.x == 0) {
         const double t = static_cast<double>(max(*T.step, 1));
-        sh[0] = static_cast<float>(1.0 / (1.0 - pow(static_cast<double>(T.beta1), t)));
-        sh[1] = static_cast<float>(1.0 / sqrt(1.0 - pow(static_cast<double>(T.beta2), t)));
+        sh[0] = static_cast<float>(1.0 / (1.0 - pow(T.beta1, t)));
+        sh[1] = static_cast<float>(1.0 / sqrt(1.0 - pow(T.beta2, t)));
     }
     __syncthreads();
     return Bias{sh[0], sh[1]};
@@ -245,10 +257,9 @@ __global__ void __launch_bounds__(kThreads) opt_grouped_e4m3_kernel(const __grid
                     float* rp = &r[h].x;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const float r0 = rp[j] * sr;
-                        float mj = mp[j] * sm, vj = r0 * r0;
-                        update<true>(T.o, t, b, gp[j] * gs, wp[j], mj, vj, rp[j]);
-                        mp[j] = mj;
+                        mp[j] *= sm;
+                        rp[j] *= sr;
+                        update8(T.o, t, b, gp[j] * gs, wp[j], mp[j], rp[j]);
                     }
                 }
             } else {  // the tensor's last, shorter block: elements past its end count as zeros
@@ -263,32 +274,32 @@ __global__ void __launch_bounds__(kThreads) opt_grouped_e4m3_kernel(const __grid
                         wp[j] = mp[j] = rp[j] = 0.f;
                         if (e < t.n) {
                             wp[j] = t.W[e];
-                            const float r0 = from_e4m3(tv[e]).x * sr;
-                            float mj = from_e4m3(tm[e]).x * sm, vj = r0 * r0;
-                            update<true>(T.o, t, b, load_g1<kGbf16>(t.G, e) * gs, wp[j], mj, vj, rp[j]);
-                            mp[j] = mj;
+                            mp[j] = from_e4m3(tm[e]).x * sm;
+                            rp[j] = from_e4m3(tv[e]).x * sr;
+                            update8(T.o, t, b, load_g1<kGbf16>(t.G, e) * gs, wp[j], mp[j], rp[j]);
                         }
                     }
                 }
             }
             const float top_m = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, max_bits(max_bits(0u, m[0]), m[1])));
             const float top_r = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, max_bits(max_bits(0u, r[0]), r[1])));
-            const bool zm = top_m < kTiny, zr = top_r < kTiny;  // false for NaN
-            const float im = zm ? 0.f : kTop / top_m, ir = zr ? 0.f : kTop / top_r;
-            if (lane == 0) {
-                t.ms[blk] = zm ? 0.f : top_m * (1.0f / kTop);
-                t.vs[blk] = zr ? 0.f : top_r * (1.0f / kTop);
-            }
+            // even lanes form m's factors and odd lanes r's, so that the quotient is taken once
+            const float top = (lane & 1) ? top_r : top_m;
+            const bool tiny = top < kTiny;  // false for NaN
+            const float inv = tiny ? 0.f : kTop / top;
+            const float im = __shfl_sync(0xFFFFFFFFu, inv, 0), ir = __shfl_sync(0xFFFFFFFFu, inv, 1);
+            if (lane < 2) (lane ? t.vs : t.ms)[blk] = tiny ? 0.f : top * (1.0f / kTop);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int64_t e = e0 + 128 * h + 4 * lane;
-                const uint32_t cm = to_e4m3(make_float4(m[h].x * im, m[h].y * im, m[h].z * im, m[h].w * im));
-                uint32_t cr = to_e4m3(make_float4(r[h].x * ir, r[h].y * ir, r[h].z * ir, r[h].w * ir));
-                // a positive r keeps at least the smallest code
-                const float* rp = &r[h].x;
+                float* rp = &r[h].x;
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (!zr && rp[j] > 0.f && ((cr >> (8 * j)) & 0xFFu) == 0u) cr |= 1u << (8 * j);
+                for (int j = 0; j < 4; ++j) {
+                    const float y = rp[j] * ir;
+                    rp[j] = y > 0.f ? fmaxf(y, kLeast) : y;  // a positive r keeps at least the smallest code
+                }
+                const uint32_t cm = to_e4m3(make_float4(m[h].x * im, m[h].y * im, m[h].z * im, m[h].w * im));
+                const uint32_t cr = to_e4m3(r[h]);
                 if (whole) {
                     *reinterpret_cast<float4*>(t.W + e) = w[h];
                     *reinterpret_cast<uint32_t*>(tm + e) = cm;
@@ -314,18 +325,29 @@ __global__ void __launch_bounds__(kThreads) opt_grouped_e4m3_kernel(const __grid
 constexpr int kFew = 32;
 constexpr int kMany = 256;
 
+// 1 - beta is formed from the decimal that an fp32 beta stands for: 1 - 0.999f is off by 1.3e-5
+// relative.  A beta that is not the fp32 nearest to a decimal of seven places is taken as it is.
+double meant(float beta) {
+    const double d = std::round(static_cast<double>(beta) * 1e7) / 1e7;
+    return static_cast<float>(d) == beta ? d : static_cast<double>(beta);
+}
+
 template <int kMax>
 dust_status launch(const OptParams& o, const dust_opt_params* p, const dust_opt_tensor* ts, int n,
                    bool g_bf16, bool eight, const float* g_scale, const int32_t* step, cudaStream_t s) {
     OptTable<kMax> T;
     T.o = o;
-    // the kernels multiply by the inverse corrections
-    T.o.c1 = 1.0f / o.c1;
-    T.o.c2 = static_cast<float>(1.0 / std::sqrt(static_cast<double>(o.c2)));
+    if (o.kind == DUST_OPT_ADAM) {
+        T.beta1 = meant(p->beta1);
+        T.beta2 = meant(p->beta2);
+        T.o.omb1 = static_cast<float>(1.0 - T.beta1);
+        T.o.omb2 = static_cast<float>(1.0 - T.beta2);
+        // the kernels multiply by the inverse corrections
+        T.o.c1 = static_cast<float>(1.0 / (1.0 - std::pow(T.beta1, p->step)));
+        T.o.c2 = static_cast<float>(1.0 / std::sqrt(1.0 - std::pow(T.beta2, p->step)));
+    }
     T.g_scale = g_scale;
     T.step = o.kind == DUST_OPT_ADAM ? step : nullptr;
-    T.beta1 = p->beta1;
-    T.beta2 = p->beta2;
     T.n = 0;
     int64_t units = 0;
     for (int i = 0; i < n; ++i) {
