@@ -18,8 +18,9 @@
 // All arithmetic is fp32; the codes are rounded from the fp32 moments after the weights have
 // used them.
 //
-// HBM-bound: per element 4 (G) + 8 (w) + 2 (bf16 copy) + 16 bytes with fp32 moments, + 4.06 with
-// 8-bit ones.
+// HBM-bound: per element 4 (G) + 8 (w) + 2 (bf16 copy) + 16 bytes with fp32 moments, + 4.03 with
+// 8-bit ones.  Measured: 85 M weights in 120 tensors with fp32 moments 393 us (floor 390), 201 M in 40
+// tensors with 8-bit moments 592 us (floor 556).
 #include <cuda_fp8.h>
 
 #include <algorithm>
@@ -32,13 +33,15 @@ namespace dust {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnit = 4096;  // elements of one work unit: 16 blocks of an 8-bit tensor
+constexpr int kUnit = 4096;       // elements of one work unit with fp32 moments
+constexpr int kUnit8Small = 2048;  // with 8-bit moments: one block a warp,
+constexpr int kUnit8 = 16384;      // or eight, where that leaves enough units
+constexpr int kCtas8 = 4;          // CTAs of the 8-bit kernel that an SM holds
 constexpr int kBlock = DUST_STATE_BLOCK;
 constexpr float kTop = 448.0f;  // largest e4m3 value
 // A block whose largest magnitude is below this is held as zeros: 448 / max stays finite.
 constexpr float kTiny = 7.888609052210118e-31f;  // 2^-100
 constexpr float kLeast = 1.0f / 512.0f;  // smallest positive e4m3 value
-constexpr int kCtasPerSm = 32;
 
 struct OptTensor {
     const void* G;
@@ -61,7 +64,7 @@ struct OptTable {
     const int32_t* step;
     double beta1, beta2;
     int64_t units;
-    int n;
+    int n, unit;
 };
 
 __device__ __forceinline__ float sqrt_approx(float x) {
@@ -99,15 +102,23 @@ __device__ __forceinline__ void store_b4(__nv_bfloat16* p, float4 w) {
     *reinterpret_cast<uint2*>(p) = b;
 }
 
-// One element of an 8-bit tensor: m and r = sqrt(v) in, m' and r' out.  The moments are formed with
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ F2 both(float x) { return F2{x, x}; }
+
+// Two elements of an 8-bit tensor: m and r = sqrt(v) in, m' and r' out.  The moments are formed with
 // one rounding for each product, sum and root, so that the codes are those of the formulas evaluated
 // step by step in fp32 (a contraction into a multiply-add moves one code in a million by a step).
-__device__ __forceinline__ void update8(const OptParams& o, const OptTensor& t, Bias b, float g, float& w,
-                                        float& m, float& r) {
-    m = __fadd_rn(__fmul_rn(m, o.b1), __fmul_rn(g, o.omb1));
-    r = __fsqrt_rn(__fadd_rn(__fmul_rn(__fmul_rn(r, r), o.b2), __fmul_rn(__fmul_rn(g, g), o.omb2)));
-    w = fmaf(-t.lr_wd, w, w);
-    w = fmaf(-t.lr, __fdividef(m * b.i1, fmaf(r, b.i2, o.eps)), w);
+__device__ __forceinline__ void update8(const OptParams& o, const OptTensor& t, Bias b, F2 g, F2& w, F2& m, F2& r) {
+    m = add2(mul2(m, both(o.b1)), mul2(g, both(o.omb1)));
+    const F2 v = add2(mul2(mul2(r, r), both(o.b2)), mul2(mul2(g, g), both(o.omb2)));
+    r = F2{__fsqrt_rn(v.x), __fsqrt_rn(v.y)};
+    w = fma2(both(-t.lr_wd), w, w);
+    const F2 den = fma2(r, both(b.i2), both(o.eps)), num = mul2(m, both(b.i1));
+    w = fma2(both(-t.lr), mul2(num, F2{rcp_approx(den.x), rcp_approx(den.y)}), w);
 }
 
 // One element: the new moments and weight; `r` returns sqrt(v').
@@ -209,114 +220,159 @@ __device__ __forceinline__ uint32_t to_e4m3(float4 y) {
     const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y.z, y.w), __NV_SATFINITE, __NV_E4M3);
     return lo | (hi << 16);
 }
-// The largest magnitude over the warp, as bits: magnitudes order like their bit patterns, with
-// infinity above every number and NaN above infinity, so neither is lost.
-__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
-__device__ __forceinline__ uint32_t max_bits(uint32_t a, float4 x) {
-    return max(max(max(a, abs_bits(x.x)), abs_bits(x.y)), max(abs_bits(x.z), abs_bits(x.w)));
+// The larger magnitude, NaN if either is.
+__device__ __forceinline__ float max_abs(float a, float b) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(fabsf(a)), "f"(fabsf(b)));
+    return y;
+}
+__device__ __forceinline__ float max_abs4(float4 x) { return max_abs(max_abs(x.x, x.y), max_abs(x.z, x.w)); }
+// The largest over the warp: magnitudes order like their bit patterns, with infinity above every number
+// and NaN above infinity.
+__device__ __forceinline__ float warp_max(float x) {
+    return __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(x)));
 }
 
-// A warp takes one block at a time: lane l holds elements 4 l .. 4 l + 3 and 128 + 4 l .. + 3, so
-// every access of the warp is contiguous; the block's largest magnitudes are two warp reductions.
+// One block's operands as they are loaded: lane l holds elements 4 l .. 4 l + 3 and 128 + 4 l .. + 3, so
+// every access of the warp is contiguous.
+struct Block8 {
+    float4 g[2], w[2];
+    uint32_t cm[2], cr[2];
+};
+
+template <bool kGbf16>
+__device__ __forceinline__ void load_block(const OptTensor& t, int64_t blk, int lane, Block8& x) {
+    const uint8_t* const tm = static_cast<const uint8_t*>(t.m);
+    const uint8_t* const tv = static_cast<const uint8_t*>(t.v);
+    const int64_t e0 = blk * kBlock;
+    if (e0 + kBlock <= t.n) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int64_t e = e0 + 128 * h + 4 * lane;
+            x.g[h] = load_g4<kGbf16>(t.G, e);
+            x.w[h] = *reinterpret_cast<const float4*>(t.W + e);
+            x.cm[h] = *reinterpret_cast<const uint32_t*>(tm + e);
+            x.cr[h] = *reinterpret_cast<const uint32_t*>(tv + e);
+        }
+    } else {  // the tensor's last, shorter block: elements past its end count as zeros
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float* gp = &x.g[h].x;
+            float* wp = &x.w[h].x;
+            x.cm[h] = x.cr[h] = 0u;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int64_t e = e0 + 128 * h + 4 * lane + j;
+                gp[j] = wp[j] = 0.f;
+                if (e < t.n) {
+                    gp[j] = load_g1<kGbf16>(t.G, e);
+                    wp[j] = t.W[e];
+                    x.cm[h] |= static_cast<uint32_t>(tm[e]) << (8 * j);
+                    x.cr[h] |= static_cast<uint32_t>(tv[e]) << (8 * j);
+                }
+            }
+        }
+    }
+}
+
+// A positive r keeps at least the smallest code (a NaN stays one).
+__device__ __forceinline__ float held_root(float y) { return y > 0.f ? fmaxf(y, kLeast) : y; }
+
+// The step on one block and its stores; the block's largest magnitudes are two warp reductions.  The scales
+// come in and go out in sm and sr.
+__device__ __forceinline__ void step_block(const OptParams& o, const OptTensor& t, Bias b, float gs, int64_t blk,
+                                           int lane, Block8& x, float& sm, float& sr) {
+    uint8_t* const tm = static_cast<uint8_t*>(t.m);
+    uint8_t* const tv = static_cast<uint8_t*>(t.v);
+    const int64_t e0 = blk * kBlock;
+    const bool whole = e0 + kBlock <= t.n;
+    float4 m[2], r[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        m[h] = from_e4m3(x.cm[h]);
+        r[h] = from_e4m3(x.cr[h]);
+        const F2 g0 = mul2(F2{x.g[h].x, x.g[h].y}, both(gs)), g1 = mul2(F2{x.g[h].z, x.g[h].w}, both(gs));
+        F2 m0 = mul2(F2{m[h].x, m[h].y}, both(sm)), m1 = mul2(F2{m[h].z, m[h].w}, both(sm));
+        F2 r0 = mul2(F2{r[h].x, r[h].y}, both(sr)), r1 = mul2(F2{r[h].z, r[h].w}, both(sr));
+        F2 w0{x.w[h].x, x.w[h].y}, w1{x.w[h].z, x.w[h].w};
+        update8(o, t, b, g0, w0, m0, r0);
+        update8(o, t, b, g1, w1, m1, r1);
+        m[h] = make_float4(m0.x, m0.y, m1.x, m1.y);
+        r[h] = make_float4(r0.x, r0.y, r1.x, r1.y);
+        x.w[h] = make_float4(w0.x, w0.y, w1.x, w1.y);
+        if (whole) {
+            const int64_t e = e0 + 128 * h + 4 * lane;
+            *reinterpret_cast<float4*>(t.W + e) = x.w[h];
+            if (t.Wb) store_b4(t.Wb + e, x.w[h]);
+        }
+    }
+    const float top_m = warp_max(max_abs(max_abs4(m[0]), max_abs4(m[1])));
+    const float top_r = warp_max(max_abs(max_abs4(r[0]), max_abs4(r[1])));
+    // even lanes form m's factors and odd lanes r's, so that the quotient is taken once
+    const float top = (lane & 1) ? top_r : top_m;
+    const bool tiny = top < kTiny;  // false for NaN
+    const float inv = tiny ? 0.f : kTop / top;
+    const float im = __shfl_sync(0xFFFFFFFFu, inv, 0), ir = __shfl_sync(0xFFFFFFFFu, inv, 1);
+    const float scale = tiny ? 0.f : top * (1.0f / kTop);
+    sm = __shfl_sync(0xFFFFFFFFu, scale, 0);
+    sr = __shfl_sync(0xFFFFFFFFu, scale, 1);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int64_t e = e0 + 128 * h + 4 * lane;
+        const F2 m0 = mul2(F2{m[h].x, m[h].y}, both(im)), m1 = mul2(F2{m[h].z, m[h].w}, both(im));
+        const F2 r0 = mul2(F2{r[h].x, r[h].y}, both(ir)), r1 = mul2(F2{r[h].z, r[h].w}, both(ir));
+        const uint32_t cm = to_e4m3(make_float4(m0.x, m0.y, m1.x, m1.y));
+        const uint32_t cr = to_e4m3(make_float4(held_root(r0.x), held_root(r0.y), held_root(r1.x), held_root(r1.y)));
+        if (whole) {
+            *reinterpret_cast<uint32_t*>(tm + e) = cm;
+            *reinterpret_cast<uint32_t*>(tv + e) = cr;
+        } else {
+            const float* wp = &x.w[h].x;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (e + j < t.n) {
+                    t.W[e + j] = wp[j];
+                    tm[e + j] = static_cast<uint8_t>(cm >> (8 * j));
+                    tv[e + j] = static_cast<uint8_t>(cr >> (8 * j));
+                    if (t.Wb) t.Wb[e + j] = __float2bfloat16_rn(wp[j]);
+                }
+        }
+    }
+}
+
+// A warp takes a run of up to eight consecutive blocks, so that their scales are one 32-byte sector
+// each way: with a 4-byte load and store for each block the launch took 24% longer.
 template <int kMax, bool kGbf16>
-__global__ void __launch_bounds__(kThreads) opt_grouped_e4m3_kernel(const __grid_constant__ OptTable<kMax> T) {
+__global__ void __launch_bounds__(kThreads, kCtas8) opt_grouped_e4m3_kernel(const __grid_constant__ OptTable<kMax> T) {
     __shared__ float sh[2];
     const Bias b = bias_of(T, sh);
     const float gs = T.g_scale ? __ldg(T.g_scale) : 1.0f;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    constexpr int kWarps = kThreads / 32;
+    const int run = T.unit / kBlock / (kThreads / 32);
     for (int64_t u = blockIdx.x; u < T.units; u += gridDim.x) {
         const OptTensor& t = T.t[find_tensor(T, u)];
-        uint8_t* const tm = static_cast<uint8_t*>(t.m);
-        uint8_t* const tv = static_cast<uint8_t*>(t.v);
-        for (int k = warp; k < kUnit / kBlock; k += kWarps) {
-            const int64_t blk = (u - t.unit_begin) * (kUnit / kBlock) + k;
-            const int64_t e0 = blk * kBlock;
-            if (e0 >= t.n) break;
-            const float sm = t.ms[blk], sr = t.vs[blk];
-            float4 w[2], m[2], r[2];
-            const bool whole = e0 + kBlock <= t.n;
-            if (whole) {
-                float4 g[2];
-                uint32_t cm[2], cr[2];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int64_t e = e0 + 128 * h + 4 * lane;
-                    g[h] = load_g4<kGbf16>(t.G, e);
-                    w[h] = *reinterpret_cast<const float4*>(t.W + e);
-                    cm[h] = *reinterpret_cast<const uint32_t*>(tm + e);
-                    cr[h] = *reinterpret_cast<const uint32_t*>(tv + e);
-                }
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    m[h] = from_e4m3(cm[h]);
-                    r[h] = from_e4m3(cr[h]);
-                    float* gp = &g[h].x;
-                    float* wp = &w[h].x;
-                    float* mp = &m[h].x;
-                    float* rp = &r[h].x;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        mp[j] *= sm;
-                        rp[j] *= sr;
-                        update8(T.o, t, b, gp[j] * gs, wp[j], mp[j], rp[j]);
-                    }
-                }
-            } else {  // the tensor's last, shorter block: elements past its end count as zeros
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float* wp = &w[h].x;
-                    float* mp = &m[h].x;
-                    float* rp = &r[h].x;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int64_t e = e0 + 128 * h + 4 * lane + j;
-                        wp[j] = mp[j] = rp[j] = 0.f;
-                        if (e < t.n) {
-                            wp[j] = t.W[e];
-                            mp[j] = from_e4m3(tm[e]).x * sm;
-                            rp[j] = from_e4m3(tv[e]).x * sr;
-                            update8(T.o, t, b, load_g1<kGbf16>(t.G, e) * gs, wp[j], mp[j], rp[j]);
-                        }
-                    }
-                }
+        const int64_t first = ((u - t.unit_begin) * (kThreads / 32) + warp) * run;
+        const int64_t blocks = (t.n + kBlock - 1) / kBlock;
+        if (first >= blocks) continue;
+        const int cnt = static_cast<int>(min(static_cast<int64_t>(run), blocks - first));
+        float my_sm = 0.f, my_sr = 0.f;  // lane k: block first + k
+        if (lane < cnt) {
+            my_sm = t.ms[first + lane];
+            my_sr = t.vs[first + lane];
+        }
+        for (int k = 0; k < cnt; ++k) {
+            Block8 x;
+            load_block<kGbf16>(t, first + k, lane, x);
+            float sm = __shfl_sync(0xFFFFFFFFu, my_sm, k), sr = __shfl_sync(0xFFFFFFFFu, my_sr, k);
+            step_block(T.o, t, b, gs, first + k, lane, x, sm, sr);
+            if (lane == k) {
+                my_sm = sm;
+                my_sr = sr;
             }
-            const float top_m = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, max_bits(max_bits(0u, m[0]), m[1])));
-            const float top_r = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, max_bits(max_bits(0u, r[0]), r[1])));
-            // even lanes form m's factors and odd lanes r's, so that the quotient is taken once
-            const float top = (lane & 1) ? top_r : top_m;
-            const bool tiny = top < kTiny;  // false for NaN
-            const float inv = tiny ? 0.f : kTop / top;
-            const float im = __shfl_sync(0xFFFFFFFFu, inv, 0), ir = __shfl_sync(0xFFFFFFFFu, inv, 1);
-            if (lane < 2) (lane ? t.vs : t.ms)[blk] = tiny ? 0.f : top * (1.0f / kTop);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int64_t e = e0 + 128 * h + 4 * lane;
-                float* rp = &r[h].x;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float y = rp[j] * ir;
-                    rp[j] = y > 0.f ? fmaxf(y, kLeast) : y;  // a positive r keeps at least the smallest code
-                }
-                const uint32_t cm = to_e4m3(make_float4(m[h].x * im, m[h].y * im, m[h].z * im, m[h].w * im));
-                const uint32_t cr = to_e4m3(r[h]);
-                if (whole) {
-                    *reinterpret_cast<float4*>(t.W + e) = w[h];
-                    *reinterpret_cast<uint32_t*>(tm + e) = cm;
-                    *reinterpret_cast<uint32_t*>(tv + e) = cr;
-                    if (t.Wb) store_b4(t.Wb + e, w[h]);
-                } else {
-                    const float* wp = &w[h].x;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (e + j < t.n) {
-                            t.W[e + j] = wp[j];
-                            tm[e + j] = static_cast<uint8_t>(cm >> (8 * j));
-                            tv[e + j] = static_cast<uint8_t>(cr >> (8 * j));
-                            if (t.Wb) t.Wb[e + j] = __float2bfloat16_rn(wp[j]);
-                        }
-                }
-            }
+        }
+        if (lane < cnt) {
+            t.ms[first + lane] = my_sm;
+            t.vs[first + lane] = my_sr;
         }
     }
 }
@@ -338,6 +394,7 @@ dust_status launch(const OptParams& o, const dust_opt_params* p, const dust_opt_
     OptTable<kMax> T;
     T.o = o;
     if (o.kind == DUST_OPT_ADAM) {
+        T.o.eps = std::max(o.eps, 1.17549435e-38f);  // the quotients flush subnormal divisors to zero
         T.beta1 = meant(p->beta1);
         T.beta2 = meant(p->beta2);
         T.o.omb1 = static_cast<float>(1.0 - T.beta1);
@@ -349,6 +406,9 @@ dust_status launch(const OptParams& o, const dust_opt_params* p, const dust_opt_
     T.g_scale = g_scale;
     T.step = o.kind == DUST_OPT_ADAM ? step : nullptr;
     T.n = 0;
+    int64_t total = 0;
+    for (int i = 0; i < n; ++i) total += ts[i].n;
+    T.unit = !eight ? kUnit : total / kUnit8 >= static_cast<int64_t>(num_sms()) * kCtas8 * 4 ? kUnit8 : kUnit8Small;
     int64_t units = 0;
     for (int i = 0; i < n; ++i) {
         if (ts[i].n == 0) continue;
@@ -364,11 +424,12 @@ dust_status launch(const OptParams& o, const dust_opt_params* p, const dust_opt_
         t.unit_begin = units;
         t.lr = o.lr * ts[i].lr_scale;
         t.lr_wd = t.lr * p->weight_decay * ts[i].decay_scale;
-        units += (t.n + kUnit - 1) / kUnit;
+        units += (t.n + T.unit - 1) / T.unit;
     }
     if (units == 0) return DUST_OK;
     T.units = units;
-    const unsigned blocks = static_cast<unsigned>(std::min<int64_t>(units, static_cast<int64_t>(num_sms()) * kCtasPerSm));
+    // one CTA a unit: the block scheduler evens out the SMs (402 us with 32 CTAs an SM on the twelve-block stack)
+    const unsigned blocks = static_cast<unsigned>(std::min<int64_t>(units, 1 << 30));
     prof_begin(s);
     if (eight) {
         if (g_bf16)
