@@ -222,11 +222,6 @@ dust_status wgrad_launch(const float* r, int64_t ld_r, const void* x, dust_dtype
                          int g_terms, void* ws, cudaStream_t s, const OptParams* opt = nullptr,
                          const OptTargets* targets = nullptr);
 
-// The contraction alone on a given operand g [terms N, d_out]: out (+)= g^T x.
-size_t contract_workspace_bytes(int64_t N, int32_t d_in, int32_t d_out);
-dust_status contract_launch(const void* g, int64_t ld_g, int terms, const void* x, int64_t ld_x, int64_t N,
-                            int32_t d_in, int32_t d_out, float* out, int accumulate, void* ws, cudaStream_t s);
-
 // ---- linear layer with its epilogue, and its backward pass (dust_linear.cu)
 dust_status linear_launch(const void* x, int64_t ld_x, const void* W, const float* bias, int act, const void* res,
                           int64_t ld_res, int64_t N, int32_t d_in, int32_t d_out, void* y, int out_bf16,

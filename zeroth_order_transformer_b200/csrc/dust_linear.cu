@@ -3,15 +3,14 @@
 //   z = x W^T + b,  y = act(z) + residual
 //   dz = dy act'(z),  db = sum_t dz_t,  dW = dz^T x,  dx = dz W
 //
-// Three forms of the product:
+// Two forms of the product:
 //   linear_rows_kernel    few tokens (one sequence being extended): bound by reading W once.  A warp
 //                         holds four output rows of W against every token, 16 bytes a lane; where
 //                         there are few output rows the warps of a CTA split the contraction.
 //   linear_gemm_kernel    tcgen05 GEMM, persistent and warp-specialised: one warp feeds a TMA ring, one
-//                         thread issues the MMAs of a 128-token tile into one of two accumulators in
+//                         thread issues the MMAs of a 128-row tile into one of two accumulators in
 //                         tensor memory, eight warps run the epilogue of the previous tile from the other.
-//                         B is W [d_out, d_in], K-major in the forward product and MN-major in dx.
-//   the contraction of dust_wgrad.cu for dW.
+//                         The forward product, dx and dW differ in which operands are MN-major.
 // dz is formed once (linear_dz_kernel) as a bf16 operand, or as hi + lo bf16 terms (dz = hi + lo to
 // about 16 bits), with the column sums for db on the way.
 #include <algorithm>
@@ -32,10 +31,27 @@ constexpr float kInvSqrt2Pi = 0.39894228040143268f;
 
 __device__ __forceinline__ float logistic(float u) { return __fdividef(1.0f, 1.0f + __expf(-u)); }
 
+// Phi(-|z|) = erfc(|z| / sqrt 2) / 2 by the rational approximation 7.1.26 of Abramowitz and Stegun
+// (error of erf at most 1.5e-7, falling with exp(-z^2 / 2)); e returns exp(-z^2 / 2), which the density shares.
+__device__ __forceinline__ float lower_tail(float z, float& e) {
+    const float x = fabsf(z) * kSqrtHalf;
+    const float t = __fdividef(1.0f, fmaf(0.3275911f, x, 1.0f));
+    e = __expf(-x * x);
+    float p = fmaf(1.061405429f, t, -1.453152027f);
+    p = fmaf(p, t, 1.421413741f);
+    p = fmaf(p, t, -0.284496736f);
+    p = fmaf(p, t, 0.254829592f);
+    return 0.5f * p * t * e;
+}
+
 template <int kAct>
 __device__ __forceinline__ float act_fn(float z) {
     if (kAct == DUST_ACT_RELU) return z <= 0.f ? 0.f : z;  // keeps a NaN
-    if (kAct == DUST_ACT_GELU) return 0.5f * z * (1.0f + erff(z * kSqrtHalf));
+    if (kAct == DUST_ACT_GELU) {
+        float e;
+        const float q = z * lower_tail(z, e);
+        return z > 0.f ? z - q : q;
+    }
     if (kAct == DUST_ACT_GELU_TANH) return z * logistic(z * fmaf(kGeluB, z * z, kGeluA));
     if (kAct == DUST_ACT_SILU) return z * logistic(z);
     return z;
@@ -45,7 +61,9 @@ template <int kAct>
 __device__ __forceinline__ float act_slope(float z) {
     if (kAct == DUST_ACT_RELU) return z > 0.f ? 1.f : 0.f;
     if (kAct == DUST_ACT_GELU) {
-        const float cdf = 0.5f * (1.0f + erff(z * kSqrtHalf)), e = __expf(-0.5f * z * z);
+        float e;
+        const float q = lower_tail(z, e);
+        const float cdf = z > 0.f ? 1.0f - q : q;
         return e == 0.f ? cdf : fmaf(z * kInvSqrt2Pi, e, cdf);
     }
     if (kAct == DUST_ACT_GELU_TANH) {
@@ -67,6 +85,20 @@ __device__ __forceinline__ float act_any(int act, float z) {
         case DUST_ACT_SILU: return act_fn<DUST_ACT_SILU>(z);
     }
     return z;
+}
+template <int kAct, int kN>
+__device__ __forceinline__ void act_all(float (&v)[kN]) {
+#pragma unroll
+    for (int j = 0; j < kN; ++j) v[j] = act_fn<kAct>(v[j]);
+}
+template <int kN>
+__device__ __forceinline__ void act_block(int act, float (&v)[kN]) {
+    switch (act) {  // uniform over the grid
+        case DUST_ACT_RELU: act_all<DUST_ACT_RELU>(v); break;
+        case DUST_ACT_GELU: act_all<DUST_ACT_GELU>(v); break;
+        case DUST_ACT_GELU_TANH: act_all<DUST_ACT_GELU_TANH>(v); break;
+        case DUST_ACT_SILU: act_all<DUST_ACT_SILU>(v); break;
+    }
 }
 
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
@@ -165,220 +197,412 @@ __global__ void __launch_bounds__(kRThreads) linear_rows_kernel(const __grid_con
 }
 
 // ------------------------------------------------------------------ tensor-core GEMM
+// C [M, n_out] = sum over kTerms of A_term B, in 128 x kBN tiles and blocks of 64 along the contraction.  A is
+// K-major [M, K] (x, dz) or MN-major [K, M] (dz in dW, the tokens being the contraction); the second
+// term's rows follow the first's.  B is K-major [n_out, K] (W) or MN-major [K, n_out] (W in dx, x in dW).
 constexpr int kBM = 128;
 constexpr int kBK = 64;
 constexpr int kThreads = 320;  // TMA warp, MMA warp, eight epilogue warps
 constexpr uint32_t kABytes = kBM * kBK * 2;
+constexpr uint32_t kBox = kBK * 128;          // a 64-row x 64-element box of an MN-major operand
+constexpr uint32_t kStaging = 8 * 2 * 2048;   // each epilogue warp: 32 rows x 64 bytes of y and of z
+// The tensor cores truncate as they add to the accumulator: a sum of K products is off by about K 1.1e-9 of
+// its size toward zero (measured: 4.7e-7 at K = 512, 9.1e-6 at K = 8192).  An fp32 output is therefore collected
+// in registers, rounded to nearest, after every 16 blocks (1024 products) in the accumulator; a bf16 output's own
+// rounding is 200 times the largest error of K = 8192, and it is not.
+constexpr int kFlush = 16;
 
-template <int kBN>
+template <int kBN, int kTerms>
 struct Shape {
     static constexpr uint32_t kBBytes = kBN * kBK * 2;
-    static constexpr uint32_t kStageBytes = kABytes + kBBytes;
-    static constexpr int kStages = kBN == 256 ? 4 : kBN == 128 ? 6 : 8;
-    static constexpr uint32_t kSmem = kStages * kStageBytes + 1024 + 256;
+    static constexpr uint32_t kStageBytes = kTerms * kABytes + kBBytes;
+    static constexpr int kStages = static_cast<int>(192 * 1024 / kStageBytes);
+    static constexpr uint32_t kSmem = kStages * kStageBytes + kStaging + 1024 + 512;
     static constexpr uint32_t kTmemCols = 2 * kBN;
 };
+static_assert(Shape<256, 1>::kSmem <= 227 * 1024 && Shape<256, 2>::kSmem <= 227 * 1024, "exceeds shared memory");
 
-struct GemmArgs {
-    CUtensorMap ta;  // A [terms M, K], 64 x 128 boxes
-    CUtensorMap tb;  // K-major: B [n_out, K], 64 x kBN boxes; MN-major: B [K, n_out], 64 x 64 boxes
+struct Epilogue {
     const float* bias;
     const void* res;
     void* y;
     __nv_bfloat16* z;
-    ErrorWord* ew;
-    int64_t M, ld_res, ld_y, ld_z;
-    int n_out, k_blocks, terms, m_tiles, n_tiles, out_bf16;
+    int64_t M, ld_res, ld_y, ld_z;  // strides in elements
+    int n_out, act, out_bf16;
 };
 
-template <int kBN, bool kBmn, int kAct>
-__global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_constant__ GemmArgs A) {
-    using S = Shape<kBN>;
-    constexpr int kStages = S::kStages;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                               ~static_cast<uintptr_t>(1023));
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kStages * S::kStageBytes);
-    uint64_t* empty = full + kStages;
-    uint64_t* acc_full = empty + kStages;   // [2]
-    uint64_t* acc_empty = acc_full + 2;     // [2]
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int n_tiles = A.m_tiles * A.n_tiles;
-    const int nk = A.k_blocks * A.terms;
+struct GemmArgs {
+    CUtensorMap ta;  // K-major: 64 x 128 boxes; MN-major: 64 x 64
+    CUtensorMap tb;  // K-major: 64 x kBN boxes; MN-major: 64 x 64
+    Epilogue e;
+    ErrorWord* ew;
+    int64_t term_rows;   // rows of A from the first term to the second
+    int64_t split_elems; // elements of y from one split's partial to the next
+    int k_blocks, per_split, splits, m_tiles, n_tiles;
+};
 
+struct Pipe {
+    uint64_t *full, *empty, *acc_full, *acc_empty;
+    uint32_t tmem;
+    uint8_t* stages;
+    uint8_t* staging;
+};
+
+// Barriers, tensor memory; every thread of the CTA calls it.
+template <int kBN, int kTerms>
+__device__ __forceinline__ Pipe pipe_setup(uint8_t* smem, int epilogue_warps) {
+    using S = Shape<kBN, kTerms>;
+    Pipe P;
+    P.stages = smem;
+    P.staging = smem + S::kStages * S::kStageBytes;
+    P.full = reinterpret_cast<uint64_t*>(P.staging + kStaging);
+    P.empty = P.full + S::kStages;
+    P.acc_full = P.empty + S::kStages;  // [2]
+    P.acc_empty = P.acc_full + 2;       // [2]
+    uint32_t* slot = reinterpret_cast<uint32_t*>(P.acc_empty + 2);
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kStages; ++s) {
-            mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 1);
+        for (int s = 0; s < S::kStages; ++s) {
+            mbar_init(&P.full[s], 1);
+            mbar_init(&P.empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
-            mbar_init(&acc_full[b], 1);
-            mbar_init(&acc_empty[b], 8);  // one arrival per epilogue warp
+            mbar_init(&P.acc_full[b], 1);
+            mbar_init(&P.acc_empty[b], epilogue_warps);
         }
         fence_barrier_init();
     }
-    if (warp == 1) {
-        tmem_alloc(tmem_slot, S::kTmemCols);
+    if (threadIdx.x >> 5 == 1) {
+        tmem_alloc(slot, S::kTmemCols);
         tmem_relinquish();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    P.tmem = *slot;
+    return P;
+}
+
+// One thread: loads blocks [kb0, kb1) of tile (m0, n0) into the ring; kc counts blocks over the CTA's life.
+template <int kBN, bool kAmn, bool kBmn, int kTerms>
+__device__ __forceinline__ bool pipe_load(const GemmArgs& A, const Pipe& P, int m0, int n0, int kb0, int kb1,
+                                          uint32_t& kc) {
+    using S = Shape<kBN, kTerms>;
+    for (int kb = kb0; kb < kb1; ++kb, ++kc) {
+        const int s = kc % S::kStages;
+        if (kc >= S::kStages && !mbar_wait_bounded(&P.empty[s], ((kc / S::kStages) - 1) & 1, A.ew, 501)) return false;
+        uint8_t* a = P.stages + s * S::kStageBytes;
+        uint8_t* b = a + kTerms * kABytes;
+        const int k0 = kb * kBK;
+        mbar_arrive_expect_tx(&P.full[s], S::kStageBytes);
+#pragma unroll
+        for (int t = 0; t < kTerms; ++t) {
+            const int32_t off = t ? static_cast<int32_t>(A.term_rows) : 0;
+            if (kAmn) {
+                tma_load_2d(a + t * kABytes, &A.ta, &P.full[s], m0, off + k0);
+                tma_load_2d(a + t * kABytes + kBox, &A.ta, &P.full[s], m0 + 64, off + k0);
+            } else {
+                tma_load_2d(a + t * kABytes, &A.ta, &P.full[s], k0, off + m0);
+            }
+        }
+        if (kBmn) {
+#pragma unroll
+            for (int j = 0; j < kBN / 64; ++j) tma_load_2d(b + j * kBox, &A.tb, &P.full[s], n0 + 64 * j, k0);
+        } else {
+            tma_load_2d(b, &A.tb, &P.full[s], k0, n0);
+        }
+    }
+    return true;
+}
+
+// One thread: the MMAs of blocks [kb0, kb1) into accumulator columns d.
+template <int kBN, bool kAmn, bool kBmn, int kTerms>
+__device__ __forceinline__ bool pipe_mma(const GemmArgs& A, const Pipe& P, uint32_t d, int kb0, int kb1, uint32_t& kc) {
+    using S = Shape<kBN, kTerms>;
+    constexpr uint32_t idesc = idesc_bf16_f32(kBM, kBN, kAmn ? 1 : 0, kBmn ? 1 : 0);
+    for (int kb = kb0; kb < kb1; ++kb, ++kc) {
+        const int s = kc % S::kStages;
+        if (!mbar_wait_bounded(&P.full[s], (kc / S::kStages) & 1, A.ew, 502)) return false;
+        tc_fence_after();
+        const uint32_t a_addr = smem_u32(P.stages + s * S::kStageBytes);
+        const uint32_t b_addr = a_addr + kTerms * kABytes;
+#pragma unroll
+        for (int kk = 0; kk < kBK / 16; ++kk) {
+            // K-major: 32 bytes along the swizzled row per instruction.  MN-major: 16 contraction rows of 128
+            // bytes; 8-row groups 1024 bytes apart, 64-element boxes kBox apart
+            const uint64_t bd = kBmn ? sdesc_sw128(b_addr + kk * 2048, kBox, 1024)
+                                     : sdesc_sw128(b_addr + kk * 32, 16, 1024);
+#pragma unroll
+            for (int t = 0; t < kTerms; ++t) {
+                const uint64_t ad = kAmn ? sdesc_sw128(a_addr + t * kABytes + kk * 2048, kBox, 1024)
+                                         : sdesc_sw128(a_addr + t * kABytes + kk * 32, 16, 1024);
+                umma_bf16(d, ad, bd, idesc, (kb > kb0 || kk > 0 || t > 0) ? 1u : 0u);
+            }
+        }
+        umma_commit(&P.empty[s]);
+    }
+    return true;
+}
+
+// A warp's 32 rows x 64 bytes in shared memory, 16-byte piece j of row r at j ^ (r / 2 mod 4): rows are
+// written and read thread by thread and written out four lanes to a row, both without bank conflicts.
+__device__ __forceinline__ uint4* staged(uint8_t* buf, int row, int piece) {
+    return reinterpret_cast<uint4*>(buf + row * 64 + ((piece ^ ((row >> 1) & 3)) << 4));
+}
+// The 64 bytes from column byte col_b of the warp's rows t0 .. t0 + 31, those inside [0, M) and below end_b.
+__device__ __forceinline__ void rows_out(uint8_t* buf, void* base, int64_t t0, int64_t M, int64_t pitch_b, int64_t col_b,
+                                         int64_t end_b, int lane) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int row = (lane >> 2) + 8 * i, piece = lane & 3;
+        if (t0 + row < M && col_b + 16 * piece < end_b)
+            *reinterpret_cast<uint4*>(static_cast<uint8_t*>(base) + (t0 + row) * pitch_b + col_b + 16 * piece) =
+                *staged(buf, row, piece);
+    }
+}
+__device__ __forceinline__ void rows_in(uint8_t* buf, const void* base, int64_t t0, int64_t M, int64_t pitch_b,
+                                        int64_t col_b, int64_t end_b, int lane) {
+    uint4 w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int row = (lane >> 2) + 8 * i, piece = lane & 3;
+        w[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (t0 + row < M && col_b + 16 * piece < end_b)
+            w[i] = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(base) + (t0 + row) * pitch_b + col_b +
+                                                   16 * piece);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) *staged(buf, (lane >> 2) + 8 * i, lane & 3) = w[i];
+}
+
+// Bias, pre-activation, activation, residual and store of kN columns from o of the warp's rows t0 .. + 31 (lane:
+// row).  kN = 32 for a bf16 y, 16 for an fp32 one: 64 bytes of a row.  kLayer false: no bias, z or activation.
+// All lanes call it.
+template <int kN, bool kLayer>
+__device__ __forceinline__ void finish(const Epilogue& E, void* y, float (&v)[kN], int64_t t0, int o, uint8_t* sy,
+                                       uint8_t* sz, int lane) {
+    constexpr int kEs = 64 / kN;  // bytes of an element of y
+    if (E.res) rows_in(sy, E.res, t0, E.M, E.ld_res * kEs, static_cast<int64_t>(o) * kEs, static_cast<int64_t>(E.n_out) * kEs, lane);
+    if (kLayer && E.bias) {
+#pragma unroll
+        for (int j = 0; j < kN / 4; ++j)
+            if (o + 4 * j < E.n_out) {
+                const float4 b = __ldg(reinterpret_cast<const float4*>(E.bias + o) + j);
+                v[4 * j] += b.x;
+                v[4 * j + 1] += b.y;
+                v[4 * j + 2] += b.z;
+                v[4 * j + 3] += b.w;
+            }
+    }
+    if (kLayer && E.z) {
+        uint32_t w[kN / 2];
+#pragma unroll
+        for (int j = 0; j < kN / 2; ++j) w[j] = pack2(v[2 * j], v[2 * j + 1]);
+        if (kN == 32) {
+#pragma unroll
+            for (int p = 0; p < kN / 8; ++p)
+                *staged(sz, lane, p) = make_uint4(w[4 * p], w[4 * p + 1], w[4 * p + 2], w[4 * p + 3]);
+        } else if (t0 + lane < E.M) {  // 32 bytes of a row: written by its thread
+            uint4* zp = reinterpret_cast<uint4*>(E.z + (t0 + lane) * E.ld_z + o);
+#pragma unroll
+            for (int p = 0; p < kN / 8; ++p) zp[p] = make_uint4(w[4 * p], w[4 * p + 1], w[4 * p + 2], w[4 * p + 3]);
+        }
+    }
+    if (kLayer) act_block(E.act, v);
+    __syncwarp();
+    uint32_t w[16];
+    if (E.res) {
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            const uint4 r = *staged(sy, lane, p);
+            w[4 * p] = r.x, w[4 * p + 1] = r.y, w[4 * p + 2] = r.z, w[4 * p + 3] = r.w;
+        }
+        if (kN == 32) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                v[(2 * j) % kN] += bf_lo(w[j]);
+                v[(2 * j + 1) % kN] += bf_hi(w[j]);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < kN && j < 16; ++j) v[j] += __uint_as_float(w[j]);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+        w[j] = kN == 32 ? pack2(v[(2 * j) % kN], v[(2 * j + 1) % kN]) : __float_as_uint(v[j % kN]);
+#pragma unroll
+    for (int p = 0; p < 4; ++p) *staged(sy, lane, p) = make_uint4(w[4 * p], w[4 * p + 1], w[4 * p + 2], w[4 * p + 3]);
+    __syncwarp();
+    rows_out(sy, y, t0, E.M, E.ld_y * kEs, static_cast<int64_t>(o) * kEs, static_cast<int64_t>(E.n_out) * kEs, lane);
+    if (kLayer && kN == 32 && E.z)
+        rows_out(sz, E.z, t0, E.M, E.ld_z * 2, static_cast<int64_t>(o) * 2, static_cast<int64_t>(E.n_out) * 2, lane);
+    __syncwarp();
+}
+
+// Tiles in groups of sixteen row tiles, columns slow within a group: the CTAs at work share few tiles of A and B.
+constexpr int kGroup = 16;
+__device__ __forceinline__ void tile_of(int tile, int m_tiles, int n_tiles, int& m, int& n) {
+    const int per = kGroup * n_tiles, g = tile / per, r = tile - g * per;
+    const int rows = min(kGroup, m_tiles - g * kGroup);
+    n = r / rows;
+    m = g * kGroup + r - n * rows;
+}
+
+// Persistent: one CTA per SM walks (tile, split) items; each accumulator (two of them) is read by the
+// epilogue warps while the MMAs fill the other.  kPromote: see kFlush.
+template <int kBN, bool kAmn, bool kBmn, int kTerms, bool kPromote>
+__global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_constant__ GemmArgs A) {
+    using S = Shape<kBN, kTerms>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~static_cast<uintptr_t>(1023));
+    const Pipe P = pipe_setup<kBN, kTerms>(smem, 8);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int tiles = A.m_tiles * A.n_tiles;
+    const int items = tiles * A.splits;
+    constexpr int kChunk = kPromote ? kFlush / kTerms : 1 << 30;
 
     if (warp == 0) {
         if (lane == 0) {
             prefetch_tensormap(&A.ta);
             prefetch_tensormap(&A.tb);
             uint32_t kc = 0;
-            bool ok = true;
-            for (int tile = blockIdx.x; tile < n_tiles && ok; tile += gridDim.x) {
-                const int m0 = tile % A.m_tiles * kBM;
-                const int n0 = tile / A.m_tiles * kBN;
-                for (int kb = 0; kb < nk; ++kb, ++kc) {
-                    const int s = kc % kStages;
-                    if (kc >= kStages &&
-                        !mbar_wait_bounded(&empty[s], ((kc / kStages) - 1) & 1, A.ew, 501)) {
-                        ok = false;
-                        break;
-                    }
-                    uint8_t* a = smem + s * S::kStageBytes;
-                    // the second term's rows follow the first's; B starts over with each term
-                    const int term = kb >= A.k_blocks ? 1 : 0;
-                    const int k0 = (kb - term * A.k_blocks) * kBK;
-                    mbar_arrive_expect_tx(&full[s], S::kStageBytes);
-                    tma_load_2d(a, &A.ta, &full[s], k0, m0 + (term ? static_cast<int32_t>(A.M) : 0));
-                    if (kBmn) {
-#pragma unroll
-                        for (int j = 0; j < kBN / 64; ++j)
-                            tma_load_2d(a + kABytes + j * (kBK * 128), &A.tb, &full[s], n0 + 64 * j, k0);
-                    } else {
-                        tma_load_2d(a + kABytes, &A.tb, &full[s], k0, n0);
-                    }
-                }
+            for (int it = blockIdx.x; it < items; it += gridDim.x) {
+                int m, n;
+                tile_of(it % tiles, A.m_tiles, A.n_tiles, m, n);
+                const int kb0 = it / tiles * A.per_split, kb1 = min(A.k_blocks, kb0 + A.per_split);
+                if (!pipe_load<kBN, kAmn, kBmn, kTerms>(A, P, m * kBM, n * kBN, kb0, kb1, kc)) break;
             }
         }
     } else if (warp == 1) {
         if (lane == 0) {
-            constexpr uint32_t idesc = idesc_bf16_f32(kBM, kBN, 0, kBmn ? 1 : 0);
             uint32_t kc = 0;
-            int lt = 0;
+            uint32_t ci = 0;  // chunks so far: chunk ci goes to accumulator ci mod 2
             bool ok = true;
-            for (int tile = blockIdx.x; tile < n_tiles && ok; tile += gridDim.x, ++lt) {
-                const int buf = lt & 1;
-                // the epilogue of the tile that last used this accumulator has read it
-                if (lt >= 2 && !mbar_wait_bounded(&acc_empty[buf], ((lt >> 1) - 1) & 1, A.ew, 502)) break;
-                tc_fence_after();
-                const uint32_t d = tmem + static_cast<uint32_t>(buf * kBN);
-                for (int kb = 0; kb < nk; ++kb, ++kc) {
-                    const int s = kc % kStages;
-                    if (!mbar_wait_bounded(&full[s], (kc / kStages) & 1, A.ew, 503)) {
+            for (int it = blockIdx.x; it < items && ok; it += gridDim.x) {
+                const int kb0 = it / tiles * A.per_split, kb1 = min(A.k_blocks, kb0 + A.per_split);
+                for (int k = kb0; k < kb1 && ok; ++ci) {
+                    const int k2 = kb1 - k > kChunk ? k + kChunk : kb1;
+                    const uint32_t buf = ci & 1;
+                    // the epilogue of the chunk that last used this accumulator has read it
+                    if (ci >= 2 && !mbar_wait_bounded(&P.acc_empty[buf], ((ci >> 1) - 1) & 1, A.ew, 503)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t a_addr = smem_u32(smem + s * S::kStageBytes);
-                    const uint32_t b_addr = a_addr + kABytes;
-#pragma unroll
-                    for (int kk = 0; kk < kBK / 16; ++kk) {
-                        const uint64_t ad = sdesc_sw128(a_addr + kk * 32, 16, 1024);
-                        // MN-major: 16 contraction rows of 128 bytes per instruction, 8-row groups 1024
-                        // bytes apart, 64-column boxes kBK * 128 bytes apart
-                        const uint64_t bd = kBmn ? sdesc_sw128(b_addr + kk * 2048, kBK * 128, 1024)
-                                                 : sdesc_sw128(b_addr + kk * 32, 16, 1024);
-                        umma_bf16(d, ad, bd, idesc, (kb | kk) != 0 ? 1u : 0u);
-                    }
-                    umma_commit(&empty[s]);
+                    ok = pipe_mma<kBN, kAmn, kBmn, kTerms>(A, P, P.tmem + buf * kBN, k, k2, kc);
+                    umma_commit(&P.acc_full[buf]);
+                    k = k2;
                 }
-                umma_commit(&acc_full[buf]);
             }
         }
     } else {
-        // epilogue warps 2 .. 9: tensor-memory lane quarter warp % 4, column half hf
+        // epilogue warps 2 .. 9: tensor-memory lane quarter warp % 4 (32 rows), column half hf
         const int q = warp & 3;
         const int hf = (warp - 2) >> 2;
-        int lt = 0;
-        for (int tile = blockIdx.x; tile < n_tiles; tile += gridDim.x, ++lt) {
-            const int buf = lt & 1;
-            const int n0 = tile / A.m_tiles * kBN;
-            if (!mbar_wait_bounded(&acc_full[buf], (lt >> 1) & 1, A.ew, 504)) break;
-            __syncwarp();
-            tc_fence_after();
-            const int64_t t = static_cast<int64_t>(tile % A.m_tiles) * kBM + q * 32 + lane;
-            const bool valid = t < A.M;
-            const uint32_t trow = tmem + static_cast<uint32_t>(buf * kBN) + (static_cast<uint32_t>(q * 32) << 16);
-            const int nchunks = min(kBN, A.n_out - n0) / 16;
-            const int c_end = min(nchunks, (hf + 1) * (kBN / 32));
-            for (int c = hf * (kBN / 32); c < c_end; ++c) {
-                float v[16];
-                tmem_ld16(trow + c * 16, v);
-                tmem_wait_ld();
-                if (!valid) continue;
-                const int o = n0 + c * 16;
-                if (A.bias) {
+        uint8_t* sy = P.staging + (warp - 2) * 4096;
+        uint8_t* sz = sy + 2048;
+        constexpr int kCols = kBN / 2;
+        const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
+        uint32_t ci = 0;
+        bool ok = true;
+        for (int it = blockIdx.x; it < items && ok; it += gridDim.x) {
+            int m, n;
+            tile_of(it % tiles, A.m_tiles, A.n_tiles, m, n);
+            const int split = it / tiles;
+            const int kb0 = split * A.per_split, kb1 = min(A.k_blocks, kb0 + A.per_split);
+            const int64_t t0 = static_cast<int64_t>(m) * kBM + q * 32;
+            const int o0 = n * kBN + hf * kCols;
+            void* y = static_cast<uint8_t*>(A.e.y) + split * A.split_elems * (A.e.out_bf16 ? 2 : 4);
+            if (kPromote) {
+                float acc[kCols];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float4 b = __ldg(reinterpret_cast<const float4*>(A.bias + o) + j);
-                        v[4 * j] += b.x;
-                        v[4 * j + 1] += b.y;
-                        v[4 * j + 2] += b.z;
-                        v[4 * j + 3] += b.w;
+                for (int j = 0; j < kCols; ++j) acc[j] = 0.f;
+                for (int k = kb0; k < kb1 && ok; k += kChunk, ++ci) {
+                    const uint32_t buf = ci & 1;
+                    if (!mbar_wait_bounded(&P.acc_full[buf], (ci >> 1) & 1, A.ew, 504)) {
+                        ok = false;
+                        break;
+                    }
+                    __syncwarp();
+                    tc_fence_after();
+                    const uint32_t trow = P.tmem + buf * kBN + hf * kCols + lane_base;
+#pragma unroll
+                    for (int c = 0; c < kCols / 16; ++c) {
+                        float v[16];
+                        tmem_ld16(trow + c * 16, v);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) acc[c * 16 + j] += v[j];
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&P.acc_empty[buf]);
+                }
+                if (!ok) break;
+#pragma unroll
+                for (int c = 0; c < kCols / 16; ++c) {
+                    if (o0 + c * 16 < A.e.n_out) {  // uniform over the warp
+                        float v[16];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) v[j] = acc[c * 16 + j];
+                        finish<16, !kBmn>(A.e, y, v, t0, o0 + c * 16, sy, sz, lane);
                     }
                 }
-                if (A.z) {
-                    uint4* zp = reinterpret_cast<uint4*>(A.z + t * A.ld_z + o);
-                    zp[0] = make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
-                    zp[1] = make_uint4(pack2(v[8], v[9]), pack2(v[10], v[11]), pack2(v[12], v[13]), pack2(v[14], v[15]));
-                }
+            } else {
+                const uint32_t buf = ci & 1;
+                if (!mbar_wait_bounded(&P.acc_full[buf], (ci >> 1) & 1, A.ew, 505)) break;
+                __syncwarp();
+                tc_fence_after();
+                const uint32_t trow = P.tmem + buf * kBN + hf * kCols + lane_base;
+#pragma unroll 1
+                for (int c = 0; c < kCols / 32; ++c) {
+                    if (o0 + c * 32 >= A.e.n_out) break;  // uniform over the warp
+                    float v[32];
+                    float a[16], b[16];
+                    tmem_ld16(trow + c * 32, a);
+                    tmem_ld16(trow + c * 32 + 16, b);
+                    tmem_wait_ld();
 #pragma unroll
-                for (int j = 0; j < 16; ++j) v[j] = act_fn<kAct>(v[j]);
-                if (A.out_bf16) {
-                    if (A.res) {
-                        const uint4* rp = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(A.res) +
-                                                                         t * A.ld_res + o);
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const uint4 r = rp[h];
-                            const uint32_t rw[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                v[8 * h + 2 * j] += bf_lo(rw[j]);
-                                v[8 * h + 2 * j + 1] += bf_hi(rw[j]);
-                            }
-                        }
+                    for (int j = 0; j < 16; ++j) {
+                        v[j] = a[j];
+                        v[16 + j] = b[j];
                     }
-                    uint4* yp = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(A.y) + t * A.ld_y + o);
-                    yp[0] = make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
-                    yp[1] = make_uint4(pack2(v[8], v[9]), pack2(v[10], v[11]), pack2(v[12], v[13]), pack2(v[14], v[15]));
-                } else {
-                    if (A.res) {
-                        const float4* rp = reinterpret_cast<const float4*>(static_cast<const float*>(A.res) +
-                                                                           t * A.ld_res + o);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float4 r = rp[j];
-                            v[4 * j] += r.x;
-                            v[4 * j + 1] += r.y;
-                            v[4 * j + 2] += r.z;
-                            v[4 * j + 3] += r.w;
-                        }
+                    if (c == kCols / 32 - 1 || o0 + (c + 1) * 32 >= A.e.n_out) {
+                        // the last read: the accumulator may be refilled
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&P.acc_empty[buf]);
                     }
-                    float4* yp = reinterpret_cast<float4*>(static_cast<float*>(A.y) + t * A.ld_y + o);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        yp[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                    finish<32, !kBmn>(A.e, y, v, t0, o0 + c * 32, sy, sz, lane);
                 }
+                if (o0 >= A.e.n_out) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&P.acc_empty[buf]);
+                }
+                ++ci;
             }
-            // the accumulator may be refilled once every epilogue warp has read it
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&acc_empty[buf]);
         }
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 1) tmem_dealloc(tmem, S::kTmemCols);
+    if (warp == 1) tmem_dealloc(P.tmem, S::kTmemCols);
+}
+
+// out (+)= the sum of S partials in order, four elements a thread.
+__global__ void __launch_bounds__(256) linear_join_kernel(const float4* __restrict__ part, int S, int64_t n4, float4* out,
+                                                          int accumulate) {
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n4;
+         i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+        float4 s = accumulate ? out[i] : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+        for (int k = 0; k < S; ++k) {
+            const float4 v = __ldcs(part + static_cast<int64_t>(k) * n4 + i);
+            s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
+        }
+        out[i] = s;
+    }
 }
 
 // ------------------------------------------------------------------ dz and its column sums
@@ -482,42 +706,34 @@ __global__ void __launch_bounds__(256) linear_db_kernel(const float* part, int c
 }
 
 // ------------------------------------------------------------------ host side
-template <int kBN, bool kBmn, int kAct>
+template <int kBN, bool kAmn, bool kBmn, int kTerms, bool kPromote>
 dust_status launch_gemm(const GemmArgs& A, cudaStream_t s) {
+    using S = Shape<kBN, kTerms>;
     static PerContextOnce attr;
     if (!attr.run([] {
-            return cudaFuncSetAttribute(linear_gemm_kernel<kBN, kBmn, kAct>,
+            return cudaFuncSetAttribute(linear_gemm_kernel<kBN, kAmn, kBmn, kTerms, kPromote>,
                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        static_cast<int>(Shape<kBN>::kSmem)) == cudaSuccess;
+                                        static_cast<int>(S::kSmem)) == cudaSuccess;
         }))
         return DUST_ERR_CUDA;
-    const int64_t tiles = static_cast<int64_t>(A.m_tiles) * A.n_tiles;
-    const unsigned grid = static_cast<unsigned>(std::min<int64_t>(tiles, num_sms()));
-    linear_gemm_kernel<kBN, kBmn, kAct><<<grid, kThreads, Shape<kBN>::kSmem, s>>>(A);
+    const int64_t items = static_cast<int64_t>(A.m_tiles) * A.n_tiles * A.splits;
+    const unsigned grid = static_cast<unsigned>(std::min<int64_t>(items, num_sms()));
+    linear_gemm_kernel<kBN, kAmn, kBmn, kTerms, kPromote><<<grid, kThreads, S::kSmem, s>>>(A);
     return DUST_OK;
-}
-
-template <int kBN>
-dust_status launch_fwd(const GemmArgs& A, int act, cudaStream_t s) {
-    switch (act) {
-        case DUST_ACT_RELU: return launch_gemm<kBN, false, DUST_ACT_RELU>(A, s);
-        case DUST_ACT_GELU: return launch_gemm<kBN, false, DUST_ACT_GELU>(A, s);
-        case DUST_ACT_GELU_TANH: return launch_gemm<kBN, false, DUST_ACT_GELU_TANH>(A, s);
-        case DUST_ACT_SILU: return launch_gemm<kBN, false, DUST_ACT_SILU>(A, s);
-    }
-    return launch_gemm<kBN, false, DUST_ACT_NONE>(A, s);
 }
 
 // Output tile width: the one whose waves of tiles over the SMs cost least, a tile of 128 x bn taking
 // about as long as the larger of its MMAs (bn) and its operand loads (bn + 128, at 0.6 each).
-int choose_bn(int64_t m_tiles, int n_out) {
-    int best = 256;
+// The registers of an fp32 output's sums limit its tiles to 128 columns.
+int choose_bn(int64_t m_tiles, int n_out, bool f32) {
+    int best = 0;
     double least = 0;
     for (int bn : {256, 128, 64}) {
+        if (bn == 256 && f32) continue;
         const int64_t tiles = m_tiles * ((n_out + bn - 1) / bn);
         const double cost = static_cast<double>((tiles + num_sms() - 1) / num_sms()) *
                             std::max<double>(bn, 0.6 * (bn + 128));
-        if (bn == 256 || cost < least) {
+        if (best == 0 || cost < least) {
             least = cost;
             best = bn;
         }
@@ -525,18 +741,29 @@ int choose_bn(int64_t m_tiles, int n_out) {
     return best;
 }
 
-// y [M, n_out] = A [terms M, K] B, B K-major [n_out, K] or MN-major [K, n_out].
-dust_status gemm(const void* a, int64_t ld_a, int terms, int64_t M, int K, const void* b, bool b_mn, int n_out,
-                 GemmArgs& G, int act, const char* name, cudaStream_t s) {
+template <bool kBmn, int kTerms, bool kPromote>
+dust_status launch_width(int bn, const GemmArgs& A, cudaStream_t s) {
+    if constexpr (!kPromote)
+        if (bn == 256) return launch_gemm<256, false, kBmn, kTerms, kPromote>(A, s);
+    return bn >= 128 ? launch_gemm<128, false, kBmn, kTerms, kPromote>(A, s)
+                     : launch_gemm<64, false, kBmn, kTerms, kPromote>(A, s);
+}
+
+// y [M, n_out] = A [terms M, K] B with the epilogue of G.e; B K-major [n_out, K] or MN-major [K, n_out].
+dust_status gemm_rows(const void* a, int64_t ld_a, int terms, int K, const void* b, bool b_mn, GemmArgs& G,
+                      const char* name, cudaStream_t s) {
+    const int64_t M = G.e.M;
+    const int n_out = G.e.n_out;
     const int64_t m_tiles = (M + kBM - 1) / kBM;
-    const int bn = choose_bn(m_tiles, n_out);
+    const int bn = choose_bn(m_tiles, n_out, !G.e.out_bf16);
     G.ew = device_error_word();
-    G.M = M;
-    G.n_out = n_out;
+    G.term_rows = M;
+    G.split_elems = 0;
     G.k_blocks = (K + kBK - 1) / kBK;
-    G.terms = terms;
+    G.per_split = G.k_blocks;
+    G.splits = 1;
     G.n_tiles = (n_out + bn - 1) / bn;
-    if (m_tiles * G.n_tiles > 2147483647LL) return DUST_ERR_UNSUPPORTED;
+    if (m_tiles * G.n_tiles > 1 << 30) return DUST_ERR_UNSUPPORTED;
     G.m_tiles = static_cast<int>(m_tiles);
     if (!make_tmap_bf16_2d_ld(&G.ta, a, static_cast<uint64_t>(terms * M), K, ld_a, kBM, kBK)) return DUST_ERR_CUDA;
     if (b_mn ? !make_tmap_bf16_2d_ld(&G.tb, b, K, n_out, n_out, kBK, 64)
@@ -545,13 +772,83 @@ dust_status gemm(const void* a, int64_t ld_a, int terms, int64_t M, int K, const
     prof_begin(s);
     dust_status st;
     if (b_mn)
-        st = bn == 256   ? launch_gemm<256, true, DUST_ACT_NONE>(G, s)
-             : bn == 128 ? launch_gemm<128, true, DUST_ACT_NONE>(G, s)
-                         : launch_gemm<64, true, DUST_ACT_NONE>(G, s);
+        st = G.e.out_bf16 ? launch_width<true, 1, false>(bn, G, s)
+             : terms == 2 ? launch_width<true, 2, true>(bn, G, s)
+                          : launch_width<true, 1, true>(bn, G, s);
     else
-        st = bn == 256 ? launch_fwd<256>(G, act, s) : bn == 128 ? launch_fwd<128>(G, act, s) : launch_fwd<64>(G, act, s);
+        st = G.e.out_bf16 ? launch_width<false, 1, false>(bn, G, s) : launch_width<false, 1, true>(bn, G, s);
     prof_end(s, name);
     return st;
+}
+
+// dW [d_out, d_in] (+)= dz^T x: 128 x 256 tiles, the tokens in as many splits as cost least: the waves of
+// items over the SMs (about 0.45 us a block of 64 tokens and 2 us an item) and, with more than one, the
+// partials written and read back at about 6 GB/ms and one more launch.  The partials are added in order.
+constexpr int kMinBlocks = 4;
+constexpr int kMaxSplits = 64;
+struct DwPlan {
+    int m_tiles, n_tiles, k_blocks, splits, per_split;
+};
+DwPlan dw_plan(int64_t N, int32_t d_in, int32_t d_out) {
+    DwPlan p;
+    p.m_tiles = (d_out + kBM - 1) / kBM;
+    p.n_tiles = (d_in + 255) / 256;
+    p.k_blocks = static_cast<int>((N + kBK - 1) / kBK);
+    const int64_t tiles = static_cast<int64_t>(p.m_tiles) * p.n_tiles;
+    const double bytes = 8.0 * d_out * d_in;
+    int64_t S = 1;
+    double least = 0;
+    for (int64_t k = 1; k <= kMaxSplits && (k == 1 || p.k_blocks / k >= kMinBlocks); ++k) {
+        const double waves = static_cast<double>((tiles * k + num_sms() - 1) / num_sms());
+        const double cost = waves * (0.45 * static_cast<double>((p.k_blocks + k - 1) / k) + 2.0) +
+                            (k > 1 ? 3.0 + k * bytes / 6e6 : 0.0);
+        if (k == 1 || cost < least) {
+            least = cost;
+            S = k;
+        }
+    }
+    p.per_split = static_cast<int>((p.k_blocks + S - 1) / S);
+    p.splits = (p.k_blocks + p.per_split - 1) / p.per_split;  // none of them empty
+    return p;
+}
+size_t dw_bytes(int64_t N, int32_t d_in, int32_t d_out) {
+    const DwPlan p = dw_plan(N, d_in, d_out);
+    return p.splits > 1 ? align_up(static_cast<size_t>(p.splits) * d_out * d_in * 4, 256) : 0;
+}
+dust_status gemm_dw(const void* dz, int64_t ld_dz, int terms, const void* x, int64_t ld_x, int64_t N, int32_t d_in,
+                    int32_t d_out, float* dW, int accumulate, float* part, cudaStream_t s) {
+    const DwPlan p = dw_plan(N, d_in, d_out);
+    GemmArgs G{};
+    G.e.M = d_out;
+    G.e.n_out = d_in;
+    G.e.y = p.splits > 1 ? part : dW;
+    G.e.ld_y = d_in;
+    G.e.res = p.splits == 1 && accumulate ? dW : nullptr;
+    G.e.ld_res = d_in;
+    G.ew = device_error_word();
+    G.term_rows = N;
+    G.split_elems = static_cast<int64_t>(d_out) * d_in;
+    G.k_blocks = p.k_blocks;
+    G.per_split = p.per_split;
+    G.splits = p.splits;
+    G.m_tiles = p.m_tiles;
+    G.n_tiles = p.n_tiles;
+    if (static_cast<int64_t>(p.m_tiles) * p.n_tiles * p.splits > 1 << 30) return DUST_ERR_UNSUPPORTED;
+    if (!make_tmap_bf16_2d_ld(&G.ta, dz, static_cast<uint64_t>(terms * N), d_out, ld_dz, kBK, 64) ||
+        !make_tmap_bf16_2d_ld(&G.tb, x, static_cast<uint64_t>(N), d_in, ld_x, kBK, 64))
+        return DUST_ERR_CUDA;
+    prof_begin(s);
+    const dust_status st = terms == 2 ? launch_gemm<256, true, true, 2, true>(G, s)
+                                      : launch_gemm<256, true, true, 1, true>(G, s);
+    prof_end(s, "linear_dw_tcgen05");
+    if (st != DUST_OK || p.splits == 1) return st;
+    const int64_t n4 = G.split_elems / 4;
+    prof_begin(s);
+    linear_join_kernel<<<static_cast<unsigned>(std::min<int64_t>((n4 + 255) / 256, static_cast<int64_t>(num_sms()) * 16)),
+                         256, 0, s>>>(reinterpret_cast<const float4*>(part), p.splits, n4,
+                                      reinterpret_cast<float4*>(dW), accumulate);
+    prof_end(s, "linear_dw_join");
+    return DUST_OK;
 }
 
 template <typename T>
@@ -608,21 +905,14 @@ dust_status linear_launch(const void* x, int64_t ld_x, const void* W, const floa
         return cudaGetLastError() == cudaSuccess ? DUST_OK : DUST_ERR_CUDA;
     }
     GemmArgs G{};
-    G.bias = bias;
-    G.res = res;
-    G.y = y;
-    G.z = static_cast<__nv_bfloat16*>(z);
-    G.ld_res = ld_res;
-    G.ld_y = ld_y;
-    G.ld_z = ld_z;
-    G.out_bf16 = out_bf16;
-    const dust_status st = gemm(x, ld_x, 1, N, d_in, W, false, d_out, G, act, "linear_tcgen05", s);
+    G.e = Epilogue{bias, res, y, static_cast<__nv_bfloat16*>(z), N, ld_res, ld_y, ld_z, d_out, act, out_bf16};
+    const dust_status st = gemm_rows(x, ld_x, 1, d_in, W, false, G, "linear_tcgen05", s);
     if (st != DUST_OK) return st;
     return cudaGetLastError() == cudaSuccess ? DUST_OK : DUST_ERR_CUDA;
 }
 
 size_t linear_backward_workspace_bytes(int64_t N, int32_t d_in, int32_t d_out) {
-    return dz_bytes(N, d_out) + db_bytes(N, d_out) + contract_workspace_bytes(N, d_in, d_out);
+    return dz_bytes(N, d_out) + db_bytes(N, d_out) + dw_bytes(N, d_in, d_out);
 }
 
 dust_status linear_backward_launch(const void* dy, int dy_bf16, int64_t ld_dy, const void* z, int64_t ld_z,
@@ -632,7 +922,7 @@ dust_status linear_backward_launch(const void* dy, int dy_bf16, int64_t ld_dy, c
     char* w = static_cast<char*>(ws);
     __nv_bfloat16* hi = reinterpret_cast<__nv_bfloat16*>(w);
     float* part = reinterpret_cast<float*>(w + dz_bytes(N, d_out));
-    void* split = w + dz_bytes(N, d_out) + db_bytes(N, d_out);
+    float* split = reinterpret_cast<float*>(w + dz_bytes(N, d_out) + db_bytes(N, d_out));
     // without an activation a bf16 dy is the operand itself, exactly, in one term
     const bool direct = act == DUST_ACT_NONE && dy_bf16;
     const bool products = dx || dW;
@@ -661,16 +951,17 @@ dust_status linear_backward_launch(const void* dy, int dy_bf16, int64_t ld_dy, c
     const int64_t ld_op = direct ? ld_dy : d_out;
     if (dx) {
         GemmArgs G{};
-        G.y = dx;
-        G.ld_y = ld_dx;
-        G.out_bf16 = dx_bf16;
+        G.e.M = N;
+        G.e.n_out = d_in;
+        G.e.y = dx;
+        G.e.ld_y = ld_dx;
+        G.e.out_bf16 = dx_bf16;
         // a bf16 dx is rounded as coarsely as one term of dz; an fp32 dx takes both terms
-        const dust_status st = gemm(op, ld_op, dx_bf16 ? 1 : terms, N, d_out, W, true, d_in, G, DUST_ACT_NONE,
-                                    "linear_dx_tcgen05", s);
+        const dust_status st = gemm_rows(op, ld_op, dx_bf16 ? 1 : terms, d_out, W, true, G, "linear_dx_tcgen05", s);
         if (st != DUST_OK) return st;
     }
     if (dW) {
-        const dust_status st = contract_launch(op, ld_op, terms, x, ld_x, N, d_in, d_out, dW, accumulate, split, s);
+        const dust_status st = gemm_dw(op, ld_op, terms, x, ld_x, N, d_in, d_out, dW, accumulate, split, s);
         if (st != DUST_OK) return st;
     }
     return cudaGetLastError() == cudaSuccess ? DUST_OK : DUST_ERR_CUDA;

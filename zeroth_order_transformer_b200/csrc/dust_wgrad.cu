@@ -562,62 +562,6 @@ dust_status launch_bf16_tables(const WgradLayerArgs* layers, int n, int64_t N, i
 
 }  // namespace
 
-// The contraction alone, g already an operand: out (+)= g^T x with g [terms N, d_out] (hi rows, then lo
-// rows) of row stride ld_g and x [N, d_in] of row stride ld_x, the token sum split as in the estimator.
-size_t contract_workspace_bytes(int64_t N, int32_t d_in, int32_t d_out) {
-    const int S = choose_splits(gw_tiles(d_in, d_out), N);
-    return S > 1 ? align_up(static_cast<size_t>(S) * d_out * d_in * 4, 256) : 0;
-}
-
-dust_status contract_launch(const void* g, int64_t ld_g, int terms, const void* x, int64_t ld_x, int64_t N,
-                            int32_t d_in, int32_t d_out, float* out, int accumulate, void* ws, cudaStream_t s) {
-    const int64_t tiles = gw_tiles(d_in, d_out);
-    const int S = choose_splits(tiles, N);
-    const int64_t nkb = (N + kGK - 1) / kGK;
-    GwTable<1> W;
-    W.opt = OptParams{};
-    W.ew = device_error_word();
-    W.N = N;
-    W.n_layers = 1;
-    const uint32_t box = terms == 2 ? GwShape<2>::kK : GwShape<1>::kK;
-    if (!make_tmap_bf16_2d_ld(&W.tmg[0], g, static_cast<uint64_t>(terms * N), d_out, ld_g, box, 64) ||
-        !make_tmap_bf16_2d_ld(&W.tmx[0], x, static_cast<uint64_t>(N), d_in, ld_x, box, 64))
-        return DUST_ERR_CUDA;
-    GwLayer& L = W.layer[0];
-    L.o_tiles = (d_out + kGM - 1) / kGM;
-    L.k_tiles = (d_in + kGN - 1) / kGN;
-    L.splits = S;
-    L.tokens_per_split = ((nkb + S - 1) / S) * kGK;
-    L.d_in = d_in;
-    L.d_out = d_out;
-    L.tile_begin = 0;
-    L.opt = OptTargets{};
-    L.out = S == 1 ? out : static_cast<float*>(ws);
-    L.accumulate = S == 1 ? accumulate : 0;
-    if (tiles * S > 2147483647LL) return DUST_ERR_UNSUPPORTED;
-    prof_begin(s);
-    const dust_status st = terms == 2 ? launch_gw<1, 2>(W, tiles * S, s) : launch_gw<1, 1>(W, tiles * S, s);
-    prof_end(s, "gw_bf16_tcgen05");
-    if (st != DUST_OK) return st;
-    if (S > 1) {
-        SplitTable<1> R;
-        R.opt = W.opt;
-        SplitLayer& Rl = R.layer[0];
-        Rl.part = reinterpret_cast<const float4*>(L.out);
-        Rl.out = reinterpret_cast<float4*>(out);
-        Rl.opt = OptTargets{};
-        Rl.n4 = static_cast<int64_t>(d_out) * d_in / 4;
-        Rl.S = S;
-        Rl.accumulate = accumulate;
-        const unsigned bx = static_cast<unsigned>(
-            std::min<int64_t>((Rl.n4 + 255) / 256, static_cast<int64_t>(num_sms()) * kGCtasPerSm));
-        prof_begin(s);
-        splitk_reduce_kernel<1><<<dim3(bx, 1), 256, 0, s>>>(R);
-        prof_end(s, "gw_splitk_reduce");
-    }
-    return cudaGetLastError() == cudaSuccess ? DUST_OK : DUST_ERR_CUDA;
-}
-
 size_t wgrad_workspace_bytes(dust_dtype dt, int64_t N, int32_t d_in, int32_t d_out) {
     if (dt == DUST_BF16) return bf16_layer_ws(N, d_in, d_out, choose_splits(gw_tiles(d_in, d_out), N));
     return align_up(static_cast<size_t>(N) * d_out * 4, 256);
