@@ -111,6 +111,14 @@ def test_few_tokens(z, N, d_in, d_out):
     fwd_case(z, N, d_in, d_out, ACTS[k % 5], bool(k & 1), bool(k & 2), bool(k & 4), ["bf16", "f32"][(k >> 1) & 1], k)
 
 
+@pytest.mark.parametrize("N,d_in,d_out", [(9, 128, 64), (24, 2048, 512), (128, 4112, 80), (129, 784, 336), (100, 64, 4112), (17, 320, 1040),
+                                          (300, 1552, 16)])
+def test_contraction_over_a_cluster(z, N, d_in, d_out):
+    """Few output tiles and contractions of one to many blocks, shares that are short or empty among them."""
+    for k, out in enumerate(("bf16", "f32")):
+        fwd_case(z, N, d_in, d_out, ACTS[(N + k) % 5], True, bool((N + k) & 1), True, out, N + k, ld_extra=8 * k)
+
+
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("out", ["bf16", "f32"])
 def test_activations(z, act, out):

@@ -3,7 +3,7 @@
 //   z = x W^T + b,  y = act(z) + residual
 //   dz = dy act'(z),  db = sum_t dz_t,  dW = dz^T x,  dx = dz W
 //
-// Two forms of the product:
+// Three forms of the product:
 //   linear_rows_kernel    few tokens (one sequence being extended): bound by reading W once.  A warp
 //                         holds four output rows of W against every token, 16 bytes a lane; where
 //                         there are few output rows the warps of a CTA split the contraction.
@@ -11,6 +11,8 @@
 //                         thread issues the MMAs of a 128-row tile into one of two accumulators in
 //                         tensor memory, eight warps run the epilogue of the previous tile from the other.
 //                         The forward product, dx and dW differ in which operands are MN-major.
+//   linear_cluster_kernel the same pipeline for outputs of few tiles, the contraction cut over the CTAs of a
+//                         cluster and joined through distributed shared memory.
 // dz is formed once (linear_dz_kernel) as a bf16 operand, or as hi + lo bf16 terms (dz = hi + lo to
 // about 16 bits), with the column sums for db on the way.
 #include <algorithm>
@@ -205,19 +207,21 @@ constexpr int kBK = 64;
 constexpr int kThreads = 320;  // TMA warp, MMA warp, eight epilogue warps
 constexpr uint32_t kABytes = kBM * kBK * 2;
 constexpr uint32_t kBox = kBK * 128;          // a 64-row x 64-element box of an MN-major operand
-constexpr uint32_t kStaging = 8 * 2 * 2048;   // each epilogue warp: 32 rows x 64 bytes of y and of z
+// Each epilogue warp: 32 rows x 64 bytes of y and of z, and the biases of 32 columns.
+constexpr uint32_t kWarpStaging = 2 * 2048;
+constexpr uint32_t kStaging = 8 * (kWarpStaging + 128);
 // The tensor cores truncate as they add to the accumulator: a sum of K products is off by about K 1.1e-9 of
 // its size toward zero (measured: 4.7e-7 at K = 512, 9.1e-6 at K = 8192).  An fp32 output is therefore collected
-// in registers, rounded to nearest, after every 16 blocks (1024 products) in the accumulator; a bf16 output's own
+// in registers, rounded to nearest, after every 8 blocks (512 products) in the accumulator; a bf16 output's own
 // rounding is 200 times the largest error of K = 8192, and it is not.
-constexpr int kFlush = 16;
+constexpr int kFlush = 8;
 
 template <int kBN, int kTerms>
 struct Shape {
     static constexpr uint32_t kBBytes = kBN * kBK * 2;
     static constexpr uint32_t kStageBytes = kTerms * kABytes + kBBytes;
     static constexpr int kStages = static_cast<int>(192 * 1024 / kStageBytes);
-    static constexpr uint32_t kSmem = kStages * kStageBytes + kStaging + 1024 + 512;
+    static constexpr uint32_t kSmem = kStages * kStageBytes + kStaging + 1024 + 256;
     static constexpr uint32_t kTmemCols = 2 * kBN;
 };
 static_assert(Shape<256, 1>::kSmem <= 227 * 1024 && Shape<256, 2>::kSmem <= 227 * 1024, "exceeds shared memory");
@@ -375,23 +379,24 @@ __device__ __forceinline__ void rows_in(uint8_t* buf, const void* base, int64_t 
 }
 
 // Bias, pre-activation, activation, residual and store of kN columns from o of the warp's rows t0 .. + 31 (lane:
-// row).  kN = 32 for a bf16 y, 16 for an fp32 one: 64 bytes of a row.  kLayer false: no bias, z or activation.
+// row), chunk c of the warp's columns; bias: those of its columns 4 lane .. + 3.  kN = 32 for a bf16 y, 16 for an fp32 one: 64 bytes of a row.  kLayer false: no bias, z or activation.
 // All lanes call it.
 template <int kN, bool kLayer>
 __device__ __forceinline__ void finish(const Epilogue& E, void* y, float (&v)[kN], int64_t t0, int o, uint8_t* sy,
-                                       uint8_t* sz, int lane) {
+                                       uint8_t* sz, float4* sb, float4 bias, int c, int lane) {
     constexpr int kEs = 64 / kN;  // bytes of an element of y
     if (E.res) rows_in(sy, E.res, t0, E.M, E.ld_res * kEs, static_cast<int64_t>(o) * kEs, static_cast<int64_t>(E.n_out) * kEs, lane);
     if (kLayer && E.bias) {
+        if (lane / (kN / 4) == c) sb[lane % (kN / 4)] = bias;
+        __syncwarp();
 #pragma unroll
-        for (int j = 0; j < kN / 4; ++j)
-            if (o + 4 * j < E.n_out) {
-                const float4 b = __ldg(reinterpret_cast<const float4*>(E.bias + o) + j);
-                v[4 * j] += b.x;
-                v[4 * j + 1] += b.y;
-                v[4 * j + 2] += b.z;
-                v[4 * j + 3] += b.w;
-            }
+        for (int j = 0; j < kN / 4; ++j) {
+            const float4 b = sb[j];
+            v[4 * j] += b.x;
+            v[4 * j + 1] += b.y;
+            v[4 * j + 2] += b.z;
+            v[4 * j + 3] += b.w;
+        }
     }
     if (kLayer && E.z) {
         uint32_t w[kN / 2];
@@ -460,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_c
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int tiles = A.m_tiles * A.n_tiles;
     const int items = tiles * A.splits;
-    constexpr int kChunk = kPromote ? kFlush / kTerms : 1 << 30;
+    constexpr int kChunk = kPromote ? kFlush : 1 << 30;
 
     if (warp == 0) {
         if (lane == 0) {
@@ -500,10 +505,16 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_c
         // epilogue warps 2 .. 9: tensor-memory lane quarter warp % 4 (32 rows), column half hf
         const int q = warp & 3;
         const int hf = (warp - 2) >> 2;
-        uint8_t* sy = P.staging + (warp - 2) * 4096;
+        uint8_t* sy = P.staging + (warp - 2) * kWarpStaging;
         uint8_t* sz = sy + 2048;
+        float4* sb = reinterpret_cast<float4*>(P.staging + 8 * kWarpStaging) + (warp - 2) * 8;
         constexpr int kCols = kBN / 2;
         const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
+        auto release = [&](uint32_t buf) {  // the warp has read its part of the accumulator: it may be refilled
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&P.acc_empty[buf]);
+        };
         uint32_t ci = 0;
         bool ok = true;
         for (int it = blockIdx.x; it < items && ok; it += gridDim.x) {
@@ -514,6 +525,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_c
             const int64_t t0 = static_cast<int64_t>(m) * kBM + q * 32;
             const int o0 = n * kBN + hf * kCols;
             void* y = static_cast<uint8_t*>(A.e.y) + split * A.split_elems * (A.e.out_bf16 ? 2 : 4);
+            float4 bias = make_float4(0.f, 0.f, 0.f, 0.f);  // on its way before the wait for the tile
+            if (!kBmn && A.e.bias && 4 * lane < kCols && o0 + 4 * lane < A.e.n_out)
+                bias = __ldg(reinterpret_cast<const float4*>(A.e.bias + o0) + lane);
             if (kPromote) {
                 float acc[kCols];
 #pragma unroll
@@ -535,9 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_c
 #pragma unroll
                         for (int j = 0; j < 16; ++j) acc[c * 16 + j] += v[j];
                     }
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&P.acc_empty[buf]);
+                    release(buf);
                 }
                 if (!ok) break;
 #pragma unroll
@@ -546,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_c
                         float v[16];
 #pragma unroll
                         for (int j = 0; j < 16; ++j) v[j] = acc[c * 16 + j];
-                        finish<16, !kBmn>(A.e, y, v, t0, o0 + c * 16, sy, sz, lane);
+                        finish<16, !kBmn>(A.e, y, v, t0, o0 + c * 16, sy, sz, sb, bias, c, lane);
                     }
                 }
             } else {
@@ -555,32 +567,27 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_c
                 __syncwarp();
                 tc_fence_after();
                 const uint32_t trow = P.tmem + buf * kBN + hf * kCols + lane_base;
+                const int left = A.e.n_out - o0;
+                const int cnt = left <= 0 ? 0 : min(kCols, left + 31) / 32;  // chunks of 32 columns
+                float next[32];
+                if (cnt > 0) {
+                    tmem_ld32(trow, next);
+                    tmem_wait_ld32(next);
+                }
 #pragma unroll 1
-                for (int c = 0; c < kCols / 32; ++c) {
-                    if (o0 + c * 32 >= A.e.n_out) break;  // uniform over the warp
+                for (int c = 0; c < cnt; ++c) {
                     float v[32];
-                    float a[16], b[16];
-                    tmem_ld16(trow + c * 32, a);
-                    tmem_ld16(trow + c * 32 + 16, b);
-                    tmem_wait_ld();
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        v[j] = a[j];
-                        v[16 + j] = b[j];
+                    for (int j = 0; j < 32; ++j) v[j] = next[j];
+                    if (c + 1 < cnt) {
+                        tmem_ld32(trow + (c + 1) * 32, next);  // on its way while this chunk is worked on
+                    } else {
+                        release(buf);
                     }
-                    if (c == kCols / 32 - 1 || o0 + (c + 1) * 32 >= A.e.n_out) {
-                        // the last read: the accumulator may be refilled
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&P.acc_empty[buf]);
-                    }
-                    finish<32, !kBmn>(A.e, y, v, t0, o0 + c * 32, sy, sz, lane);
+                    finish<32, !kBmn>(A.e, y, v, t0, o0 + c * 32, sy, sz, sb, bias, c, lane);
+                    if (c + 1 < cnt) tmem_wait_ld32(next);
                 }
-                if (o0 >= A.e.n_out) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&P.acc_empty[buf]);
-                }
+                if (cnt == 0) release(buf);
                 ++ci;
             }
         }
@@ -589,6 +596,129 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_c
     __syncthreads();
     if (warp == 1) tmem_dealloc(P.tmem, S::kTmemCols);
 }
+
+// Few tiles: 128 x 64 tiles whose contraction is cut over the CTAs of a cluster.  Each CTA sums its share as
+// the persistent kernel does, sends its sums to the CTAs that own their columns (64 / S of them each) through
+// distributed shared memory, and each owner adds the S shares in rank order and runs the epilogue.
+constexpr int kCBN = 64;
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+
+__global__ void __launch_bounds__(kThreads, 1) linear_cluster_kernel(const __grid_constant__ GemmArgs A) {
+    using S = Shape<kCBN, 1>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~static_cast<uintptr_t>(1023));
+    const Pipe P = pipe_setup<kCBN, 1>(smem, 8);
+    cluster_arrive();  // waited for before the first remote store: the peers are running by then
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int ranks = A.splits, rank = static_cast<int>(blockIdx.x) % ranks;
+    const int n0 = static_cast<int>(blockIdx.x) / ranks * kCBN;
+    const int m0 = static_cast<int>(blockIdx.y) * kBM;
+    const int kb0 = min(A.k_blocks, rank * A.per_split), kb1 = min(A.k_blocks, kb0 + A.per_split);
+    const int w = kCBN / ranks;  // columns that a rank owns: 8, 16, 32 or 64
+    float acc[kCBN / 2];
+    if (warp == 0) {
+        if (lane == 0) {
+            prefetch_tensormap(&A.ta);
+            prefetch_tensormap(&A.tb);
+            uint32_t kc = 0;
+            pipe_load<kCBN, false, false, 1>(A, P, m0, n0, kb0, kb1, kc);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            uint32_t kc = 0, ci = 0;
+            bool ok = true;
+            for (int k = kb0; k < kb1 && ok; k += kFlush, ++ci) {
+                const uint32_t buf = ci & 1;
+                if (ci >= 2 && !mbar_wait_bounded(&P.acc_empty[buf], ((ci >> 1) - 1) & 1, A.ew, 513)) break;
+                tc_fence_after();
+                ok = pipe_mma<kCBN, false, false, 1>(A, P, P.tmem + buf * kCBN, k, min(kb1, k + kFlush), kc);
+                umma_commit(&P.acc_full[buf]);
+            }
+        }
+    } else {
+        const int q = warp & 3, hf = (warp - 2) >> 2;
+#pragma unroll
+        for (int j = 0; j < kCBN / 2; ++j) acc[j] = 0.f;
+        uint32_t ci = 0;
+        for (int k = kb0; k < kb1; k += kFlush, ++ci) {
+            const uint32_t buf = ci & 1;
+            if (!mbar_wait_bounded(&P.acc_full[buf], (ci >> 1) & 1, A.ew, 514)) break;
+            __syncwarp();
+            tc_fence_after();
+            float v[32];
+            tmem_ld32(P.tmem + buf * kCBN + hf * 32 + (static_cast<uint32_t>(q * 32) << 16), v);
+            tmem_wait_ld32(v);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) acc[j] += v[j];
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&P.acc_empty[buf]);
+        }
+    }
+    __syncwarp();
+    cluster_wait();
+    if (warp >= 2) {
+        const int q = warp & 3, hf = (warp - 2) >> 2;
+        const int row = q * 32 + lane;
+        if (m0 + row < A.e.M) {
+            const uint32_t mine = smem_u32(P.staging);
+#pragma unroll
+            for (int j = 0; j < 32; j += 4) {
+                const int col = hf * 32 + j, owner = col / w;
+                const uint32_t at = mine + static_cast<uint32_t>((rank * kBM + row) * w + (col - owner * w)) * 4u;
+                uint32_t remote;
+                asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(at), "r"(owner));
+                asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(remote), "f"(acc[j]),
+                             "f"(acc[j + 1]), "f"(acc[j + 2]), "f"(acc[j + 3])
+                             : "memory");
+            }
+        }
+    }
+    cluster_arrive();
+    cluster_wait();
+    // this CTA's columns n0 + rank w .. + w - 1 of the tile's rows, four columns a thread
+    const float* part = reinterpret_cast<const float*>(P.staging);
+    const int rows = static_cast<int>(min(static_cast<int64_t>(kBM), A.e.M - m0)), quads = w / 4;
+    for (int e = threadIdx.x; e < rows * quads; e += kThreads) {
+        const int row = e / quads, c = 4 * (e - row * quads);
+        const int o = n0 + rank * w + c;
+        if (o >= A.e.n_out) continue;  // n_out is a multiple of 16
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = 0; k < ranks; ++k) {
+            const float4 v = *reinterpret_cast<const float4*>(part + (k * kBM + row) * w + c);
+            a = make_float4(a.x + v.x, a.y + v.y, a.z + v.z, a.w + v.w);
+        }
+        const int64_t t = m0 + row;
+        if (A.e.bias) {
+            const float4 b = __ldg(reinterpret_cast<const float4*>(A.e.bias + o));
+            a = make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+        }
+        if (A.e.z)
+            *reinterpret_cast<uint2*>(A.e.z + t * A.e.ld_z + o) = make_uint2(pack2(a.x, a.y), pack2(a.z, a.w));
+        float v[4] = {a.x, a.y, a.z, a.w};
+        act_block(A.e.act, v);
+        if (A.e.out_bf16) {
+            if (A.e.res) {
+                const uint2 r = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(A.e.res) + t * A.e.ld_res + o);
+                v[0] += bf_lo(r.x), v[1] += bf_hi(r.x), v[2] += bf_lo(r.y), v[3] += bf_hi(r.y);
+            }
+            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(A.e.y) + t * A.e.ld_y + o) =
+                make_uint2(pack2(v[0], v[1]), pack2(v[2], v[3]));
+        } else {
+            if (A.e.res) {
+                const float4 r = *reinterpret_cast<const float4*>(static_cast<const float*>(A.e.res) + t * A.e.ld_res + o);
+                v[0] += r.x, v[1] += r.y, v[2] += r.z, v[3] += r.w;
+            }
+            *reinterpret_cast<float4*>(static_cast<float*>(A.e.y) + t * A.e.ld_y + o) = make_float4(v[0], v[1], v[2], v[3]);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) tmem_dealloc(P.tmem, S::kTmemCols);
+}
+static_assert(kBM * kCBN * 4 <= kStaging, "the shares of one owner");
 
 // out (+)= the sum of S partials in order, four elements a thread.
 __global__ void __launch_bounds__(256) linear_join_kernel(const float4* __restrict__ part, int S, int64_t n4, float4* out,
@@ -609,7 +739,13 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const float4* __restri
 constexpr int kDThreads = 256;
 constexpr int kDWarps = kDThreads / 32;
 constexpr int kDCols = 256;  // 32 lanes x 8 columns
-constexpr int kDRows = 256;  // rows of one partial sum
+// Rows of one partial sum: 256, fewer (down to 32) while there are fewer than six CTAs an SM.
+int dz_rows(int64_t N, int32_t d_out) {
+    int rows = 256;
+    while (rows > 32 && (N + rows - 1) / rows * ((d_out + kDCols - 1) / kDCols) < static_cast<int64_t>(num_sms()) * 6)
+        rows /= 2;
+    return rows;
+}
 
 struct DzArgs {
     const void* dy;
@@ -618,7 +754,7 @@ struct DzArgs {
     __nv_bfloat16* lo;  // [N, d_out], or null
     float* part;        // [row chunks, d_out] column sums, or null
     int64_t N, ld_dy, ld_z;
-    int d_out;
+    int d_out, rows;
 };
 
 template <typename T, int kAct>
@@ -626,8 +762,8 @@ __global__ void __launch_bounds__(kDThreads) linear_dz_kernel(const __grid_const
     __shared__ float sh[kDWarps][kDCols + 8];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int col = blockIdx.x * kDCols + lane * 8;
-    const int64_t r0 = static_cast<int64_t>(blockIdx.y) * kDRows;
-    const int64_t r1 = min(A.N, r0 + kDRows);
+    const int64_t r0 = static_cast<int64_t>(blockIdx.y) * A.rows;
+    const int64_t r1 = min(A.N, r0 + A.rows);
     float s[8] = {};
     if (col < A.d_out) {
 #pragma unroll 2
@@ -749,13 +885,46 @@ dust_status launch_width(int bn, const GemmArgs& A, cudaStream_t s) {
                      : launch_gemm<64, false, kBmn, kTerms, kPromote>(A, s);
 }
 
+// Ranks that share a tile's contraction: while the tiles fill at most half of the SMs and each rank keeps
+// two blocks of 64.  0: there are tiles enough without.
+int cluster_ranks(int64_t tiles, int k_blocks) {
+    if (tiles * 2 > num_sms()) return 0;
+    int r = 1;
+    while (r < 8 && tiles * r * 2 <= num_sms() && k_blocks >= 4 * r) r *= 2;
+    return r;
+}
+
+dust_status launch_cluster(const GemmArgs& A, cudaStream_t s) {
+    using S = Shape<kCBN, 1>;
+    static PerContextOnce attr;
+    if (!attr.run([] {
+            return cudaFuncSetAttribute(linear_cluster_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        static_cast<int>(S::kSmem)) == cudaSuccess;
+        }))
+        return DUST_ERR_CUDA;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = static_cast<unsigned>(A.splits);
+    at.val.clusterDim.y = 1;
+    at.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(A.n_tiles * A.splits), static_cast<unsigned>(A.m_tiles), 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = S::kSmem;
+    cfg.stream = s;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, linear_cluster_kernel, A) == cudaSuccess ? DUST_OK : DUST_ERR_CUDA;
+}
+
 // y [M, n_out] = A [terms M, K] B with the epilogue of G.e; B K-major [n_out, K] or MN-major [K, n_out].
 dust_status gemm_rows(const void* a, int64_t ld_a, int terms, int K, const void* b, bool b_mn, GemmArgs& G,
                       const char* name, cudaStream_t s) {
     const int64_t M = G.e.M;
     const int n_out = G.e.n_out;
     const int64_t m_tiles = (M + kBM - 1) / kBM;
-    const int bn = choose_bn(m_tiles, n_out, !G.e.out_bf16);
+    const int ranks = b_mn ? 0 : cluster_ranks(m_tiles * ((n_out + kCBN - 1) / kCBN), (K + kBK - 1) / kBK);
+    const int bn = ranks ? kCBN : choose_bn(m_tiles, n_out, !G.e.out_bf16);
     G.ew = device_error_word();
     G.term_rows = M;
     G.split_elems = 0;
@@ -771,7 +940,11 @@ dust_status gemm_rows(const void* a, int64_t ld_a, int terms, int K, const void*
         return DUST_ERR_CUDA;
     prof_begin(s);
     dust_status st;
-    if (b_mn)
+    if (ranks) {
+        G.splits = ranks;
+        G.per_split = (G.k_blocks + ranks - 1) / ranks;
+        st = launch_cluster(G, s);
+    } else if (b_mn)
         st = G.e.out_bf16 ? launch_width<true, 1, false>(bn, G, s)
              : terms == 2 ? launch_width<true, 2, true>(bn, G, s)
                           : launch_width<true, 1, true>(bn, G, s);
@@ -864,7 +1037,8 @@ void launch_dz(const DzArgs& A, int act, dim3 grid, cudaStream_t s) {
 
 size_t dz_bytes(int64_t N, int32_t d_out) { return align_up(static_cast<size_t>(2 * N) * d_out * 2, 256); }
 size_t db_bytes(int64_t N, int32_t d_out) {
-    return align_up(static_cast<size_t>((N + kDRows - 1) / kDRows) * d_out * 4, 256);
+    const int rows = dz_rows(N, d_out);
+    return align_up(static_cast<size_t>((N + rows - 1) / rows) * d_out * 4, 256);
 }
 
 // Tokens up to which W is streamed through the CUDA cores.
@@ -928,8 +1102,8 @@ dust_status linear_backward_launch(const void* dy, int dy_bf16, int64_t ld_dy, c
     const bool products = dx || dW;
     if (direct) terms = 1;
     if (db || (products && !direct)) {
-        const int chunks = static_cast<int>((N + kDRows - 1) / kDRows);
-        DzArgs A{dy, static_cast<const __nv_bfloat16*>(z), nullptr, nullptr, db ? part : nullptr, N, ld_dy, ld_z, d_out};
+        const int rows = dz_rows(N, d_out), chunks = static_cast<int>((N + rows - 1) / rows);
+        DzArgs A{dy, static_cast<const __nv_bfloat16*>(z), nullptr, nullptr, db ? part : nullptr, N, ld_dy, ld_z, d_out, rows};
         if (products && !direct) {
             A.hi = hi;
             A.lo = terms == 2 ? hi + N * d_out : nullptr;
