@@ -72,8 +72,8 @@ def _egrad(**kw):
 @pytest.mark.parametrize("kw,code", [
     (dict(ids=None), 1), (dict(g=None), 1), (dict(G=None), 1), (dict(N=0), 1), (dict(V=-1), 1), (dict(d=0), 1),
     (dict(g=P + 8), 1), (dict(G=P + 8), 1), (dict(ld=56), 1), (dict(ld=62), 1), (dict(ld_G=61), 1), (dict(dt=3), 1),
-    (dict(dt=z.DUST_BF16, ld=60), 1), (dict(V=2147483647), 2), (dict(N=1 << 31), 2), (dict(ws=None), 5),
-    (dict(nb=64), 5),
+    (dict(dt=z.DUST_BF16, ld=60), 1), (dict(V=2147483647), 2), (dict(N=1 << 31), 2), (dict(N=5000, ws=None), 5),
+    (dict(N=5000, nb=64), 5),
 ])
 def test_embedding_grad_refuses(kw, code):
     assert _egrad(**kw) == code
@@ -117,7 +117,8 @@ def test_workspace_sizes():
     assert lb(2000, 64, 128) > lb(1000, 64, 128)
     assert lb(10, 0, 128) == 0
     eg = lambda N, V, d: z.dust_workspace_size(z.DUST_OP_EMBEDDING_GRAD, z.DUST_F32, N, V, d, 0)  # noqa: E731
-    assert eg(1, 1, 1) > 0 and eg(100000, 50, 64) >= 4 * 4 * 100000
+    assert eg(4096, 1, 1) == 0 and eg(4097, 1, 1) > 0  # up to 4096 tokens are sorted in shared memory
+    assert eg(100000, 50, 64) >= 4 * 4 * 100000
     assert eg(10, 10, 0) == 0
 
 

@@ -533,59 +533,59 @@ def dust_weight_grad_step(r, x, d_out: int, K_total: int, sigma: float, key: Noi
 
 # ------------------------------------------------------------------ around the estimator
 
-def _raw_stream(device) -> int:
-    """The handle of the current stream (without the Stream object around it, 3 us of host time)."""
-    return _torch()._C._cuda_getCurrentRawStream(device.index)
+def _raw_stream(index: int) -> int:
+    """The handle of the device's current stream (without the Stream object around it, 3 us of host time)."""
+    return _torch()._C._cuda_getCurrentRawStream(index)
 
 
-class _NoScope:
-    def __enter__(self):
-        return None
-
-    def __exit__(self, *exc):
-        return False
-
-
-_NO_SCOPE = _NoScope()
-
-
-def _scope(device, stream):
-    """What a call runs under: its tensors' device, and its stream, so that outputs and workspaces
-    that the call allocates belong to the stream that uses them."""
+def _scope(index: int, stream):
+    """What a call has to run under: its tensors' device, and its stream, so that outputs and workspaces
+    that the call allocates belong to the stream that uses them.  None if it is current already."""
     torch = _torch()
+    if index < 0:
+        raise ValueError("the tensors must be CUDA tensors")
     if stream is not None:
-        if stream.device != device:
-            raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
+        if stream.device.index != index:
+            raise ValueError(f"stream is on {stream.device}, the tensors are on cuda:{index}")
         return torch.cuda.stream(stream)
-    if device.index != torch.cuda.current_device():
-        return torch.cuda.device(device)
-    return _NO_SCOPE
+    if index != torch.cuda.current_device():
+        return torch.cuda.device(index)
+    return None
 
 
-def _rows(t, name: str, rows: int, cols: int, device, dtypes) -> int:
+def _rows(t, name: str, rows: int, cols: int, index: int, dtypes) -> int:
     """Checks a CUDA matrix [rows, cols] with contiguous rows and returns its row stride."""
-    if t.device != device or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor on {device}")
+    if t.get_device() != index or index < 0:
+        raise ValueError(f"{name} must be a CUDA tensor on cuda:{index}")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be one of {dtypes}, not {t.dtype}")
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols or (cols > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name} must be [{rows}, {cols}] with contiguous rows, got {tuple(t.shape)}, "
-                         f"strides {t.stride()}")
-    return t.stride(0) if rows > 1 else -(-cols // 8) * 8
+    shape, strides = t.shape, t.stride()
+    if shape != (rows, cols) or (cols > 1 and strides[1] != 1):
+        raise ValueError(f"{name} must be [{rows}, {cols}] with contiguous rows, got {tuple(shape)}, "
+                         f"strides {strides}")
+    return strides[0] if rows > 1 else -(-cols // 8) * 8
 
 
-def _flat(t, name: str, n: int, device, dtype):
-    if t.device != device or not t.is_cuda or t.dtype != dtype or t.numel() != n or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of {n} elements on {device}")
+def _flat(t, name: str, n: int, index: int, dtype):
+    if t.get_device() != index or index < 0 or t.dtype != dtype or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of {n} elements on cuda:{index}")
     return t
 
 
-def _new_rows(rows: int, cols: int, dtype, device, vec: int):
+def _new_rows(like, rows: int, cols: int, dtype, vec: int):
     """A new [rows, cols] matrix whose rows begin at multiples of `vec` elements."""
-    torch = _torch()
     if cols % vec == 0:
-        return torch.empty((rows, cols), dtype=dtype, device=device)
-    return torch.empty((rows, -(-cols // vec) * vec), dtype=dtype, device=device)[:, :cols]
+        return like.new_empty((rows, cols), dtype=dtype)
+    return like.new_empty((rows, -(-cols // vec) * vec), dtype=dtype)[:, :cols]
+
+
+def _new_workspace(workspace, nbytes: int, like):
+    torch = _torch()
+    if workspace is None or workspace.numel() * workspace.element_size() < nbytes:
+        workspace = like.new_empty(max(nbytes, 1), dtype=torch.uint8)
+    elif workspace.get_device() != like.get_device() or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {like.device}")
+    return workspace, workspace.numel() * workspace.element_size()
 
 
 def _act_code(act: str) -> int:
@@ -602,33 +602,36 @@ def dust_linear(x, W, bias=None, act: str = "none", residual=None, y=None, z=Non
     x, residual, y and z may be further apart than their length."""
     torch = _torch()
     bf, f32 = torch.bfloat16, torch.float32
-    dev = x.device
+    dev = x.get_device()
+    scope = _scope(dev, stream)
+    if scope is not None:
+        with scope:
+            return dust_linear(x, W, bias, act, residual, y, z, out_dtype)
     if x.dim() != 2 or W.dim() != 2:
         raise ValueError("x must be [N, d_in] and W [d_out, d_in]")
     N, d_in = x.shape
-    d_out = W.shape[0]
+    d_out, k = W.shape
+    if k != d_in:
+        raise ValueError("x must be [N, d_in] and W [d_out, d_in]")
     ld_x = _rows(x, "x", N, d_in, dev, (bf,))
     _flat(W, "W", d_out * d_in, dev, bf)
-    if W.shape[1] != d_in:
-        raise ValueError("x must be [N, d_in] and W [d_out, d_in]")
     if bias is not None:
         _flat(bias, "bias", d_out, dev, f32)
-    code = _act_code(act)
-    with _scope(dev, stream):
-        if y is None:
-            y = torch.empty((N, d_out), dtype=out_dtype or bf, device=dev)
-        elif out_dtype is not None and y.dtype != out_dtype:
+    if y is None:
+        y = x.new_empty((N, d_out), dtype=out_dtype or bf)
+        ld_y = d_out
+    else:
+        if out_dtype is not None and y.dtype != out_dtype:
             raise TypeError(f"y is {y.dtype}, out_dtype {out_dtype}")
         ld_y = _rows(y, "y", N, d_out, dev, (bf, f32))
-        ld_res = _rows(residual, "residual", N, d_out, dev, (y.dtype,)) if residual is not None else 0
-        keep = z is not None and z is not False
-        if z is True:
-            z = torch.empty((N, d_out), dtype=bf, device=dev)
-        ld_z = _rows(z, "z", N, d_out, dev, (bf,)) if keep else 0
-        st = lib().dust_linear(x.data_ptr(), ld_x, W.data_ptr(), _ptr(bias), code, _ptr(residual), ld_res,
-                               DUST_BF16, N, d_in, d_out, y.data_ptr(),
-                               DUST_BF16 if y.dtype == bf else DUST_F32, ld_y,
-                               z.data_ptr() if keep else None, ld_z, _raw_stream(dev))
+    ld_res = _rows(residual, "residual", N, d_out, dev, (y.dtype,)) if residual is not None else 0
+    keep = z is not None and z is not False
+    if z is True:
+        z = x.new_empty((N, d_out))
+    ld_z = _rows(z, "z", N, d_out, dev, (bf,)) if keep else 0
+    st = lib().dust_linear(x.data_ptr(), ld_x, W.data_ptr(), _ptr(bias), _act_code(act), _ptr(residual), ld_res,
+                           DUST_BF16, N, d_in, d_out, y.data_ptr(), _dtype_code(y), ld_y,
+                           z.data_ptr() if keep else None, ld_z, _raw_stream(dev))
     _check(st, "dust_linear")
     return (y, z) if keep else y
 
@@ -641,54 +644,55 @@ def dust_linear_backward(dy, x, W, act: str = "none", z=None, dx=True, dW=True, 
     accumulate=True adds to the given dW and db."""
     torch = _torch()
     bf, f32 = torch.bfloat16, torch.float32
-    dev = dy.device
+    dev = dy.get_device()
+    scope = _scope(dev, stream)
+    if scope is not None:
+        with scope:
+            return dust_linear_backward(dy, x, W, act, z, dx, dW, db, accumulate, dx_dtype, workspace, None, g_terms)
     if dy.dim() != 2 or x.dim() != 2 or W.dim() != 2:
         raise ValueError("dy must be [N, d_out], x [N, d_in], W [d_out, d_in]")
     N, d_out = dy.shape
     d_in = x.shape[1]
     ld_dy = _rows(dy, "dy", N, d_out, dev, (bf, f32))
     ld_x = _rows(x, "x", N, d_in, dev, (bf,))
-    _flat(W, "W", d_out * d_in, dev, bf)
-    if tuple(W.shape) != (d_out, d_in):
+    if W.shape != (d_out, d_in):
         raise ValueError("dy must be [N, d_out], x [N, d_in], W [d_out, d_in]")
+    _flat(W, "W", d_out * d_in, dev, bf)
     code = _act_code(act)
     if code and z is None:
         raise ValueError(f"act={act!r} needs the pre-activation z that dust_linear kept")
     ld_z = _rows(z, "z", N, d_out, dev, (bf,)) if code else 0
     if accumulate and (dW is True or db is True):
         raise ValueError("accumulate adds to given dW and db tensors; pass them, or None to skip them")
-    with _scope(dev, stream):
-        if dx is True:
-            dx = torch.empty((N, d_in), dtype=dx_dtype or bf, device=dev)
-        if dW is True:
-            dW = torch.empty((d_out, d_in), dtype=f32, device=dev)
-        if db is True:
-            db = torch.empty(d_out, dtype=f32, device=dev)
-        dx, dW, db = (None if t is False else t for t in (dx, dW, db))
-        if dx is not None and dx_dtype is not None and dx.dtype != dx_dtype:
-            raise TypeError(f"dx is {dx.dtype}, dx_dtype {dx_dtype}")
-        ld_dx = _rows(dx, "dx", N, d_in, dev, (bf, f32)) if dx is not None else 0
-        if dW is not None:
-            _flat(dW, "dW", d_out * d_in, dev, f32)
-        if db is not None:
-            _flat(db, "db", d_out, dev, f32)
-        ws, nb = _workspace(workspace, dust_workspace_size(DUST_OP_LINEAR_BACKWARD, DUST_BF16, N, d_in, d_out, 0),
-                            dev)
-        st = lib().dust_linear_backward(dy.data_ptr(), _dtype_code(dy), ld_dy, z.data_ptr() if code else None, ld_z,
-                                        x.data_ptr(), ld_x, W.data_ptr(), code, DUST_BF16, N, d_in, d_out,
-                                        int(g_terms), _ptr(dx),
-                                        DUST_F32 if dx is not None and dx.dtype == f32 else DUST_BF16, ld_dx,
-                                        _ptr(dW), _ptr(db), 1 if accumulate else 0, _ptr(ws), nb,
-                                        _raw_stream(dev))
+    if dx is True:
+        dx = x.new_empty((N, d_in), dtype=dx_dtype or bf)
+    if dW is True:
+        dW = x.new_empty((d_out, d_in), dtype=f32)
+    if db is True:
+        db = x.new_empty(d_out, dtype=f32)
+    dx, dW, db = (None if t is False else t for t in (dx, dW, db))
+    if dx is not None and dx_dtype is not None and dx.dtype != dx_dtype:
+        raise TypeError(f"dx is {dx.dtype}, dx_dtype {dx_dtype}")
+    ld_dx = _rows(dx, "dx", N, d_in, dev, (bf, f32)) if dx is not None else 0
+    if dW is not None:
+        _flat(dW, "dW", d_out * d_in, dev, f32)
+    if db is not None:
+        _flat(db, "db", d_out, dev, f32)
+    ws, nb = _new_workspace(workspace, dust_workspace_size(DUST_OP_LINEAR_BACKWARD, DUST_BF16, N, d_in, d_out, 0), x)
+    st = lib().dust_linear_backward(dy.data_ptr(), _dtype_code(dy), ld_dy, z.data_ptr() if code else None, ld_z,
+                                    x.data_ptr(), ld_x, W.data_ptr(), code, DUST_BF16, N, d_in, d_out,
+                                    int(g_terms), _ptr(dx),
+                                    DUST_F32 if dx is not None and dx.dtype == f32 else DUST_BF16, ld_dx,
+                                    _ptr(dW), _ptr(db), 1 if accumulate else 0, ws.data_ptr(), nb, _raw_stream(dev))
     _check(st, "dust_linear_backward")
     return dx, dW, db
 
 
-def _check_ids(ids):
+def _check_ids(ids) -> int:
     torch = _torch()
     if ids.dtype != torch.int32:
         raise TypeError("ids must be int32")
-    if not ids.is_cuda or ids.dim() != 1 or not ids.is_contiguous():
+    if ids.dim() != 1 or not ids.is_contiguous():
         raise ValueError("ids must be a contiguous CUDA vector")
     return ids.numel()
 
@@ -699,19 +703,22 @@ def dust_embedding(ids, E, scale: float = 1.0, out=None, out_dtype=None, stream=
     torch = _torch()
     both = (torch.bfloat16, torch.float32)
     N = _check_ids(ids)
-    dev = ids.device
+    dev = ids.get_device()
+    scope = _scope(dev, stream)
+    if scope is not None:
+        with scope:
+            return dust_embedding(ids, E, scale, out, out_dtype)
     if E.dim() != 2:
         raise ValueError("E must be [V, d]")
     V, d = E.shape
     ld_E = _rows(E, "E", V, d, dev, both)
-    with _scope(dev, stream):
-        if out is None:
-            out = _new_rows(N, d, out_dtype or E.dtype, dev, 8)
-        elif out_dtype is not None and out.dtype != out_dtype:
-            raise TypeError(f"out is {out.dtype}, out_dtype {out_dtype}")
-        ld_out = _rows(out, "out", N, d, dev, both)
-        st = lib().dust_embedding(ids.data_ptr(), E.data_ptr(), _dtype_code(E), ld_E, N, V, d, float(scale),
-                                  out.data_ptr(), _dtype_code(out), ld_out, _raw_stream(dev))
+    if out is None:
+        out = _new_rows(E, N, d, out_dtype or E.dtype, 8)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise TypeError(f"out is {out.dtype}, out_dtype {out_dtype}")
+    ld_out = _rows(out, "out", N, d, dev, both)
+    st = lib().dust_embedding(ids.data_ptr(), E.data_ptr(), _dtype_code(E), ld_E, N, V, d, float(scale),
+                              out.data_ptr(), _dtype_code(out), ld_out, _raw_stream(dev))
     _check(st, "dust_embedding")
     return out
 
@@ -722,22 +729,24 @@ def dust_embedding_grad(ids, g, V: int, scale: float = 1.0, G=None, accumulate: 
     [N, d] (bf16 or fp32).  accumulate=True adds to the rows of the given G that have tokens."""
     torch = _torch()
     N = _check_ids(ids)
-    dev = ids.device
+    dev = ids.get_device()
+    scope = _scope(dev, stream)
+    if scope is not None:
+        with scope:
+            return dust_embedding_grad(ids, g, V, scale, G, accumulate, workspace)
     if g.dim() != 2:
         raise ValueError("g must be [N, d]")
     d = g.shape[1]
     ld_g = _rows(g, "g", N, d, dev, (torch.bfloat16, torch.float32))
     if accumulate and G is None:
         raise ValueError("accumulate adds to a given G")
-    with _scope(dev, stream):
-        if G is None:
-            G = _new_rows(V, d, torch.float32, dev, 4)
-        ld_G = _rows(G, "G", V, d, dev, (torch.float32,))
-        dt = _dtype_code(g)
-        ws, nb = _workspace(workspace, dust_workspace_size(DUST_OP_EMBEDDING_GRAD, dt, N, V, d, 0), dev)
-        st = lib().dust_embedding_grad(ids.data_ptr(), g.data_ptr(), dt, ld_g, N, V, d, float(scale), G.data_ptr(),
-                                       ld_G, 1 if accumulate else 0, _ptr(ws), nb,
-                                       _raw_stream(dev))
+    if G is None:
+        G = _new_rows(g, V, d, torch.float32, 4)
+    ld_G = _rows(G, "G", V, d, dev, (torch.float32,))
+    dt = _dtype_code(g)
+    ws, nb = _new_workspace(workspace, dust_workspace_size(DUST_OP_EMBEDDING_GRAD, dt, N, V, d, 0), g)
+    st = lib().dust_embedding_grad(ids.data_ptr(), g.data_ptr(), dt, ld_g, N, V, d, float(scale), G.data_ptr(),
+                                   ld_G, 1 if accumulate else 0, ws.data_ptr(), nb, _raw_stream(dev))
     _check(st, "dust_embedding_grad")
     return G
 
@@ -762,6 +771,7 @@ class DustOptimizer:
         if k == 0:
             raise ValueError("no tensors")
         self.device = self.W[0].device
+        self._index = self.W[0].get_device()
         dev, f32 = self.device, torch.float32
         sizes = [t.numel() for t in self.W]
         state = f32 if bits == 32 else torch.float8_e4m3fn
@@ -774,7 +784,7 @@ class DustOptimizer:
                 raise ValueError(f"{what} must have one entry for each of the {k} tensors")
             for i, (t, n) in enumerate(zip(given, counts)):
                 if t is not None or not may_skip:
-                    _flat(t, f"{what}[{i}]", n, dev, dtype)
+                    _flat(t, f"{what}[{i}]", n, self._index, dtype)
             return given
 
         take(self.W, "W", f32, sizes)
@@ -809,7 +819,7 @@ class DustOptimizer:
         if dtype not in (torch.float32, torch.bfloat16):
             raise TypeError(f"gradients are fp32 or bf16, not {dtype}")
         for i, (g, w) in enumerate(zip(G, self.W)):
-            _flat(g, f"G[{i}]", w.numel(), self.device, dtype)
+            _flat(g, f"G[{i}]", w.numel(), self._index, dtype)
         self.G, self._g_dt = G, DUST_F32 if dtype == torch.float32 else DUST_BF16
         for d, g in zip(self._desc, G):
             d.G = g.data_ptr()
@@ -819,15 +829,17 @@ class DustOptimizer:
         CUDA scalar that multiplies every gradient.  step: optional int32 CUDA scalar with Adam's
         step count, read when the step runs (for captured graphs); None takes opt.step."""
         torch = _torch()
+        scope = _scope(self._index, stream)
+        if scope is not None:
+            with scope:
+                return self.step(opt, g_scale, step)
         if g_scale is not None:
-            _flat(g_scale, "g_scale", 1, self.device, torch.float32)
+            _flat(g_scale, "g_scale", 1, self._index, torch.float32)
         if step is not None:
-            _flat(step, "step", 1, self.device, torch.int32)
-        with _scope(self.device, stream):
-            st = lib().dust_optimizer_step_grouped(ctypes.byref(opt), self._desc, len(self.W), self._g_dt,
-                                                   DUST_STATE_F32 if self.bits == 32 else DUST_STATE_E4M3,
-                                                   _ptr(g_scale), _ptr(step),
-                                                   _raw_stream(self.device))
+            _flat(step, "step", 1, self._index, torch.int32)
+        st = lib().dust_optimizer_step_grouped(ctypes.byref(opt), self._desc, len(self.W), self._g_dt,
+                                               DUST_STATE_F32 if self.bits == 32 else DUST_STATE_E4M3,
+                                               _ptr(g_scale), _ptr(step), _raw_stream(self._index))
         _check(st, "dust_optimizer_step_grouped")
         return self.W
 

@@ -13,8 +13,11 @@
 // chunks of equal length; one warp sums a chunk's rows over 128 (fp32) or 256 (bf16) columns,
 // sixteen bytes a lane, eight rows in flight, and writes a table row whenever the id changes.  An id
 // that crosses a chunk border leaves partial sums, which a last kernel adds in chunk order: no
-// atomics on floats, and the same result on every run.  Rows that no token names are cleared in the
-// same launch by CTAs that look for their ids in the sorted list, so every row is written once.
+// sum depends on the order of atomics, and every run gives the same result.  Rows that no token names are
+// cleared in the same launch by CTAs that look for their ids in the sorted list, so every row is written once.
+//
+// Up to 4096 tokens take one launch instead: each CTA picks the tokens whose id falls to its share of the
+// table (id mod the number of shares), sorts those few in shared memory and sums them.
 //
 // Both are HBM-bound: the rows read and written once.
 #include <algorithm>
@@ -60,8 +63,8 @@ __device__ __forceinline__ V8 load8(const __nv_bfloat16* p, int n) {
 }
 __device__ __forceinline__ void store8(float* p, const V8& r, int n) {
     if (n >= 8) {
-        reinterpret_cast<float4*>(p)[0] = make_float4(r.v[0], r.v[1], r.v[2], r.v[3]);
-        reinterpret_cast<float4*>(p)[1] = make_float4(r.v[4], r.v[5], r.v[6], r.v[7]);
+        __stcs(reinterpret_cast<float4*>(p), make_float4(r.v[0], r.v[1], r.v[2], r.v[3]));
+        __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(r.v[4], r.v[5], r.v[6], r.v[7]));
     } else {
         for (int j = 0; j < n; ++j) p[j] = r.v[j];
     }
@@ -75,7 +78,7 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const V8& r, int n) {
             const __nv_bfloat162 b = __floats2bfloat162_rn(r.v[2 * j], r.v[2 * j + 1]);
             wp[j] = *reinterpret_cast<const uint32_t*>(&b);
         }
-        *reinterpret_cast<uint4*>(p) = w;
+        __stcs(reinterpret_cast<uint4*>(p), w);
     } else {
         for (int j = 0; j < n; ++j) p[j] = __float2bfloat16_rn(r.v[j]);
     }
@@ -129,15 +132,18 @@ constexpr int kBinBits = 9;
 constexpr int kBins = 1 << kBinBits;
 constexpr int kSThreads = 512;  // one thread per bin in the prefix sums
 constexpr int kSWarps = kSThreads / 32;
-constexpr int kSRounds = 8;     // keys per lane
-constexpr int kTile = kSThreads * kSRounds;
 static_assert(kSThreads == kBins, "one thread per bin");
+// Keys per lane: a tile is 512 of each.  Small tiles spread a sort over more SMs, large ones shorten the
+// sums over the tiles' counts, which every CTA takes itself.
+constexpr int kFewRounds = 2, kManyRounds = 8;
+constexpr int64_t kManyTokens = 1 << 18;
 
 __device__ __forceinline__ uint32_t key_of(int32_t id, int32_t V) {
     return id >= 0 && id < V ? static_cast<uint32_t>(id) : static_cast<uint32_t>(V);  // no row: last
 }
 
 // Digit counts of each tile: hist[tile][bin].
+template <int kSRounds>
 __global__ void __launch_bounds__(kSThreads) embed_hist_kernel(const int32_t* __restrict__ ids,
                                                                const uint32_t* __restrict__ keys, int64_t N,
                                                                int32_t V, int shift, uint32_t mask,
@@ -145,7 +151,7 @@ __global__ void __launch_bounds__(kSThreads) embed_hist_kernel(const int32_t* __
     __shared__ int32_t cnt[kBins];
     cnt[threadIdx.x] = 0;
     __syncthreads();
-    const int64_t p0 = static_cast<int64_t>(blockIdx.x) * kTile;
+    const int64_t p0 = static_cast<int64_t>(blockIdx.x) * (kSThreads * kSRounds);
 #pragma unroll
     for (int r = 0; r < kSRounds; ++r) {
         const int64_t p = p0 + r * kSThreads + threadIdx.x;
@@ -161,6 +167,7 @@ __global__ void __launch_bounds__(kSThreads) embed_hist_kernel(const int32_t* __
 // Where each of this thread's keys goes within a stable order of the tile by digit, on top of
 // base[bin].  Keys are taken warp by warp, round by round, lane by lane: their order in the tile.
 // `n` keys are valid.  All threads of the CTA call it; wh [kSWarps][kBins] is scratch.
+template <int kSRounds>
 __device__ __forceinline__ void tile_ranks(const uint32_t (&digit)[kSRounds], int n, int32_t base,
                                            int32_t (*wh)[kBins], int32_t (&pos)[kSRounds]) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -223,6 +230,7 @@ __device__ __forceinline__ int32_t scan_bins(int32_t x, int32_t* sh) {
 
 // One pass over a tile: reads its keys (ids in the first pass), writes keys and token indices in
 // the order of the pass's digit.  Each CTA sums the other tiles' counts itself.
+template <int kSRounds>
 __global__ void __launch_bounds__(kSThreads) embed_scatter_kernel(
     const int32_t* __restrict__ ids, const uint32_t* __restrict__ keys, const int32_t* __restrict__ idx,
     int64_t N, int32_t V, int shift, uint32_t mask, const int32_t* __restrict__ hist, int tiles,
@@ -238,6 +246,7 @@ __global__ void __launch_bounds__(kSThreads) embed_scatter_kernel(
         if (t < tile) earlier += c;
     }
     const int32_t base = scan_bins(all, sh) + earlier;
+    constexpr int kTile = kSThreads * kSRounds;
     const int64_t p0 = static_cast<int64_t>(tile) * kTile;
     const int n = static_cast<int>(min(static_cast<int64_t>(kTile), N - p0));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -254,7 +263,7 @@ __global__ void __launch_bounds__(kSThreads) embed_scatter_kernel(
         }
         digit[r] = (key[r] >> shift) & mask;
     }
-    tile_ranks(digit, n, base, wh, pos);
+    tile_ranks<kSRounds>(digit, n, base, wh, pos);
 #pragma unroll
     for (int r = 0; r < kSRounds; ++r) {
         const int at = (warp * kSRounds + r) * 32 + lane;
@@ -264,69 +273,6 @@ __global__ void __launch_bounds__(kSThreads) embed_scatter_kernel(
         }
     }
 }
-
-// A batch of at most one tile: all passes in one CTA, through shared memory.
-__global__ void __launch_bounds__(kSThreads) embed_sort_tile_kernel(const int32_t* __restrict__ ids, int N,
-                                                                    int32_t V, int passes, int bits,
-                                                                    uint32_t* keys_out, int32_t* idx_out) {
-    extern __shared__ int32_t dyn[];
-    int32_t(*wh)[kBins] = reinterpret_cast<int32_t(*)[kBins]>(dyn);
-    uint32_t* skey = reinterpret_cast<uint32_t*>(dyn + kSWarps * kBins);  // [kTile]
-    int32_t* sval = reinterpret_cast<int32_t*>(skey + kTile);             // [kTile]
-    int32_t* cnt = sval + kTile;                                          // [kBins]
-    int32_t* sh = cnt + kBins;                                            // [32]
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    uint32_t key[kSRounds], digit[kSRounds];
-    int32_t val[kSRounds], pos[kSRounds];
-#pragma unroll
-    for (int r = 0; r < kSRounds; ++r) {
-        const int at = (warp * kSRounds + r) * 32 + lane;
-        key[r] = at < N ? key_of(ids[at], V) : 0u;
-        val[r] = at;
-    }
-    const uint32_t mask = (1u << bits) - 1u;
-    for (int pass = 0; pass < passes; ++pass) {
-        cnt[threadIdx.x] = 0;
-        __syncthreads();
-#pragma unroll
-        for (int r = 0; r < kSRounds; ++r) {
-            const int at = (warp * kSRounds + r) * 32 + lane;
-            digit[r] = (key[r] >> (pass * bits)) & mask;
-            if (at < N) atomicAdd(&cnt[digit[r]], 1);
-        }
-        __syncthreads();
-        const int32_t base = scan_bins(cnt[threadIdx.x], sh);
-        tile_ranks(digit, N, base, wh, pos);
-        if (pass + 1 == passes) break;
-#pragma unroll
-        for (int r = 0; r < kSRounds; ++r) {
-            const int at = (warp * kSRounds + r) * 32 + lane;
-            if (at < N) {
-                skey[pos[r]] = key[r];
-                sval[pos[r]] = val[r];
-            }
-        }
-        __syncthreads();
-#pragma unroll
-        for (int r = 0; r < kSRounds; ++r) {
-            const int at = (warp * kSRounds + r) * 32 + lane;
-            if (at < N) {
-                key[r] = skey[at];
-                val[r] = sval[at];
-            }
-        }
-        __syncthreads();
-    }
-#pragma unroll
-    for (int r = 0; r < kSRounds; ++r) {
-        const int at = (warp * kSRounds + r) * 32 + lane;
-        if (at < N) {
-            keys_out[pos[r]] = key[r];
-            idx_out[pos[r]] = val[r];
-        }
-    }
-}
-constexpr int kSortTileSmem = (kSWarps * kBins + 2 * kTile + kBins + 32) * 4;
 
 // ------------------------------------------------------------------ the sums
 constexpr int kGThreads = 256;
@@ -382,19 +328,20 @@ struct Lane<__nv_bfloat16> {
     }
 };
 
+// Writes or adds a finished row piece.  Each element gets one addition in the whole call, so the
+// reductions (which the warp does not wait for, unlike a load of the old row) leave no order open.
 template <int kN>
 __device__ __forceinline__ void put_row(float* row, const float (&a)[kN], int n, float scale, bool accumulate) {
     if (n >= kN) {
-        float4* r4 = reinterpret_cast<float4*>(row);
 #pragma unroll
-        for (int j = 0; j < kN / 4; ++j) {
-            float4 w = make_float4(a[4 * j] * scale, a[4 * j + 1] * scale, a[4 * j + 2] * scale,
-                                   a[4 * j + 3] * scale);
-            if (accumulate) {
-                const float4 o = r4[j];
-                w = make_float4(o.x + w.x, o.y + w.y, o.z + w.z, o.w + w.w);
-            }
-            r4[j] = w;
+        for (int j = 0; j < kN; j += 4) {
+            const float4 w = make_float4(a[j] * scale, a[j + 1] * scale, a[j + 2] * scale, a[j + 3] * scale);
+            if (accumulate)
+                asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(row + j), "f"(w.x), "f"(w.y),
+                             "f"(w.z), "f"(w.w)
+                             : "memory");
+            else
+                *reinterpret_cast<float4*>(row + j) = w;
         }
     } else {
 #pragma unroll
@@ -507,19 +454,19 @@ __global__ void __launch_bounds__(kGThreads) embed_grad_kernel(const __grid_cons
         put_row(A.G + static_cast<int64_t>(cur) * A.ld_G + col, acc, n, A.scale, A.accumulate != 0);
 }
 
-// CTA (chunk, 128 columns): if an id begins in the chunk and goes on past its end, adds its partial
-// sums.  The eight warps take consecutive runs of chunks, summed in order and then warp by warp.
+// CTA (chunk, 512 columns): if an id begins in the chunk and goes on past its end, adds its partial
+// sums.  Two halves of the CTA take consecutive runs of chunks, each summed in order.
+constexpr int kJoinCols = 512;
 __global__ void __launch_bounds__(kGThreads) embed_join_kernel(const __grid_constant__ GradArgs A, int32_t slabs) {
     const int64_t c = blockIdx.x / slabs;
-    const int64_t p1 = (c + 1) * A.chunk;
+    const int64_t p0 = c * A.chunk, p1 = p0 + A.chunk;
     if (p1 >= A.N) return;
-    const uint32_t cur = __ldg(A.key + p1 - 1);
-    if (cur == static_cast<uint32_t>(A.V) || __ldg(A.key + p1) != cur) return;
-    const int64_t p0 = c * A.chunk;
-    if (p0 > 0 && __ldg(A.key + p0 - 1) == cur) return;  // it began earlier
-    __shared__ float4 part[kGWarps][32];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int col = static_cast<int>(blockIdx.x - c * slabs) * 128 + 4 * lane;
+    const uint32_t cur = __ldg(A.key + p1 - 1), after = __ldg(A.key + p1);
+    const uint32_t before = p0 > 0 ? __ldg(A.key + p0 - 1) : ~cur;
+    if (cur == static_cast<uint32_t>(A.V) || after != cur || before == cur) return;
+    __shared__ float4 part[kGThreads / 2];
+    const int half = threadIdx.x / (kGThreads / 2), at = threadIdx.x % (kGThreads / 2);
+    const int col = static_cast<int>(blockIdx.x - c * slabs) * kJoinCols + 4 * at;
     // chunks c + 1 .. end - 1 begin with this id
     int64_t lo = c + 1, hi = A.chunks;
     while (lo < hi) {
@@ -529,27 +476,194 @@ __global__ void __launch_bounds__(kGThreads) embed_join_kernel(const __grid_cons
         else
             hi = mid;
     }
-    const int64_t cnt = lo - (c + 1), per = (cnt + kGWarps - 1) / kGWarps;
-    const int64_t a = c + 1 + warp * per, b = min(lo, a + per);
+    const int64_t mid = c + 1 + (lo - c) / 2;
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
     if (col < A.dpad) {
-        if (warp == 0) s = *reinterpret_cast<const float4*>(A.tail + c * A.dpad + col);
+        if (half == 0) s = *reinterpret_cast<const float4*>(A.tail + c * A.dpad + col);
 #pragma unroll 8
-        for (int64_t k = a; k < b; ++k) {
+        for (int64_t k = half ? mid : c + 1; k < (half ? lo : mid); ++k) {
             const float4 h = *reinterpret_cast<const float4*>(A.head + k * A.dpad + col);
             s = make_float4(s.x + h.x, s.y + h.y, s.z + h.z, s.w + h.w);
         }
     }
-    part[warp][lane] = s;
+    if (half) part[at] = s;
     __syncthreads();
-    if (warp == 0 && col < A.d) {
-        for (int w = 1; w < kGWarps; ++w) {
-            const float4 h = part[w][lane];
-            s = make_float4(s.x + h.x, s.y + h.y, s.z + h.z, s.w + h.w);
-        }
-        const float acc[4] = {s.x, s.y, s.z, s.w};
+    if (!half && col < A.d) {
+        const float4 h = part[at];
+        const float acc[4] = {s.x + h.x, s.y + h.y, s.z + h.z, s.w + h.w};
         put_row(A.G + static_cast<int64_t>(cur) * A.ld_G + col, acc, A.d - col, A.scale, A.accumulate != 0);
     }
+}
+
+// ------------------------------------------------------------------ small batches in one launch
+constexpr int kSmallTokens = 4096;
+constexpr int kIdsPerThread = kSmallTokens / kGThreads;
+
+struct SmallArgs {
+    const int32_t* ids;
+    const void* g;
+    float* G;
+    int64_t ld_g, ld_G;
+    int32_t N, V, d, shares, accumulate;  // shares: a power of two
+    float scale;
+};
+
+// CTA (share, 32 kN columns).  Keys are (id, token), all different, so that sorting them orders each id's
+// tokens; the eight warps sum consecutive runs of the sorted list and join the ids that cross runs.
+template <typename T>
+__global__ void __launch_bounds__(kGThreads) embed_grad_small_kernel(const __grid_constant__ SmallArgs A) {
+    constexpr int kN = Lane<T>::kN;
+    extern __shared__ uint64_t list[];  // [kSmallTokens]
+    __shared__ float first[kGWarps][32 * kN], last[kGWarps][32 * kN];
+    int32_t* sums = reinterpret_cast<int32_t*>(first);  // until the list is complete
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int32_t share = static_cast<int32_t>(blockIdx.x);
+
+    // this share's tokens, in order: thread t looks at ids [16 t, 16 t + 16)
+    int32_t id[kIdsPerThread];
+    int count = 0;
+    const int at0 = threadIdx.x * kIdsPerThread;
+#pragma unroll
+    for (int j = 0; j < kIdsPerThread; ++j) {
+        id[j] = at0 + j < A.N ? __ldg(A.ids + at0 + j) : -1;
+        if (id[j] < 0 || id[j] >= A.V || (id[j] & (A.shares - 1)) != share) id[j] = -1;
+        count += id[j] >= 0;
+    }
+    int incl = count;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+        if (lane >= o) incl += v;
+    }
+    if (lane == 31) sums[warp] = incl;
+    __syncthreads();
+    int base = incl - count, n = 0;
+    for (int w = 0; w < kGWarps; ++w) {
+        if (w < warp) base += sums[w];
+        n += sums[w];
+    }
+#pragma unroll
+    for (int j = 0; j < kIdsPerThread; ++j)
+        if (id[j] >= 0) list[base++] = (static_cast<uint64_t>(id[j]) << 32) | static_cast<uint32_t>(at0 + j);
+    int size = 1;
+    while (size < n) size <<= 1;
+    for (int i = n + threadIdx.x; i < size; i += kGThreads) list[i] = ~0ull;  // sorts behind all
+    __syncthreads();
+    // bitonic sort
+    for (int k = 2; k <= size; k <<= 1)
+        for (int j = k >> 1; j > 0; j >>= 1) {
+            for (int i = threadIdx.x; i < size / 2; i += kGThreads) {
+                const int a = 2 * i - (i & (j - 1)), b = a + j;
+                const uint64_t x = list[a], y = list[b];
+                if ((x > y) == ((a & k) == 0)) {
+                    list[a] = y;
+                    list[b] = x;
+                }
+            }
+            __syncthreads();
+        }
+
+    const int col = static_cast<int>(blockIdx.y) * (32 * kN) + kN * lane;
+    const int left = A.d - col;
+    const T* g = static_cast<const T*>(A.g) + col;
+    // warp w: positions [p0, p1) of the list
+    const int per = (n + kGWarps - 1) / kGWarps;
+    const int p0 = min(n, warp * per), p1 = min(n, p0 + per);
+    auto key = [&](int p) { return static_cast<int32_t>(list[p] >> 32); };
+    if (p0 < p1) {
+        int32_t cur = key(p0);
+        bool began_before = p0 > 0 && key(p0 - 1) == cur;
+        float acc[kN] = {};
+        for (int p = p0; p < p1; p += 8) {
+            typename Lane<T>::Raw raw[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                raw[j] = typename Lane<T>::Raw{};
+                if (p + j < p1) {
+                    const int64_t t = static_cast<uint32_t>(list[p + j]);
+                    if (left >= kN)
+                        raw[j] = __ldcs(reinterpret_cast<const typename Lane<T>::Raw*>(g + t * A.ld_g));
+                    else if (left > 0)
+                        raw[j] = Lane<T>::tail(g + t * A.ld_g, left);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if (p + j >= p1) break;
+                const int32_t k = key(p + j);
+                if (k != cur) {
+                    if (began_before) {
+#pragma unroll
+                        for (int i = 0; i < kN; ++i) first[warp][kN * lane + i] = acc[i];
+                    } else if (left > 0) {
+                        put_row(A.G + static_cast<int64_t>(cur) * A.ld_G + col, acc, left, A.scale, A.accumulate != 0);
+                    }
+                    began_before = false;
+                    cur = k;
+#pragma unroll
+                    for (int i = 0; i < kN; ++i) acc[i] = 0.f;
+                }
+                Lane<T>::add(acc, raw[j]);
+            }
+        }
+        const bool goes_on = p1 < n && key(p1) == cur;
+        if (began_before) {
+#pragma unroll
+            for (int i = 0; i < kN; ++i) first[warp][kN * lane + i] = acc[i];
+        } else if (goes_on) {
+#pragma unroll
+            for (int i = 0; i < kN; ++i) last[warp][kN * lane + i] = acc[i];
+        } else if (left > 0) {
+            put_row(A.G + static_cast<int64_t>(cur) * A.ld_G + col, acc, left, A.scale, A.accumulate != 0);
+        }
+    }
+    __syncthreads();
+    // the warp in whose run an id begins that goes on past it adds the later runs' shares in order
+    if (p0 < p1 && p1 < n) {
+        const int32_t cur = key(p1 - 1);
+        if (key(p1) == cur && !(p0 > 0 && key(p0 - 1) == cur) && left > 0) {
+            float acc[kN];
+#pragma unroll
+            for (int i = 0; i < kN; ++i) acc[i] = last[warp][kN * lane + i];
+            for (int w = warp + 1; w < kGWarps && w * per < n && key(w * per) == cur; ++w)
+#pragma unroll
+                for (int i = 0; i < kN; ++i) acc[i] += first[w][kN * lane + i];
+            put_row(A.G + static_cast<int64_t>(cur) * A.ld_G + col, acc, left, A.scale, A.accumulate != 0);
+        }
+    }
+    if (A.accumulate) return;
+    // clear this share's rows that no token names: each lane looks for one row, the warp clears them
+    const int64_t rows = (static_cast<int64_t>(A.V) - share + A.shares - 1) / A.shares;  // share + k shares < V
+    for (int64_t k0 = 32 * warp; k0 < rows; k0 += 32 * kGWarps) {
+        const int64_t k = k0 + lane;
+        bool absent = false;
+        if (k < rows) {
+            const uint64_t v = static_cast<uint64_t>(share + k * A.shares) << 32;
+            int lo = 0, hi = n;
+            while (lo < hi) {
+                const int mid = (lo + hi) >> 1;
+                if (list[mid] < v)
+                    lo = mid + 1;
+                else
+                    hi = mid;
+            }
+            absent = lo == n || (list[lo] >> 32) != (v >> 32);
+        }
+        uint32_t todo = __ballot_sync(0xFFFFFFFFu, absent);
+        const float zero[kN] = {};
+        while (todo) {
+            const int b = __ffs(todo) - 1;
+            todo &= todo - 1;
+            if (left > 0) put_row(A.G + (share + (k0 + b) * A.shares) * A.ld_G + col, zero, left, 1.0f, false);
+        }
+    }
+}
+
+template <typename T>
+dust_status launch_small(const SmallArgs& A, int slabs, cudaStream_t s) {
+    embed_grad_small_kernel<T><<<dim3(static_cast<unsigned>(A.shares), static_cast<unsigned>(slabs)), kGThreads,
+                                 kSmallTokens * 8, s>>>(A);
+    return cudaGetLastError() == cudaSuccess ? DUST_OK : DUST_ERR_CUDA;
 }
 
 struct GradPlan {
@@ -569,7 +683,8 @@ GradPlan grad_plan(dust_dtype dt, int64_t N, int32_t V, int32_t d) {
     while (c < 1024 && N / (2 * c) >= want) c *= 2;
     p.chunk = static_cast<int>(c);
     p.chunks = static_cast<int>((N + c - 1) / c);
-    p.tiles = static_cast<int>((N + kTile - 1) / kTile);
+    const int tile = kSThreads * (N < kManyTokens ? kFewRounds : kManyRounds);
+    p.tiles = static_cast<int>((N + tile - 1) / tile);
     p.dpad = (d + 7) / 8 * 8;
     int bits = 1;  // of the keys 0 .. V
     while (bits < 31 && (static_cast<int64_t>(V) >> bits) != 0) ++bits;
@@ -611,6 +726,7 @@ dust_status embedding_launch(const int32_t* ids, const void* E, dust_dtype dt, i
 }
 
 size_t embedding_grad_workspace_bytes(dust_dtype dt, int64_t N, int32_t V, int32_t d) {
+    if (N <= kSmallTokens) return 0;
     const GradPlan p = grad_plan(dt, N, V, d);
     return 4 * p.keys + p.hist + 2 * p.part;
 }
@@ -619,39 +735,45 @@ dust_status embedding_grad_launch(const int32_t* ids, const void* g, dust_dtype 
                                   int32_t V, int32_t d, float scale, float* G, int64_t ld_G, int accumulate,
                                   void* ws, cudaStream_t s) {
     const GradPlan p = grad_plan(dt, N, V, d);
+    if (N <= kSmallTokens) {
+        // about four CTAs an SM
+        int shares = 1;
+        while (shares < 512 && static_cast<int64_t>(shares) * p.slabs < static_cast<int64_t>(num_sms()) * 3) shares *= 2;
+        const SmallArgs A{ids, g, G, ld_g, ld_G, static_cast<int32_t>(N), V, d, shares, accumulate, scale};
+        if (p.slabs > 65535) return DUST_ERR_UNSUPPORTED;
+        prof_begin(s);
+        const dust_status st = dt == DUST_BF16 ? launch_small<__nv_bfloat16>(A, p.slabs, s)
+                                               : launch_small<float>(A, p.slabs, s);
+        prof_end(s, "embedding_grad_small");
+        return st;
+    }
     char* w = static_cast<char*>(ws);
     uint32_t* key[2] = {reinterpret_cast<uint32_t*>(w), reinterpret_cast<uint32_t*>(w + p.keys)};
     int32_t* idx[2] = {reinterpret_cast<int32_t*>(w + 2 * p.keys), reinterpret_cast<int32_t*>(w + 3 * p.keys)};
     int32_t* hist = reinterpret_cast<int32_t*>(w + 4 * p.keys);
     float* head = reinterpret_cast<float*>(w + 4 * p.keys + p.hist);
     float* tail = reinterpret_cast<float*>(w + 4 * p.keys + p.hist + p.part);
-    int at = 0;  // where the sorted list ends up
-    if (p.tiles == 1) {
-        static PerContextOnce attr;
-        if (!attr.run([] {
-                return cudaFuncSetAttribute(embed_sort_tile_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                            kSortTileSmem) == cudaSuccess;
-            }))
-            return DUST_ERR_CUDA;
+    const uint32_t mask = (1u << p.bits) - 1u;
+    int at = 1;  // where the sorted list ends up
+    for (int pass = 0; pass < p.passes; ++pass) {
+        const int32_t* first = pass == 0 ? ids : nullptr;
+        const int to = at ^ 1, shift = pass * p.bits;
+        const bool few = N < kManyTokens;
         prof_begin(s);
-        embed_sort_tile_kernel<<<1, kSThreads, kSortTileSmem, s>>>(ids, static_cast<int>(N), V, p.passes, p.bits,
-                                                                  key[0], idx[0]);
+        if (few)
+            embed_hist_kernel<kFewRounds><<<p.tiles, kSThreads, 0, s>>>(first, key[at], N, V, shift, mask, hist);
+        else
+            embed_hist_kernel<kManyRounds><<<p.tiles, kSThreads, 0, s>>>(first, key[at], N, V, shift, mask, hist);
+        prof_end(s, "embedding_sort_count");
+        prof_begin(s);
+        if (few)
+            embed_scatter_kernel<kFewRounds><<<p.tiles, kSThreads, 0, s>>>(first, key[at], idx[at], N, V, shift, mask,
+                                                                          hist, p.tiles, key[to], idx[to]);
+        else
+            embed_scatter_kernel<kManyRounds><<<p.tiles, kSThreads, 0, s>>>(first, key[at], idx[at], N, V, shift, mask,
+                                                                           hist, p.tiles, key[to], idx[to]);
         prof_end(s, "embedding_sort");
-    } else {
-        const uint32_t mask = (1u << p.bits) - 1u;
-        at = 1;
-        for (int pass = 0; pass < p.passes; ++pass) {
-            const int32_t* first = pass == 0 ? ids : nullptr;
-            const int to = at ^ 1;
-            prof_begin(s);
-            embed_hist_kernel<<<p.tiles, kSThreads, 0, s>>>(first, key[at], N, V, pass * p.bits, mask, hist);
-            prof_end(s, "embedding_sort_count");
-            prof_begin(s);
-            embed_scatter_kernel<<<p.tiles, kSThreads, 0, s>>>(first, key[at], idx[at], N, V, pass * p.bits, mask,
-                                                              hist, p.tiles, key[to], idx[to]);
-            prof_end(s, "embedding_sort");
-            at = to;
-        }
+        at = to;
     }
     GradArgs A{};
     A.key = key[at];
@@ -674,7 +796,7 @@ dust_status embedding_grad_launch(const int32_t* ids, const void* g, dust_dtype 
     A.scale = scale;
     A.zero_blocks = accumulate ? 0 : (V + kZeroRows - 1) / kZeroRows;
     const int64_t blocks = (A.units + kGWarps - 1) / kGWarps + A.zero_blocks;
-    const int join_slabs = (d + 127) / 128;
+    const int join_slabs = (d + kJoinCols - 1) / kJoinCols;
     if (blocks > 2147483647LL || static_cast<int64_t>(p.chunks) * join_slabs > 2147483647LL)
         return DUST_ERR_UNSUPPORTED;
     prof_begin(s);
