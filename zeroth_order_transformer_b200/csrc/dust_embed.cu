@@ -467,14 +467,11 @@ __global__ void __launch_bounds__(kGThreads) embed_join_kernel(const __grid_cons
     __shared__ float4 part[kGThreads / 2];
     const int half = threadIdx.x / (kGThreads / 2), at = threadIdx.x % (kGThreads / 2);
     const int col = static_cast<int>(blockIdx.x - c * slabs) * kJoinCols + 4 * at;
-    // chunks c + 1 .. end - 1 begin with this id
-    int64_t lo = c + 1, hi = A.chunks;
-    while (lo < hi) {
-        const int64_t mid = (lo + hi) >> 1;
-        if (__ldg(A.key + mid * A.chunk) == cur)
-            lo = mid + 1;
-        else
-            hi = mid;
+    // chunks c + 1 .. lo - 1 begin with this id
+    int64_t lo = c + 1;
+    for (int more = kGThreads; more == kGThreads; lo += more) {
+        const int64_t k = lo + threadIdx.x;
+        more = __syncthreads_count(k < A.chunks && __ldg(A.key + k * A.chunk) == cur);
     }
     const int64_t mid = c + 1 + (lo - c) / 2;
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);

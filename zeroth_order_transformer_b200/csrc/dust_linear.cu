@@ -11,8 +11,9 @@
 //                         thread issues the MMAs of a 128-row tile into one of two accumulators in
 //                         tensor memory, eight warps run the epilogue of the previous tile from the other.
 //                         The forward product, dx and dW differ in which operands are MN-major.
-//   linear_cluster_kernel the same pipeline for outputs of few tiles, the contraction cut over the CTAs of a
-//                         cluster and joined through distributed shared memory.
+//   linear_tokens_kernel  the same pipeline for outputs of few tiles: W's rows are the 128 rows of an MMA, the
+//                         tokens its columns, the contraction cut over the CTAs of a cluster and
+//                         joined through distributed shared memory.
 // dz is formed once (linear_dz_kernel) as a bf16 operand, or as hi + lo bf16 terms (dz = hi + lo to
 // about 16 bits), with the column sums for db on the way.
 #include <algorithm>
@@ -88,10 +89,58 @@ __device__ __forceinline__ float act_any(int act, float z) {
     }
     return z;
 }
+// The same on pairs with packed fp32 arithmetic, for the GEMM epilogues, which have two warps to a scheduler
+// and so pay for every instruction (a 128 x 256 tile with act_fn's GELU took 4.7 us longer than one without).
+__device__ __forceinline__ F2 both(float x) { return F2{x, x}; }
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float ex2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+// z / (1 + 2^e); e = -u log2 of e
+__device__ __forceinline__ F2 gated(F2 z, F2 e) {
+    const F2 d = add2(F2{ex2_approx(e.x), ex2_approx(e.y)}, both(1.0f));
+    return mul2(z, F2{rcp_approx(d.x), rcp_approx(d.y)});
+}
+template <int kAct>
+__device__ __forceinline__ F2 act_pair(F2 z) {
+    if (kAct == DUST_ACT_GELU) {
+        // z Phi(z) = max(z, 0) - |z| erfc(|z| / sqrt 2) / 2 with 7.1.28 of Abramowitz and Stegun, erfc(x) =
+        // (1 + a1 x + ... + a6 x^6)^-16 to 3e-7: one reciprocal, no exponential
+        const F2 az{fabsf(z.x), fabsf(z.y)};
+        const F2 x = mul2(az, both(kSqrtHalf));
+        F2 p = fma2(both(0.0000430638f), x, both(0.0002765672f));
+        p = fma2(p, x, both(0.0001520143f));
+        p = fma2(p, x, both(0.0092705272f));
+        p = fma2(p, x, both(0.0422820123f));
+        p = fma2(p, x, both(0.0705230784f));
+        p = fma2(p, x, both(1.0f));
+        p = mul2(p, p);
+        p = mul2(p, p);
+        p = mul2(p, p);
+        p = mul2(p, p);  // overflows to infinity far out: its reciprocal is 0
+        const F2 r{rcp_approx(p.x), rcp_approx(p.y)};
+        return fma2(mul2(az, both(-0.5f)), r, F2{z.x < 0.f ? 0.f : z.x, z.y < 0.f ? 0.f : z.y});
+    }
+    if (kAct == DUST_ACT_GELU_TANH)
+        return gated(z, mul2(z, fma2(mul2(z, z), both(-kGeluB * kLog2e), both(-kGeluA * kLog2e))));
+    if (kAct == DUST_ACT_SILU) return gated(z, mul2(z, both(-kLog2e)));
+    return F2{act_fn<kAct>(z.x), act_fn<kAct>(z.y)};
+}
 template <int kAct, int kN>
 __device__ __forceinline__ void act_all(float (&v)[kN]) {
 #pragma unroll
-    for (int j = 0; j < kN; ++j) v[j] = act_fn<kAct>(v[j]);
+    for (int j = 0; j < kN; j += 2) {
+        const F2 y = act_pair<kAct>(F2{v[j], v[j + 1]});
+        v[j] = y.x;
+        v[j + 1] = y.y;
+    }
 }
 template <int kN>
 __device__ __forceinline__ void act_block(int act, float (&v)[kN]) {
@@ -141,7 +190,7 @@ __global__ void __launch_bounds__(kRThreads) linear_rows_kernel(const __grid_con
         for (int r = 0; r < kRRows; ++r)
             w[r] = reinterpret_cast<const uint4*>(A.W + static_cast<int64_t>(o0 + r) * A.d_in);
         const int nv = A.d_in >> 3;
-#pragma unroll 2
+#pragma unroll(kTok == 1 ? 4 : 2)
         for (int v = share * 32 + lane; v < nv; v += A.split * 32) {
             uint4 ww[kRRows];
 #pragma unroll
@@ -245,6 +294,15 @@ struct GemmArgs {
     int k_blocks, per_split, splits, m_tiles, n_tiles;
 };
 
+// One thread of a converged warp.  The warps that issue TMA and MMAs take it in place of a lane test: with
+// it the compiler keeps descriptors in uniform registers (24 tokens 8192 -> 2048: 11.8 us from 15.9).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.u32 %0, 1, 0, P;\n\t}" : "=r"(p));
+    return p != 0;
+}
+__device__ __forceinline__ int warp_index() { return __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0); }
+
 struct Pipe {
     uint64_t *full, *empty, *acc_full, *acc_empty;
     uint32_t tmem;
@@ -328,20 +386,17 @@ __device__ __forceinline__ bool pipe_mma(const GemmArgs& A, const Pipe& P, uint3
         if (!mbar_wait_bounded(&P.full[s], (kc / S::kStages) & 1, A.ew, 502)) return false;
         tc_fence_after();
         const uint32_t a_addr = smem_u32(P.stages + s * S::kStageBytes);
-        const uint32_t b_addr = a_addr + kTerms * kABytes;
+        // K-major: 32 bytes along the swizzled row per instruction.  MN-major: 16 contraction rows of 128
+        // bytes; 8-row groups 1024 bytes apart, 64-element boxes kBox apart.  Descriptors count 16 bytes.
+        const uint64_t ad = sdesc_sw128(a_addr, kAmn ? kBox : 16, 1024);
+        const uint64_t bd = sdesc_sw128(a_addr + kTerms * kABytes, kBmn ? kBox : 16, 1024);
+        constexpr uint32_t kAStep = kAmn ? 2048 / 16 : 2, kBStep = kBmn ? 2048 / 16 : 2;
 #pragma unroll
-        for (int kk = 0; kk < kBK / 16; ++kk) {
-            // K-major: 32 bytes along the swizzled row per instruction.  MN-major: 16 contraction rows of 128
-            // bytes; 8-row groups 1024 bytes apart, 64-element boxes kBox apart
-            const uint64_t bd = kBmn ? sdesc_sw128(b_addr + kk * 2048, kBox, 1024)
-                                     : sdesc_sw128(b_addr + kk * 32, 16, 1024);
+        for (int kk = 0; kk < kBK / 16; ++kk)
 #pragma unroll
-            for (int t = 0; t < kTerms; ++t) {
-                const uint64_t ad = kAmn ? sdesc_sw128(a_addr + t * kABytes + kk * 2048, kBox, 1024)
-                                         : sdesc_sw128(a_addr + t * kABytes + kk * 32, 16, 1024);
-                umma_bf16(d, ad, bd, idesc, (kb > kb0 || kk > 0 || t > 0) ? 1u : 0u);
-            }
-        }
+            for (int t = 0; t < kTerms; ++t)
+                umma_bf16(d, ad + t * (kABytes / 16) + kk * kAStep, bd + kk * kBStep, idesc,
+                          (kb > kb0 || kk > 0 || t > 0) ? 1u : 0u);
         umma_commit(&P.empty[s]);
     }
     return true;
@@ -363,29 +418,38 @@ __device__ __forceinline__ void rows_out(uint8_t* buf, void* base, int64_t t0, i
                 *staged(buf, row, piece);
     }
 }
-__device__ __forceinline__ void rows_in(uint8_t* buf, const void* base, int64_t t0, int64_t M, int64_t pitch_b,
-                                        int64_t col_b, int64_t end_b, int lane) {
+// The other way, in two steps: four loads, and their values into shared memory.
+struct Rows {
     uint4 w[4];
+};
+__device__ __forceinline__ void rows_load(Rows& r, const void* base, int64_t t0, int64_t M, int64_t pitch_b, int64_t col_b,
+                                          int64_t end_b, int lane) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int row = (lane >> 2) + 8 * i, piece = lane & 3;
-        w[i] = make_uint4(0u, 0u, 0u, 0u);
+        r.w[i] = make_uint4(0u, 0u, 0u, 0u);
         if (t0 + row < M && col_b + 16 * piece < end_b)
-            w[i] = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(base) + (t0 + row) * pitch_b + col_b +
-                                                   16 * piece);
+            r.w[i] = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(base) + (t0 + row) * pitch_b + col_b +
+                                                     16 * piece);
     }
+}
+__device__ __forceinline__ void rows_stage(const Rows& r, uint8_t* buf, int lane) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) *staged(buf, (lane >> 2) + 8 * i, lane & 3) = w[i];
+    for (int i = 0; i < 4; ++i) *staged(buf, (lane >> 2) + 8 * i, lane & 3) = r.w[i];
 }
 
 // Bias, pre-activation, activation, residual and store of kN columns from o of the warp's rows t0 .. + 31 (lane:
-// row), chunk c of the warp's columns; bias: those of its columns 4 lane .. + 3.  kN = 32 for a bf16 y, 16 for an fp32 one: 64 bytes of a row.  kLayer false: no bias, z or activation.
+// row), chunk c of the warp's columns, which end at o_end; bias: those of its columns 4 lane .. + 3.  kN = 32 for a bf16 y, 16 for an fp32 one: 64 bytes of a row.  kLayer false: no bias, z or activation.
 // All lanes call it.
 template <int kN, bool kLayer>
-__device__ __forceinline__ void finish(const Epilogue& E, void* y, float (&v)[kN], int64_t t0, int o, uint8_t* sy,
-                                       uint8_t* sz, float4* sb, float4 bias, int c, int lane) {
+__device__ __forceinline__ void finish(const Epilogue& E, void* y, float (&v)[kN], int64_t t0, int o, int o_end, uint8_t* sy,
+                                       uint8_t* sz, float4* sb, float4 bias, Rows& res, int c, int lane) {
     constexpr int kEs = 64 / kN;  // bytes of an element of y
-    if (E.res) rows_in(sy, E.res, t0, E.M, E.ld_res * kEs, static_cast<int64_t>(o) * kEs, static_cast<int64_t>(E.n_out) * kEs, lane);
+    if (E.res) {  // this chunk's residual is here; the next one's is sent for
+        rows_stage(res, sy, lane);
+        rows_load(res, E.res, t0, E.M, E.ld_res * kEs, static_cast<int64_t>(o + kN) * kEs,
+                  static_cast<int64_t>(min(E.n_out, o_end)) * kEs, lane);
+    }
     if (kLayer && E.bias) {
         if (lane / (kN / 4) == c) sb[lane % (kN / 4)] = bias;
         __syncwarp();
@@ -462,13 +526,13 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_c
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
     const Pipe P = pipe_setup<kBN, kTerms>(smem, 8);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = warp_index(), lane = threadIdx.x & 31;
     const int tiles = A.m_tiles * A.n_tiles;
     const int items = tiles * A.splits;
     constexpr int kChunk = kPromote ? kFlush : 1 << 30;
 
     if (warp == 0) {
-        if (lane == 0) {
+        if (elect_one()) {
             prefetch_tensormap(&A.ta);
             prefetch_tensormap(&A.tb);
             uint32_t kc = 0;
@@ -480,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_c
             }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
+        if (elect_one()) {
             uint32_t kc = 0;
             uint32_t ci = 0;  // chunks so far: chunk ci goes to accumulator ci mod 2
             bool ok = true;
@@ -528,6 +592,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_c
             float4 bias = make_float4(0.f, 0.f, 0.f, 0.f);  // on its way before the wait for the tile
             if (!kBmn && A.e.bias && 4 * lane < kCols && o0 + 4 * lane < A.e.n_out)
                 bias = __ldg(reinterpret_cast<const float4*>(A.e.bias + o0) + lane);
+            Rows res;
+            if (!kPromote && A.e.res)
+                rows_load(res, A.e.res, t0, A.e.M, A.e.ld_res * 2, static_cast<int64_t>(o0) * 2,
+                          static_cast<int64_t>(min(A.e.n_out, o0 + kCols)) * 2, lane);
             if (kPromote) {
                 float acc[kCols];
 #pragma unroll
@@ -552,13 +620,16 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_c
                     release(buf);
                 }
                 if (!ok) break;
+                if (A.e.res)
+                    rows_load(res, A.e.res, t0, A.e.M, A.e.ld_res * 4, static_cast<int64_t>(o0) * 4,
+                              static_cast<int64_t>(min(A.e.n_out, o0 + kCols)) * 4, lane);
 #pragma unroll
                 for (int c = 0; c < kCols / 16; ++c) {
                     if (o0 + c * 16 < A.e.n_out) {  // uniform over the warp
                         float v[16];
 #pragma unroll
                         for (int j = 0; j < 16; ++j) v[j] = acc[c * 16 + j];
-                        finish<16, !kBmn>(A.e, y, v, t0, o0 + c * 16, sy, sz, sb, bias, c, lane);
+                        finish<16, !kBmn>(A.e, y, v, t0, o0 + c * 16, o0 + kCols, sy, sz, sb, bias, res, c, lane);
                     }
                 }
             } else {
@@ -584,7 +655,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_c
                     } else {
                         release(buf);
                     }
-                    finish<32, !kBmn>(A.e, y, v, t0, o0 + c * 32, sy, sz, sb, bias, c, lane);
+                    finish<32, !kBmn>(A.e, y, v, t0, o0 + c * 32, o0 + kCols, sy, sz, sb, bias, res, c, lane);
                     if (c + 1 < cnt) tmem_wait_ld32(next);
                 }
                 if (cnt == 0) release(buf);
@@ -597,100 +668,160 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_c
     if (warp == 1) tmem_dealloc(P.tmem, S::kTmemCols);
 }
 
-// Few tiles: 128 x 64 tiles whose contraction is cut over the CTAs of a cluster.  Each CTA sums its share as
-// the persistent kernel does, sends its sums to the CTAs that own their columns (64 / S of them each) through
-// distributed shared memory, and each owner adds the S shares in rank order and runs the epilogue.
-constexpr int kCBN = 64;
+// Few tokens, more than a handful: W streams through the tensor cores as the operand of 128 rows (output
+// channels), against up to kTok tokens as the columns, and the contraction is cut over the CTAs of a cluster.
+// Each CTA sums its share as the persistent kernel does, sends its sums to the CTAs that own their channels
+// (128 / ranks of them each) through distributed shared memory, and each owner adds the shares in rank
+// order and runs the epilogue.  (With the tokens as the 128 rows and 64 channels as columns an MMA moves half
+// of W: 344 ns a block of 64, which an SM could load in 186.)
+template <int kTok>
+struct CShape {
+    static constexpr uint32_t kXBytes = kTok * 128;
+    static constexpr uint32_t kStageBytes = kABytes + kXBytes;
+    static constexpr uint32_t kStaging = kBM * kTok * 4;  // the shares of one owner
+    static constexpr int kFit = static_cast<int>((225 * 1024 - kStaging) / kStageBytes);
+    static constexpr int kStages = kFit < 10 ? kFit : 10;
+    static constexpr uint32_t kSmem = kStages * kStageBytes + kStaging + 1024 + 512;
+    static constexpr uint32_t kTmemCols = 2 * kTok;
+};
+static_assert(CShape<128>::kSmem <= 227 * 1024 && CShape<64>::kSmem <= 227 * 1024 && CShape<32>::kSmem <= 227 * 1024,
+              "exceeds shared memory");
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 
-__global__ void __launch_bounds__(kThreads, 1) linear_cluster_kernel(const __grid_constant__ GemmArgs A) {
-    using S = Shape<kCBN, 1>;
+// GemmArgs: ta is W (64 x 128 boxes), tb is x (64 x kTok), m tiles are of channels and n tiles of tokens.
+template <int kTok>
+__global__ void __launch_bounds__(kThreads, 1) linear_tokens_kernel(const __grid_constant__ GemmArgs A) {
+    using S = CShape<kTok>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
-    const Pipe P = pipe_setup<kCBN, 1>(smem, 8);
+    float* staging = reinterpret_cast<float*>(smem + S::kStages * S::kStageBytes);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::kStages * S::kStageBytes + S::kStaging);
+    uint64_t* empty = full + S::kStages;
+    uint64_t* acc_full = empty + S::kStages;
+    uint64_t* acc_empty = acc_full + 2;
+    uint32_t* slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
+    const int warp = warp_index(), lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S::kStages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&acc_full[b], 1);
+            mbar_init(&acc_empty[b], 8);
+        }
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(slot, S::kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *slot;
     cluster_arrive();  // waited for before the first remote store: the peers are running by then
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int ranks = A.splits, rank = static_cast<int>(blockIdx.x) % ranks;
-    const int n0 = static_cast<int>(blockIdx.x) / ranks * kCBN;
-    const int m0 = static_cast<int>(blockIdx.y) * kBM;
+    const int o0 = static_cast<int>(blockIdx.x) / ranks * kBM;
+    const int t0 = static_cast<int>(blockIdx.y) * kTok;
     const int kb0 = min(A.k_blocks, rank * A.per_split), kb1 = min(A.k_blocks, kb0 + A.per_split);
-    const int w = kCBN / ranks;  // columns that a rank owns: 8, 16, 32 or 64
-    float acc[kCBN / 2];
+    const int w = kBM / ranks;  // channels that a rank owns: 16, 32, 64 or 128
+    constexpr int kHalf = kTok / 2;
+    float acc[kHalf];  // epilogue warps: channel q 32 + lane, tokens hf kHalf ..
+    const int q = warp & 3, hf = (warp - 2) >> 2;
     if (warp == 0) {
-        if (lane == 0) {
+        if (elect_one()) {
             prefetch_tensormap(&A.ta);
             prefetch_tensormap(&A.tb);
-            uint32_t kc = 0;
-            pipe_load<kCBN, false, false, 1>(A, P, m0, n0, kb0, kb1, kc);
+            for (int kb = kb0; kb < kb1; ++kb) {
+                const int i = kb - kb0, s = i % S::kStages;
+                if (i >= S::kStages && !mbar_wait_bounded(&empty[s], ((i / S::kStages) - 1) & 1, A.ew, 511)) break;
+                uint8_t* a = smem + s * S::kStageBytes;
+                mbar_arrive_expect_tx(&full[s], S::kStageBytes);
+                tma_load_2d(a, &A.ta, &full[s], kb * kBK, o0);
+                tma_load_2d(a + kABytes, &A.tb, &full[s], kb * kBK, t0);
+            }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            uint32_t kc = 0, ci = 0;
+        if (elect_one()) {
+            constexpr uint32_t idesc = idesc_bf16_f32(kBM, kTok, 0, 0);
+            uint32_t ci = 0;
             bool ok = true;
             for (int k = kb0; k < kb1 && ok; k += kFlush, ++ci) {
                 const uint32_t buf = ci & 1;
-                if (ci >= 2 && !mbar_wait_bounded(&P.acc_empty[buf], ((ci >> 1) - 1) & 1, A.ew, 513)) break;
+                if (ci >= 2 && !mbar_wait_bounded(&acc_empty[buf], ((ci >> 1) - 1) & 1, A.ew, 513)) break;
                 tc_fence_after();
-                ok = pipe_mma<kCBN, false, false, 1>(A, P, P.tmem + buf * kCBN, k, min(kb1, k + kFlush), kc);
-                umma_commit(&P.acc_full[buf]);
+                for (int kb = k; kb < min(kb1, k + kFlush); ++kb) {
+                    const int i = kb - kb0, s = i % S::kStages;
+                    if (!mbar_wait_bounded(&full[s], (i / S::kStages) & 1, A.ew, 512)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t a_addr = smem_u32(smem + s * S::kStageBytes);
+                    const uint64_t ad = sdesc_sw128(a_addr, 16, 1024), bd = sdesc_sw128(a_addr + kABytes, 16, 1024);
+#pragma unroll
+                    for (int kk = 0; kk < kBK / 16; ++kk)
+                        umma_bf16(tmem + buf * kTok, ad + 2 * kk, bd + 2 * kk, idesc, (kb > k || kk > 0) ? 1u : 0u);
+                    umma_commit(&empty[s]);
+                }
+                umma_commit(&acc_full[buf]);
             }
         }
     } else {
-        const int q = warp & 3, hf = (warp - 2) >> 2;
 #pragma unroll
-        for (int j = 0; j < kCBN / 2; ++j) acc[j] = 0.f;
+        for (int j = 0; j < kHalf; ++j) acc[j] = 0.f;
         uint32_t ci = 0;
         for (int k = kb0; k < kb1; k += kFlush, ++ci) {
             const uint32_t buf = ci & 1;
-            if (!mbar_wait_bounded(&P.acc_full[buf], (ci >> 1) & 1, A.ew, 514)) break;
+            if (!mbar_wait_bounded(&acc_full[buf], (ci >> 1) & 1, A.ew, 514)) break;
             __syncwarp();
             tc_fence_after();
-            float v[32];
-            tmem_ld32(P.tmem + buf * kCBN + hf * 32 + (static_cast<uint32_t>(q * 32) << 16), v);
-            tmem_wait_ld32(v);
+            const uint32_t at = tmem + buf * kTok + hf * kHalf + (static_cast<uint32_t>(q * 32) << 16);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) acc[j] += v[j];
+            for (int c = 0; c < kHalf / 8; ++c) {
+                float v[8];
+                tmem_ld8(at + c * 8, v);
+                tmem_wait_ld8(v);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) acc[c * 8 + j] += v[j];
+            }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&P.acc_empty[buf]);
+            if (lane == 0) mbar_arrive(&acc_empty[buf]);
         }
     }
     __syncwarp();
     cluster_wait();
+    const int tokens = static_cast<int>(min(static_cast<int64_t>(kTok), A.e.M - t0));
     if (warp >= 2) {
-        const int q = warp & 3, hf = (warp - 2) >> 2;
-        const int row = q * 32 + lane;
-        if (m0 + row < A.e.M) {
-            const uint32_t mine = smem_u32(P.staging);
+        // share [rank][token][channel of the owner]: a warp's lanes write consecutive channels
+        const int ch = q * 32 + lane, owner = ch / w;
+        const uint32_t mine = smem_u32(staging + (rank * kTok + hf * kHalf) * w + (ch - owner * w));
+        uint32_t remote;
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(mine), "r"(owner));
 #pragma unroll
-            for (int j = 0; j < 32; j += 4) {
-                const int col = hf * 32 + j, owner = col / w;
-                const uint32_t at = mine + static_cast<uint32_t>((rank * kBM + row) * w + (col - owner * w)) * 4u;
-                uint32_t remote;
-                asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(at), "r"(owner));
-                asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(remote), "f"(acc[j]),
-                             "f"(acc[j + 1]), "f"(acc[j + 2]), "f"(acc[j + 3])
+        for (int j = 0; j < kHalf; ++j)
+            if (hf * kHalf + j < tokens)
+                asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(remote + static_cast<uint32_t>(j * w * 4)), "f"(acc[j])
                              : "memory");
-            }
-        }
     }
     cluster_arrive();
     cluster_wait();
-    // this CTA's columns n0 + rank w .. + w - 1 of the tile's rows, four columns a thread
-    const float* part = reinterpret_cast<const float*>(P.staging);
-    const int rows = static_cast<int>(min(static_cast<int64_t>(kBM), A.e.M - m0)), quads = w / 4;
-    for (int e = threadIdx.x; e < rows * quads; e += kThreads) {
+    // this CTA's channels o0 + rank w .. + w - 1 of the tile's tokens, four channels a thread
+    const int quads = w / 4;
+    for (int e = threadIdx.x; e < tokens * quads; e += kThreads) {
         const int row = e / quads, c = 4 * (e - row * quads);
-        const int o = n0 + rank * w + c;
+        const int o = o0 + rank * w + c;
         if (o >= A.e.n_out) continue;  // n_out is a multiple of 16
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int k = 0; k < ranks; ++k) {
-            const float4 v = *reinterpret_cast<const float4*>(part + (k * kBM + row) * w + c);
+            const float4 v = *reinterpret_cast<const float4*>(staging + (k * kTok + row) * w + c);
             a = make_float4(a.x + v.x, a.y + v.y, a.z + v.z, a.w + v.w);
         }
-        const int64_t t = m0 + row;
+        const int64_t t = t0 + row;
         if (A.e.bias) {
             const float4 b = __ldg(reinterpret_cast<const float4*>(A.e.bias + o));
             a = make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
@@ -716,9 +847,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_cluster_kernel(const __gri
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 1) tmem_dealloc(P.tmem, S::kTmemCols);
+    if (warp == 1) tmem_dealloc(tmem, S::kTmemCols);
 }
-static_assert(kBM * kCBN * 4 <= kStaging, "the shares of one owner");
 
 // out (+)= the sum of S partials in order, four elements a thread.
 __global__ void __launch_bounds__(256) linear_join_kernel(const float4* __restrict__ part, int S, int64_t n4, float4* out,
@@ -860,12 +990,10 @@ dust_status launch_gemm(const GemmArgs& A, cudaStream_t s) {
 
 // Output tile width: the one whose waves of tiles over the SMs cost least, a tile of 128 x bn taking
 // about as long as the larger of its MMAs (bn) and its operand loads (bn + 128, at 0.6 each).
-// The registers of an fp32 output's sums limit its tiles to 128 columns.
-int choose_bn(int64_t m_tiles, int n_out, bool f32) {
+int choose_bn(int64_t m_tiles, int n_out) {
     int best = 0;
     double least = 0;
     for (int bn : {256, 128, 64}) {
-        if (bn == 256 && f32) continue;
         const int64_t tiles = m_tiles * ((n_out + bn - 1) / bn);
         const double cost = static_cast<double>((tiles + num_sms() - 1) / num_sms()) *
                             std::max<double>(bn, 0.6 * (bn + 128));
@@ -879,26 +1007,17 @@ int choose_bn(int64_t m_tiles, int n_out, bool f32) {
 
 template <bool kBmn, int kTerms, bool kPromote>
 dust_status launch_width(int bn, const GemmArgs& A, cudaStream_t s) {
-    if constexpr (!kPromote)
-        if (bn == 256) return launch_gemm<256, false, kBmn, kTerms, kPromote>(A, s);
-    return bn >= 128 ? launch_gemm<128, false, kBmn, kTerms, kPromote>(A, s)
-                     : launch_gemm<64, false, kBmn, kTerms, kPromote>(A, s);
+    return bn == 256   ? launch_gemm<256, false, kBmn, kTerms, kPromote>(A, s)
+           : bn == 128 ? launch_gemm<128, false, kBmn, kTerms, kPromote>(A, s)
+                       : launch_gemm<64, false, kBmn, kTerms, kPromote>(A, s);
 }
 
-// Ranks that share a tile's contraction: while the tiles fill at most half of the SMs and each rank keeps
-// two blocks of 64.  0: there are tiles enough without.
-int cluster_ranks(int64_t tiles, int k_blocks) {
-    if (tiles * 2 > num_sms()) return 0;
-    int r = 1;
-    while (r < 8 && tiles * r * 2 <= num_sms() && k_blocks >= 4 * r) r *= 2;
-    return r;
-}
-
-dust_status launch_cluster(const GemmArgs& A, cudaStream_t s) {
-    using S = Shape<kCBN, 1>;
+template <int kTok>
+dust_status launch_tokens(const GemmArgs& A, cudaStream_t s) {
+    using S = CShape<kTok>;
     static PerContextOnce attr;
     if (!attr.run([] {
-            return cudaFuncSetAttribute(linear_cluster_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+            return cudaFuncSetAttribute(linear_tokens_kernel<kTok>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                         static_cast<int>(S::kSmem)) == cudaSuccess;
         }))
         return DUST_ERR_CUDA;
@@ -908,13 +1027,44 @@ dust_status launch_cluster(const GemmArgs& A, cudaStream_t s) {
     at.val.clusterDim.y = 1;
     at.val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(A.n_tiles * A.splits), static_cast<unsigned>(A.m_tiles), 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(A.m_tiles * A.splits), static_cast<unsigned>(A.n_tiles), 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
     cfg.dynamicSmemBytes = S::kSmem;
     cfg.stream = s;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, linear_cluster_kernel, A) == cudaSuccess ? DUST_OK : DUST_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, linear_tokens_kernel<kTok>, A) == cudaSuccess ? DUST_OK : DUST_ERR_CUDA;
+}
+
+// Whether the outputs are few enough for linear_tokens_kernel: at most as many 128-channel tiles as SMs.
+bool few_tiles(int64_t N, int n_out) {
+    return (N + 127) / 128 * ((n_out + kBM - 1) / kBM) <= num_sms();
+}
+
+dust_status gemm_tokens(const void* x, int64_t ld_x, int K, const void* W, GemmArgs& G, cudaStream_t s) {
+    const int64_t N = G.e.M;
+    const int n_out = G.e.n_out;
+    const int tok = N <= 16 ? 16 : N <= 32 ? 32 : N <= 64 ? 64 : 128;
+    G.ew = device_error_word();
+    G.k_blocks = (K + kBK - 1) / kBK;
+    G.m_tiles = (n_out + kBM - 1) / kBM;
+    G.n_tiles = static_cast<int>((N + tok - 1) / tok);
+    // ranks that share a tile's contraction, as many as there are SMs for while each keeps two blocks of 64
+    const int64_t tiles = static_cast<int64_t>(G.m_tiles) * G.n_tiles;
+    int r = 1;
+    while (r < 4 && tiles * r * 2 <= num_sms() && G.k_blocks >= 4 * r) r *= 2;
+    G.splits = r;
+    G.per_split = (G.k_blocks + r - 1) / r;
+    if (!make_tmap_bf16_2d_ld(&G.ta, W, n_out, K, K, kBM, kBK) ||
+        !make_tmap_bf16_2d_ld(&G.tb, x, static_cast<uint64_t>(N), K, ld_x, tok, kBK))
+        return DUST_ERR_CUDA;
+    prof_begin(s);
+    const dust_status st = tok == 16   ? launch_tokens<16>(G, s)
+                           : tok == 32 ? launch_tokens<32>(G, s)
+                           : tok == 64 ? launch_tokens<64>(G, s)
+                                       : launch_tokens<128>(G, s);
+    prof_end(s, "linear_tokens_tcgen05");
+    return st;
 }
 
 // y [M, n_out] = A [terms M, K] B with the epilogue of G.e; B K-major [n_out, K] or MN-major [K, n_out].
@@ -923,8 +1073,7 @@ dust_status gemm_rows(const void* a, int64_t ld_a, int terms, int K, const void*
     const int64_t M = G.e.M;
     const int n_out = G.e.n_out;
     const int64_t m_tiles = (M + kBM - 1) / kBM;
-    const int ranks = b_mn ? 0 : cluster_ranks(m_tiles * ((n_out + kCBN - 1) / kCBN), (K + kBK - 1) / kBK);
-    const int bn = ranks ? kCBN : choose_bn(m_tiles, n_out, !G.e.out_bf16);
+    const int bn = choose_bn(m_tiles, n_out);
     G.ew = device_error_word();
     G.term_rows = M;
     G.split_elems = 0;
@@ -940,11 +1089,7 @@ dust_status gemm_rows(const void* a, int64_t ld_a, int terms, int K, const void*
         return DUST_ERR_CUDA;
     prof_begin(s);
     dust_status st;
-    if (ranks) {
-        G.splits = ranks;
-        G.per_split = (G.k_blocks + ranks - 1) / ranks;
-        st = launch_cluster(G, s);
-    } else if (b_mn)
+    if (b_mn)
         st = G.e.out_bf16 ? launch_width<true, 1, false>(bn, G, s)
              : terms == 2 ? launch_width<true, 2, true>(bn, G, s)
                           : launch_width<true, 1, true>(bn, G, s);
@@ -1042,7 +1187,7 @@ size_t db_bytes(int64_t N, int32_t d_out) {
 }
 
 // Tokens up to which W is streamed through the CUDA cores.
-constexpr int kFewTokens = 8;
+constexpr int kFewTokens = 2;
 
 template <int kTok>
 void launch_rows(const RowsArgs& A, unsigned blocks, cudaStream_t s) {
@@ -1080,7 +1225,8 @@ dust_status linear_launch(const void* x, int64_t ld_x, const void* W, const floa
     }
     GemmArgs G{};
     G.e = Epilogue{bias, res, y, static_cast<__nv_bfloat16*>(z), N, ld_res, ld_y, ld_z, d_out, act, out_bf16};
-    const dust_status st = gemm_rows(x, ld_x, 1, d_in, W, false, G, "linear_tcgen05", s);
+    const dust_status st = few_tiles(N, d_out) ? gemm_tokens(x, ld_x, d_in, W, G, s)
+                                               : gemm_rows(x, ld_x, 1, d_in, W, false, G, "linear_tcgen05", s);
     if (st != DUST_OK) return st;
     return cudaGetLastError() == cudaSuccess ? DUST_OK : DUST_ERR_CUDA;
 }
