@@ -265,15 +265,17 @@ constexpr uint32_t kStaging = 8 * (kWarpStaging + 128);
 // rounding is 200 times the largest error of K = 8192, and it is not.
 constexpr int kFlush = 8;
 
-template <int kBN, int kTerms>
+template <int kBN, int kTerms, bool kPair>
 struct Shape {
-    static constexpr uint32_t kBBytes = kBN * kBK * 2;
+    static constexpr uint32_t kBBytes = (kPair ? kBN / 2 : kBN) * kBK * 2;
     static constexpr uint32_t kStageBytes = kTerms * kABytes + kBBytes;
     static constexpr int kStages = static_cast<int>(192 * 1024 / kStageBytes);
     static constexpr uint32_t kSmem = kStages * kStageBytes + kStaging + 1024 + 256;
     static constexpr uint32_t kTmemCols = 2 * kBN;
 };
-static_assert(Shape<256, 1>::kSmem <= 227 * 1024 && Shape<256, 2>::kSmem <= 227 * 1024, "exceeds shared memory");
+static_assert(Shape<256, 1, false>::kSmem <= 227 * 1024 && Shape<256, 2, true>::kSmem <= 227 * 1024 &&
+                  Shape<256, 1, true>::kSmem <= 227 * 1024,
+              "exceeds shared memory");
 
 struct Epilogue {
     const float* bias;
@@ -310,10 +312,68 @@ struct Pipe {
     uint8_t* staging;
 };
 
+// With kPair two CTAs (a cluster, on neighbouring SMs) work on one 256-row tile: each holds its 128 rows of A and of
+// the sums, and half of B's columns, so that an SM loads 32 KB a block where one alone loads 48.  The even CTA
+// issues the MMAs for both; its full barriers take the bytes of both CTAs' loads, its commits free the
+// stages and announce the sums in both.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+__device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* map, uint32_t bar, int32_t x, int32_t y) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
+        : "memory");
+}
+__device__ __forceinline__ void umma_bf16_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                               uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// Arrives on `bar` of this CTA, or of both CTAs of the pair.
+template <bool kPair>
+__device__ __forceinline__ void commit(uint64_t* bar) {
+    if (kPair)
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                smem_u32(bar)),
+            "h"(static_cast<uint16_t>(3))
+            : "memory");
+    else
+        umma_commit(bar);
+}
+template <bool kPair>
+__device__ __forceinline__ void tmem_get(uint32_t* slot, uint32_t cols) {
+    if (kPair) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(cols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+        tmem_alloc(slot, cols);
+        tmem_relinquish();
+    }
+}
+template <bool kPair>
+__device__ __forceinline__ void tmem_free(uint32_t tmem, uint32_t cols) {
+    if (kPair)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(cols) : "memory");
+    else
+        tmem_dealloc(tmem, cols);
+}
+
 // Barriers, tensor memory; every thread of the CTA calls it.
-template <int kBN, int kTerms>
+template <int kBN, int kTerms, bool kPair>
 __device__ __forceinline__ Pipe pipe_setup(uint8_t* smem, int epilogue_warps) {
-    using S = Shape<kBN, kTerms>;
+    using S = Shape<kBN, kTerms, kPair>;
     Pipe P;
     P.stages = smem;
     P.staging = smem + S::kStages * S::kStageBytes;
@@ -329,58 +389,67 @@ __device__ __forceinline__ Pipe pipe_setup(uint8_t* smem, int epilogue_warps) {
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&P.acc_full[b], 1);
-            mbar_init(&P.acc_empty[b], epilogue_warps);
+            mbar_init(&P.acc_empty[b], epilogue_warps * (kPair ? 2 : 1));
         }
         fence_barrier_init();
     }
-    if (threadIdx.x >> 5 == 1) {
-        tmem_alloc(slot, S::kTmemCols);
-        tmem_relinquish();
-    }
+    if (threadIdx.x >> 5 == 1) tmem_get<kPair>(slot, S::kTmemCols);
     tc_fence_before();
     __syncthreads();
+    if (kPair) {  // both CTAs' barriers and tensor memory exist
+        cluster_arrive();
+        cluster_wait();
+    }
     tc_fence_after();
     P.tmem = *slot;
     return P;
 }
 
-// One thread: loads blocks [kb0, kb1) of tile (m0, n0) into the ring; kc counts blocks over the CTA's life.
-template <int kBN, bool kAmn, bool kBmn, int kTerms>
-__device__ __forceinline__ bool pipe_load(const GemmArgs& A, const Pipe& P, int m0, int n0, int kb0, int kb1,
+// One thread: loads blocks [kb0, kb1) of tile (m0, n0) into the ring; kc counts blocks over the CTA's life.  m0
+// and n0 are this CTA's own first rows; `lead`: it is the pair's even CTA.
+template <int kBN, bool kAmn, bool kBmn, int kTerms, bool kPair>
+__device__ __forceinline__ bool pipe_load(const GemmArgs& A, const Pipe& P, int m0, int n0, int kb0, int kb1, bool lead,
                                           uint32_t& kc) {
-    using S = Shape<kBN, kTerms>;
+    using S = Shape<kBN, kTerms, kPair>;
     for (int kb = kb0; kb < kb1; ++kb, ++kc) {
         const int s = kc % S::kStages;
         if (kc >= S::kStages && !mbar_wait_bounded(&P.empty[s], ((kc / S::kStages) - 1) & 1, A.ew, 501)) return false;
         uint8_t* a = P.stages + s * S::kStageBytes;
         uint8_t* b = a + kTerms * kABytes;
         const int k0 = kb * kBK;
-        mbar_arrive_expect_tx(&P.full[s], S::kStageBytes);
+        if (!kPair || lead) mbar_arrive_expect_tx(&P.full[s], S::kStageBytes * (kPair ? 2 : 1));
+        const uint32_t bar = kPair ? cluster_addr(&P.full[s], 0) : 0u;
+        auto load = [&](uint8_t* dst, const CUtensorMap* map, int x, int y) {
+            if (kPair)
+                tma_load_2d_pair(dst, map, bar, x, y);
+            else
+                tma_load_2d(dst, map, &P.full[s], x, y);
+        };
 #pragma unroll
         for (int t = 0; t < kTerms; ++t) {
             const int32_t off = t ? static_cast<int32_t>(A.term_rows) : 0;
             if (kAmn) {
-                tma_load_2d(a + t * kABytes, &A.ta, &P.full[s], m0, off + k0);
-                tma_load_2d(a + t * kABytes + kBox, &A.ta, &P.full[s], m0 + 64, off + k0);
+                load(a + t * kABytes, &A.ta, m0, off + k0);
+                load(a + t * kABytes + kBox, &A.ta, m0 + 64, off + k0);
             } else {
-                tma_load_2d(a + t * kABytes, &A.ta, &P.full[s], k0, off + m0);
+                load(a + t * kABytes, &A.ta, k0, off + m0);
             }
         }
         if (kBmn) {
 #pragma unroll
-            for (int j = 0; j < kBN / 64; ++j) tma_load_2d(b + j * kBox, &A.tb, &P.full[s], n0 + 64 * j, k0);
+            for (int j = 0; j < (kPair ? kBN / 2 : kBN) / 64; ++j) load(b + j * kBox, &A.tb, n0 + 64 * j, k0);
         } else {
-            tma_load_2d(b, &A.tb, &P.full[s], k0, n0);
+            load(b, &A.tb, k0, n0);
         }
     }
     return true;
 }
 
 // One thread: the MMAs of blocks [kb0, kb1) into accumulator columns d.
-template <int kBN, bool kAmn, bool kBmn, int kTerms>
+template <int kBN, bool kAmn, bool kBmn, int kTerms, bool kPair>
 __device__ __forceinline__ bool pipe_mma(const GemmArgs& A, const Pipe& P, uint32_t d, int kb0, int kb1, uint32_t& kc) {
-    using S = Shape<kBN, kTerms>;
-    constexpr uint32_t idesc = idesc_bf16_f32(kBM, kBN, kAmn ? 1 : 0, kBmn ? 1 : 0);
+    using S = Shape<kBN, kTerms, kPair>;
+    constexpr uint32_t idesc = idesc_bf16_f32(kPair ? 2 * kBM : kBM, kBN, kAmn ? 1 : 0, kBmn ? 1 : 0);
     for (int kb = kb0; kb < kb1; ++kb, ++kc) {
         const int s = kc % S::kStages;
         if (!mbar_wait_bounded(&P.full[s], (kc / S::kStages) & 1, A.ew, 502)) return false;
@@ -394,10 +463,14 @@ __device__ __forceinline__ bool pipe_mma(const GemmArgs& A, const Pipe& P, uint3
 #pragma unroll
         for (int kk = 0; kk < kBK / 16; ++kk)
 #pragma unroll
-            for (int t = 0; t < kTerms; ++t)
-                umma_bf16(d, ad + t * (kABytes / 16) + kk * kAStep, bd + kk * kBStep, idesc,
-                          (kb > kb0 || kk > 0 || t > 0) ? 1u : 0u);
-        umma_commit(&P.empty[s]);
+            for (int t = 0; t < kTerms; ++t) {
+                const uint32_t more = (kb > kb0 || kk > 0 || t > 0) ? 1u : 0u;
+                if (kPair)
+                    umma_bf16_pair(d, ad + t * (kABytes / 16) + kk * kAStep, bd + kk * kBStep, idesc, more);
+                else
+                    umma_bf16(d, ad + t * (kABytes / 16) + kk * kAStep, bd + kk * kBStep, idesc, more);
+            }
+        commit<kPair>(&P.empty[s]);
     }
     return true;
 }
@@ -519,14 +592,17 @@ __device__ __forceinline__ void tile_of(int tile, int m_tiles, int n_tiles, int&
 
 // Persistent: one CTA per SM walks (tile, split) items; each accumulator (two of them) is read by the
 // epilogue warps while the MMAs fill the other.  kPromote: see kFlush.
-template <int kBN, bool kAmn, bool kBmn, int kTerms, bool kPromote>
+template <int kBN, bool kAmn, bool kBmn, int kTerms, bool kPromote, bool kPair>
 __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_constant__ GemmArgs A) {
-    using S = Shape<kBN, kTerms>;
+    using S = Shape<kBN, kTerms, kPair>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
-    const Pipe P = pipe_setup<kBN, kTerms>(smem, 8);
+    const Pipe P = pipe_setup<kBN, kTerms, kPair>(smem, 8);
     const int warp = warp_index(), lane = threadIdx.x & 31;
+    const int rank = kPair ? static_cast<int>(blockIdx.x & 1) : 0;  // the clusters are CTAs 2 i, 2 i + 1
+    const int first = kPair ? static_cast<int>(blockIdx.x >> 1) : static_cast<int>(blockIdx.x);
+    const int step = kPair ? static_cast<int>(gridDim.x >> 1) : static_cast<int>(gridDim.x);
     const int tiles = A.m_tiles * A.n_tiles;
     const int items = tiles * A.splits;
     constexpr int kChunk = kPromote ? kFlush : 1 << 30;
@@ -536,19 +612,26 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_c
             prefetch_tensormap(&A.ta);
             prefetch_tensormap(&A.tb);
             uint32_t kc = 0;
-            for (int it = blockIdx.x; it < items; it += gridDim.x) {
+            for (int it = first; it < items; it += step) {
                 int m, n;
                 tile_of(it % tiles, A.m_tiles, A.n_tiles, m, n);
                 const int kb0 = it / tiles * A.per_split, kb1 = min(A.k_blocks, kb0 + A.per_split);
-                if (!pipe_load<kBN, kAmn, kBmn, kTerms>(A, P, m * kBM, n * kBN, kb0, kb1, kc)) break;
+                const int m0 = kPair ? (2 * m + rank) * kBM : m * kBM;
+                const int n0 = n * kBN + (kPair ? rank * (kBN / 2) : 0);
+                if (!pipe_load<kBN, kAmn, kBmn, kTerms, kPair>(A, P, m0, n0, kb0, kb1, rank == 0, kc)) break;
+            }
+            if (kPair) {
+                // the commits that free the last stages arrive here too: not before this CTA ends
+                for (uint32_t c = kc > S::kStages ? kc - S::kStages : 0; c < kc; ++c)
+                    if (!mbar_wait_bounded(&P.empty[c % S::kStages], (c / S::kStages) & 1, A.ew, 506)) break;
             }
         }
     } else if (warp == 1) {
-        if (elect_one()) {
+        if (rank == 0 && elect_one()) {
             uint32_t kc = 0;
             uint32_t ci = 0;  // chunks so far: chunk ci goes to accumulator ci mod 2
             bool ok = true;
-            for (int it = blockIdx.x; it < items && ok; it += gridDim.x) {
+            for (int it = first; it < items && ok; it += step) {
                 const int kb0 = it / tiles * A.per_split, kb1 = min(A.k_blocks, kb0 + A.per_split);
                 for (int k = kb0; k < kb1 && ok; ++ci) {
                     const int k2 = kb1 - k > kChunk ? k + kChunk : kb1;
@@ -559,8 +642,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_c
                         break;
                     }
                     tc_fence_after();
-                    ok = pipe_mma<kBN, kAmn, kBmn, kTerms>(A, P, P.tmem + buf * kBN, k, k2, kc);
-                    umma_commit(&P.acc_full[buf]);
+                    ok = pipe_mma<kBN, kAmn, kBmn, kTerms, kPair>(A, P, P.tmem + buf * kBN, k, k2, kc);
+                    commit<kPair>(&P.acc_full[buf]);
                     k = k2;
                 }
             }
@@ -577,16 +660,23 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_c
         auto release = [&](uint32_t buf) {  // the warp has read its part of the accumulator: it may be refilled
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&P.acc_empty[buf]);
+            if (lane == 0) {
+                if (kPair)
+                    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+                                     cluster_addr(&P.acc_empty[buf], 0))
+                                 : "memory");
+                else
+                    mbar_arrive(&P.acc_empty[buf]);
+            }
         };
         uint32_t ci = 0;
         bool ok = true;
-        for (int it = blockIdx.x; it < items && ok; it += gridDim.x) {
+        for (int it = first; it < items && ok; it += step) {
             int m, n;
             tile_of(it % tiles, A.m_tiles, A.n_tiles, m, n);
             const int split = it / tiles;
             const int kb0 = split * A.per_split, kb1 = min(A.k_blocks, kb0 + A.per_split);
-            const int64_t t0 = static_cast<int64_t>(m) * kBM + q * 32;
+            const int64_t t0 = static_cast<int64_t>(kPair ? 2 * m + rank : m) * kBM + q * 32;
             const int o0 = n * kBN + hf * kCols;
             void* y = static_cast<uint8_t*>(A.e.y) + split * A.split_elems * (A.e.out_bf16 ? 2 : 4);
             float4 bias = make_float4(0.f, 0.f, 0.f, 0.f);  // on its way before the wait for the tile
@@ -665,7 +755,11 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_c
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 1) tmem_dealloc(P.tmem, S::kTmemCols);
+    if (kPair) {  // the pair's MMAs, commits and arrivals are over
+        cluster_arrive();
+        cluster_wait();
+    }
+    if (warp == 1) tmem_free<kPair>(P.tmem, S::kTmemCols);
 }
 
 // Few tokens, more than a handful: W streams through the tensor cores as the operand of 128 rows (output
@@ -686,8 +780,6 @@ struct CShape {
 };
 static_assert(CShape<128>::kSmem <= 227 * 1024 && CShape<64>::kSmem <= 227 * 1024 && CShape<32>::kSmem <= 227 * 1024,
               "exceeds shared memory");
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 
 // GemmArgs: ta is W (64 x 128 boxes), tb is x (64 x kTok), m tiles are of channels and n tiles of tokens.
 template <int kTok>
@@ -972,19 +1064,36 @@ __global__ void __launch_bounds__(256) linear_db_kernel(const float* part, int c
 }
 
 // ------------------------------------------------------------------ host side
-template <int kBN, bool kAmn, bool kBmn, int kTerms, bool kPromote>
+template <int kBN, bool kAmn, bool kBmn, int kTerms, bool kPromote, bool kPair>
 dust_status launch_gemm(const GemmArgs& A, cudaStream_t s) {
-    using S = Shape<kBN, kTerms>;
+    using S = Shape<kBN, kTerms, kPair>;
     static PerContextOnce attr;
     if (!attr.run([] {
-            return cudaFuncSetAttribute(linear_gemm_kernel<kBN, kAmn, kBmn, kTerms, kPromote>,
+            return cudaFuncSetAttribute(linear_gemm_kernel<kBN, kAmn, kBmn, kTerms, kPromote, kPair>,
                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
                                         static_cast<int>(S::kSmem)) == cudaSuccess;
         }))
         return DUST_ERR_CUDA;
     const int64_t items = static_cast<int64_t>(A.m_tiles) * A.n_tiles * A.splits;
+    if (kPair) {
+        cudaLaunchAttribute at{};
+        at.id = cudaLaunchAttributeClusterDimension;
+        at.val.clusterDim.x = 2;
+        at.val.clusterDim.y = 1;
+        at.val.clusterDim.z = 1;
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<int64_t>(items, num_sms() / 2)), 1, 1);
+        cfg.blockDim = dim3(kThreads, 1, 1);
+        cfg.dynamicSmemBytes = S::kSmem;
+        cfg.stream = s;
+        cfg.attrs = &at;
+        cfg.numAttrs = 1;
+        return cudaLaunchKernelEx(&cfg, linear_gemm_kernel<kBN, kAmn, kBmn, kTerms, kPromote, kPair>, A) == cudaSuccess
+                   ? DUST_OK
+                   : DUST_ERR_CUDA;
+    }
     const unsigned grid = static_cast<unsigned>(std::min<int64_t>(items, num_sms()));
-    linear_gemm_kernel<kBN, kAmn, kBmn, kTerms, kPromote><<<grid, kThreads, S::kSmem, s>>>(A);
+    linear_gemm_kernel<kBN, kAmn, kBmn, kTerms, kPromote, kPair><<<grid, kThreads, S::kSmem, s>>>(A);
     return DUST_OK;
 }
 
@@ -1007,9 +1116,9 @@ int choose_bn(int64_t m_tiles, int n_out) {
 
 template <bool kBmn, int kTerms, bool kPromote>
 dust_status launch_width(int bn, const GemmArgs& A, cudaStream_t s) {
-    return bn == 256   ? launch_gemm<256, false, kBmn, kTerms, kPromote>(A, s)
-           : bn == 128 ? launch_gemm<128, false, kBmn, kTerms, kPromote>(A, s)
-                       : launch_gemm<64, false, kBmn, kTerms, kPromote>(A, s);
+    return bn == 256   ? launch_gemm<256, false, kBmn, kTerms, kPromote, true>(A, s)
+           : bn == 128 ? launch_gemm<128, false, kBmn, kTerms, kPromote, false>(A, s)
+                       : launch_gemm<64, false, kBmn, kTerms, kPromote, false>(A, s);
 }
 
 template <int kTok>
@@ -1082,10 +1191,11 @@ dust_status gemm_rows(const void* a, int64_t ld_a, int terms, int K, const void*
     G.splits = 1;
     G.n_tiles = (n_out + bn - 1) / bn;
     if (m_tiles * G.n_tiles > 1 << 30) return DUST_ERR_UNSUPPORTED;
-    G.m_tiles = static_cast<int>(m_tiles);
+    const bool pair = bn == 256;  // 256-row tiles, half of B's rows in each CTA's box
+    G.m_tiles = static_cast<int>(pair ? (m_tiles + 1) / 2 : m_tiles);
     if (!make_tmap_bf16_2d_ld(&G.ta, a, static_cast<uint64_t>(terms * M), K, ld_a, kBM, kBK)) return DUST_ERR_CUDA;
     if (b_mn ? !make_tmap_bf16_2d_ld(&G.tb, b, K, n_out, n_out, kBK, 64)
-             : !make_tmap_bf16_2d_ld(&G.tb, b, n_out, K, K, bn, kBK))
+             : !make_tmap_bf16_2d_ld(&G.tb, b, n_out, K, K, pair ? bn / 2 : bn, kBK))
         return DUST_ERR_CUDA;
     prof_begin(s);
     dust_status st;
@@ -1099,7 +1209,7 @@ dust_status gemm_rows(const void* a, int64_t ld_a, int terms, int K, const void*
     return st;
 }
 
-// dW [d_out, d_in] (+)= dz^T x: 128 x 256 tiles, the tokens in as many splits as cost least: the waves of
+// dW [d_out, d_in] (+)= dz^T x: 256 x 256 tiles, the tokens in as many splits as cost least: the waves of
 // items over the SMs (about 0.45 us a block of 64 tokens and 2 us an item) and, with more than one, the
 // partials written and read back at about 6 GB/ms and one more launch.  The partials are added in order.
 constexpr int kMinBlocks = 4;
@@ -1109,7 +1219,7 @@ struct DwPlan {
 };
 DwPlan dw_plan(int64_t N, int32_t d_in, int32_t d_out) {
     DwPlan p;
-    p.m_tiles = (d_out + kBM - 1) / kBM;
+    p.m_tiles = (d_out + 2 * kBM - 1) / (2 * kBM);
     p.n_tiles = (d_in + 255) / 256;
     p.k_blocks = static_cast<int>((N + kBK - 1) / kBK);
     const int64_t tiles = static_cast<int64_t>(p.m_tiles) * p.n_tiles;
@@ -1117,7 +1227,7 @@ DwPlan dw_plan(int64_t N, int32_t d_in, int32_t d_out) {
     int64_t S = 1;
     double least = 0;
     for (int64_t k = 1; k <= kMaxSplits && (k == 1 || p.k_blocks / k >= kMinBlocks); ++k) {
-        const double waves = static_cast<double>((tiles * k + num_sms() - 1) / num_sms());
+        const double waves = static_cast<double>((tiles * k + num_sms() / 2 - 1) / (num_sms() / 2));
         const double cost = waves * (0.45 * static_cast<double>((p.k_blocks + k - 1) / k) + 2.0) +
                             (k > 1 ? 3.0 + k * bytes / 6e6 : 0.0);
         if (k == 1 || cost < least) {
@@ -1156,8 +1266,8 @@ dust_status gemm_dw(const void* dz, int64_t ld_dz, int terms, const void* x, int
         !make_tmap_bf16_2d_ld(&G.tb, x, static_cast<uint64_t>(N), d_in, ld_x, kBK, 64))
         return DUST_ERR_CUDA;
     prof_begin(s);
-    const dust_status st = terms == 2 ? launch_gemm<256, true, true, 2, true>(G, s)
-                                      : launch_gemm<256, true, true, 1, true>(G, s);
+    const dust_status st = terms == 2 ? launch_gemm<256, true, true, 2, true, true>(G, s)
+                                      : launch_gemm<256, true, true, 1, true, true>(G, s);
     prof_end(s, "linear_dw_tcgen05");
     if (st != DUST_OK || p.splits == 1) return st;
     const int64_t n4 = G.split_elems / 4;
