@@ -94,6 +94,8 @@ __global__ void __launch_bounds__(kFThreads) embedding_kernel(const int32_t* __r
                                                               int64_t N, int32_t V, int32_t d, int32_t nv,
                                                               uint64_t nv_magic, float scale, TO* out,
                                                               int64_t ld_out) {
+    pdl_trigger();
+    pdl_wait();
     const int64_t total = N * nv;
     const int64_t base = static_cast<int64_t>(blockIdx.x) * (kFThreads * kFItems) + threadIdx.x;
     V8 r[kFItems];
@@ -149,6 +151,8 @@ __global__ void __launch_bounds__(kSThreads) embed_hist_kernel(const int32_t* __
                                                                int32_t V, int shift, uint32_t mask,
                                                                int32_t* hist) {
     __shared__ int32_t cnt[kBins];
+    pdl_trigger();
+    pdl_wait();
     cnt[threadIdx.x] = 0;
     __syncthreads();
     const int64_t p0 = static_cast<int64_t>(blockIdx.x) * (kSThreads * kSRounds);
@@ -237,6 +241,8 @@ __global__ void __launch_bounds__(kSThreads) embed_scatter_kernel(
     uint32_t* keys_out, int32_t* idx_out) {
     __shared__ int32_t wh[kSWarps][kBins];
     __shared__ int32_t sh[32];
+    pdl_trigger();
+    pdl_wait();
     int32_t all = 0, earlier = 0;
     const int tile = blockIdx.x;
 #pragma unroll 8
@@ -359,6 +365,8 @@ __device__ __forceinline__ void put_partial(float* row, const float (&a)[kN]) {
 template <typename T>
 __global__ void __launch_bounds__(kGThreads) embed_grad_kernel(const __grid_constant__ GradArgs A) {
     constexpr int kN = Lane<T>::kN;
+    pdl_trigger();
+    pdl_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t sum_blocks = (A.units + kGWarps - 1) / kGWarps;
     if (static_cast<int64_t>(blockIdx.x) >= sum_blocks) {
@@ -458,6 +466,8 @@ __global__ void __launch_bounds__(kGThreads) embed_grad_kernel(const __grid_cons
 // sums.  Two halves of the CTA take consecutive runs of chunks, each summed in order.
 constexpr int kJoinCols = 512;
 __global__ void __launch_bounds__(kGThreads) embed_join_kernel(const __grid_constant__ GradArgs A, int32_t slabs) {
+    pdl_trigger();
+    pdl_wait();
     const int64_t c = blockIdx.x / slabs;
     const int64_t p0 = c * A.chunk, p1 = p0 + A.chunk;
     if (p1 >= A.N) return;
@@ -515,6 +525,8 @@ __global__ void __launch_bounds__(kGThreads) embed_grad_small_kernel(const __gri
     int32_t* sums = reinterpret_cast<int32_t*>(first);  // until the list is complete
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int32_t share = static_cast<int32_t>(blockIdx.x);
+    pdl_trigger();
+    pdl_wait();
 
     // this share's tokens, in order: thread t looks at ids [16 t, 16 t + 16)
     int32_t id[kIdsPerThread];
@@ -658,9 +670,10 @@ __global__ void __launch_bounds__(kGThreads) embed_grad_small_kernel(const __gri
 
 template <typename T>
 dust_status launch_small(const SmallArgs& A, int slabs, cudaStream_t s) {
-    embed_grad_small_kernel<T><<<dim3(static_cast<unsigned>(A.shares), static_cast<unsigned>(slabs)), kGThreads,
-                                 kSmallTokens * 8, s>>>(A);
-    return cudaGetLastError() == cudaSuccess ? DUST_OK : DUST_ERR_CUDA;
+    return dependent_launch(embed_grad_small_kernel<T>, dim3(static_cast<unsigned>(A.shares), static_cast<unsigned>(slabs)),
+                            kGThreads, kSmallTokens * 8, s, 1, A)
+               ? DUST_OK
+               : DUST_ERR_CUDA;
 }
 
 struct GradPlan {
@@ -694,10 +707,10 @@ GradPlan grad_plan(dust_dtype dt, int64_t N, int32_t V, int32_t d) {
 }
 
 template <typename TE, typename TO>
-void launch_lookup(const int32_t* ids, const void* E, int64_t ld_E, int64_t N, int32_t V, int32_t d, float scale,
+bool launch_lookup(const int32_t* ids, const void* E, int64_t ld_E, int64_t N, int32_t V, int32_t d, float scale,
                    void* out, int64_t ld_out, unsigned blocks, int32_t nv, cudaStream_t s) {
-    embedding_kernel<TE, TO><<<blocks, kFThreads, 0, s>>>(ids, static_cast<const TE*>(E), ld_E, N, V, d, nv,
-                                                          div_magic(nv), scale, static_cast<TO*>(out), ld_out);
+    return dependent_launch(embedding_kernel<TE, TO>, dim3(blocks), kFThreads, 0, s, 1, ids, static_cast<const TE*>(E), ld_E,
+                            N, V, d, nv, div_magic(nv), scale, static_cast<TO*>(out), ld_out);
 }
 
 }  // namespace
@@ -710,16 +723,15 @@ dust_status embedding_launch(const int32_t* ids, const void* E, dust_dtype dt, i
     if (blocks > 2147483647LL) return DUST_ERR_UNSUPPORTED;
     const unsigned nb = static_cast<unsigned>(blocks);
     prof_begin(s);
-    if (dt == DUST_BF16 && out_dt == DUST_BF16)
-        launch_lookup<__nv_bfloat16, __nv_bfloat16>(ids, E, ld_E, N, V, d, scale, out, ld_out, nb, nv, s);
-    else if (dt == DUST_BF16)
-        launch_lookup<__nv_bfloat16, float>(ids, E, ld_E, N, V, d, scale, out, ld_out, nb, nv, s);
-    else if (out_dt == DUST_BF16)
-        launch_lookup<float, __nv_bfloat16>(ids, E, ld_E, N, V, d, scale, out, ld_out, nb, nv, s);
-    else
-        launch_lookup<float, float>(ids, E, ld_E, N, V, d, scale, out, ld_out, nb, nv, s);
+    using bf16 = __nv_bfloat16;
+    const bool ok =
+        dt == DUST_BF16
+            ? (out_dt == DUST_BF16 ? launch_lookup<bf16, bf16>(ids, E, ld_E, N, V, d, scale, out, ld_out, nb, nv, s)
+                                   : launch_lookup<bf16, float>(ids, E, ld_E, N, V, d, scale, out, ld_out, nb, nv, s))
+            : (out_dt == DUST_BF16 ? launch_lookup<float, bf16>(ids, E, ld_E, N, V, d, scale, out, ld_out, nb, nv, s)
+                                   : launch_lookup<float, float>(ids, E, ld_E, N, V, d, scale, out, ld_out, nb, nv, s));
     prof_end(s, "embedding");
-    return cudaGetLastError() == cudaSuccess ? DUST_OK : DUST_ERR_CUDA;
+    return ok ? DUST_OK : DUST_ERR_CUDA;
 }
 
 size_t embedding_grad_workspace_bytes(dust_dtype dt, int64_t N, int32_t V, int32_t d) {
@@ -756,20 +768,18 @@ dust_status embedding_grad_launch(const int32_t* ids, const void* g, dust_dtype 
         const int32_t* first = pass == 0 ? ids : nullptr;
         const int to = at ^ 1, shift = pass * p.bits;
         const bool few = N < kManyTokens;
+        const uint32_t* key_in = key[at];
+        const int32_t *idx_in = idx[at], *hist_in = hist;
         prof_begin(s);
-        if (few)
-            embed_hist_kernel<kFewRounds><<<p.tiles, kSThreads, 0, s>>>(first, key[at], N, V, shift, mask, hist);
-        else
-            embed_hist_kernel<kManyRounds><<<p.tiles, kSThreads, 0, s>>>(first, key[at], N, V, shift, mask, hist);
+        bool ok = dependent_launch(few ? embed_hist_kernel<kFewRounds> : embed_hist_kernel<kManyRounds>, dim3(p.tiles),
+                                   kSThreads, 0, s, 1, first, key_in, N, V, shift, mask, hist);
         prof_end(s, "embedding_sort_count");
         prof_begin(s);
-        if (few)
-            embed_scatter_kernel<kFewRounds><<<p.tiles, kSThreads, 0, s>>>(first, key[at], idx[at], N, V, shift, mask,
-                                                                          hist, p.tiles, key[to], idx[to]);
-        else
-            embed_scatter_kernel<kManyRounds><<<p.tiles, kSThreads, 0, s>>>(first, key[at], idx[at], N, V, shift, mask,
-                                                                           hist, p.tiles, key[to], idx[to]);
+        ok = ok && dependent_launch(few ? embed_scatter_kernel<kFewRounds> : embed_scatter_kernel<kManyRounds>,
+                                    dim3(p.tiles), kSThreads, 0, s, 1, first, key_in, idx_in, N, V, shift, mask, hist_in,
+                                    p.tiles, key[to], idx[to]);
         prof_end(s, "embedding_sort");
+        if (!ok) return DUST_ERR_CUDA;
         at = to;
     }
     GradArgs A{};
@@ -797,17 +807,16 @@ dust_status embedding_grad_launch(const int32_t* ids, const void* g, dust_dtype 
     if (blocks > 2147483647LL || static_cast<int64_t>(p.chunks) * join_slabs > 2147483647LL)
         return DUST_ERR_UNSUPPORTED;
     prof_begin(s);
-    if (dt == DUST_BF16)
-        embed_grad_kernel<__nv_bfloat16><<<static_cast<unsigned>(blocks), kGThreads, 0, s>>>(A);
-    else
-        embed_grad_kernel<float><<<static_cast<unsigned>(blocks), kGThreads, 0, s>>>(A);
+    bool ok = dependent_launch(dt == DUST_BF16 ? embed_grad_kernel<__nv_bfloat16> : embed_grad_kernel<float>,
+                               dim3(static_cast<unsigned>(blocks)), kGThreads, 0, s, 1, A);
     prof_end(s, "embedding_grad");
-    if (p.chunks > 1) {
+    if (ok && p.chunks > 1) {
         prof_begin(s);
-        embed_join_kernel<<<static_cast<unsigned>(p.chunks * join_slabs), kGThreads, 0, s>>>(A, join_slabs);
+        ok = dependent_launch(embed_join_kernel, dim3(static_cast<unsigned>(p.chunks * join_slabs)), kGThreads, 0, s, 1, A,
+                              join_slabs);
         prof_end(s, "embedding_grad_join");
     }
-    return cudaGetLastError() == cudaSuccess ? DUST_OK : DUST_ERR_CUDA;
+    return ok ? DUST_OK : DUST_ERR_CUDA;
 }
 
 }  // namespace dust

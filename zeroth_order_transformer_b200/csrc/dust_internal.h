@@ -259,6 +259,27 @@ inline uint64_t div_magic(int64_t d) {
     return d > 1 ? ~0ull / static_cast<uint64_t>(d) + 1 : 0;
 }
 #ifdef __CUDACC__
+// Launches a kernel that calls pdl_wait (dust_device.cuh) as a dependent of the one before it on the stream: its
+// launch and its set-up overlap that one's end.  cluster_x: CTAs of a cluster.
+template <class... P, class... Args>
+bool dependent_launch(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t s, unsigned cluster_x,
+                      Args... args) {
+    cudaLaunchAttribute at[2] = {};
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = cluster_x;
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = at;
+    cfg.numAttrs = cluster_x > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess;
+}
 __device__ __forceinline__ int64_t div_by_magic(int64_t f, int64_t d, uint64_t magic) {
     return d == 1 ? f : static_cast<int64_t>(__umul64hi(static_cast<uint64_t>(f), magic));
 }

@@ -179,6 +179,8 @@ struct RowsArgs {
 template <int kTok>
 __global__ void __launch_bounds__(kRThreads) linear_rows_kernel(const __grid_constant__ RowsArgs A) {
     __shared__ float part[kRWarps][kRRows * kTok];
+    pdl_trigger();
+    pdl_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int group = warp / A.split, share = warp % A.split;
     const int o0 = (blockIdx.x * (kRWarps / A.split) + group) * kRRows;
@@ -599,6 +601,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_c
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
     const Pipe P = pipe_setup<kBN, kTerms, kPair>(smem, 8);
+    pdl_trigger();
+    pdl_wait();
     const int warp = warp_index(), lane = threadIdx.x & 31;
     const int rank = kPair ? static_cast<int>(blockIdx.x & 1) : 0;  // the clusters are CTAs 2 i, 2 i + 1
     const int first = kPair ? static_cast<int>(blockIdx.x >> 1) : static_cast<int>(blockIdx.x);
@@ -814,6 +818,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tokens_kernel(const __grid
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *slot;
+    pdl_trigger();
+    pdl_wait();
     cluster_arrive();  // waited for before the first remote store: the peers are running by then
     const int ranks = A.splits, rank = static_cast<int>(blockIdx.x) % ranks;
     const int o0 = static_cast<int>(blockIdx.x) / ranks * kBM;
@@ -945,6 +951,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tokens_kernel(const __grid
 // out (+)= the sum of S partials in order, four elements a thread.
 __global__ void __launch_bounds__(256) linear_join_kernel(const float4* __restrict__ part, int S, int64_t n4, float4* out,
                                                           int accumulate) {
+    pdl_trigger();
+    pdl_wait();
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n4;
          i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
         float4 s = accumulate ? out[i] : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -982,6 +990,8 @@ struct DzArgs {
 template <typename T, int kAct>
 __global__ void __launch_bounds__(kDThreads) linear_dz_kernel(const __grid_constant__ DzArgs A) {
     __shared__ float sh[kDWarps][kDCols + 8];
+    pdl_trigger();
+    pdl_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int col = blockIdx.x * kDCols + lane * 8;
     const int64_t r0 = static_cast<int64_t>(blockIdx.y) * A.rows;
@@ -1046,6 +1056,8 @@ __global__ void __launch_bounds__(kDThreads) linear_dz_kernel(const __grid_const
 __global__ void __launch_bounds__(256) linear_db_kernel(const float* part, int chunks, int d_out, float* db,
                                                         int accumulate) {
     __shared__ float sh[8][32];
+    pdl_trigger();
+    pdl_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int c = blockIdx.x * 32 + lane;
     const int per = (chunks + 7) / 8;
@@ -1075,26 +1087,12 @@ dust_status launch_gemm(const GemmArgs& A, cudaStream_t s) {
         }))
         return DUST_ERR_CUDA;
     const int64_t items = static_cast<int64_t>(A.m_tiles) * A.n_tiles * A.splits;
-    if (kPair) {
-        cudaLaunchAttribute at{};
-        at.id = cudaLaunchAttributeClusterDimension;
-        at.val.clusterDim.x = 2;
-        at.val.clusterDim.y = 1;
-        at.val.clusterDim.z = 1;
-        cudaLaunchConfig_t cfg{};
-        cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<int64_t>(items, num_sms() / 2)), 1, 1);
-        cfg.blockDim = dim3(kThreads, 1, 1);
-        cfg.dynamicSmemBytes = S::kSmem;
-        cfg.stream = s;
-        cfg.attrs = &at;
-        cfg.numAttrs = 1;
-        return cudaLaunchKernelEx(&cfg, linear_gemm_kernel<kBN, kAmn, kBmn, kTerms, kPromote, kPair>, A) == cudaSuccess
-                   ? DUST_OK
-                   : DUST_ERR_CUDA;
-    }
-    const unsigned grid = static_cast<unsigned>(std::min<int64_t>(items, num_sms()));
-    linear_gemm_kernel<kBN, kAmn, kBmn, kTerms, kPromote, kPair><<<grid, kThreads, S::kSmem, s>>>(A);
-    return DUST_OK;
+    const unsigned grid = static_cast<unsigned>(
+        kPair ? 2 * std::min<int64_t>(items, num_sms() / 2) : std::min<int64_t>(items, num_sms()));
+    return dependent_launch(linear_gemm_kernel<kBN, kAmn, kBmn, kTerms, kPromote, kPair>, dim3(grid), kThreads, S::kSmem, s,
+                            kPair ? 2 : 1, A)
+               ? DUST_OK
+               : DUST_ERR_CUDA;
 }
 
 // Output tile width: the one whose waves of tiles over the SMs cost least, a tile of 128 x bn taking
@@ -1114,9 +1112,16 @@ int choose_bn(int64_t m_tiles, int n_out) {
     return best;
 }
 
+// 256-column tiles of a bf16 output go to pairs of CTAs where the contraction is long enough to pay for
+// the pair's set-up (2304 columns over 8192 tokens, alone and in pairs: K = 256 15.5 and 18.5 us, 768 25.8 and
+// 23.9, 1536 43.1 and 40.9).  An fp32 output's sums change hands every 512 products, and a pair's do so more slowly.
+bool in_pairs(int bn, int k_blocks, int out_bf16) { return bn == 256 && out_bf16 && k_blocks >= 12; }
+
 template <bool kBmn, int kTerms, bool kPromote>
-dust_status launch_width(int bn, const GemmArgs& A, cudaStream_t s) {
-    return bn == 256   ? launch_gemm<256, false, kBmn, kTerms, kPromote, true>(A, s)
+dust_status launch_width(int bn, bool pair, const GemmArgs& A, cudaStream_t s) {
+    if constexpr (!kPromote)
+        if (pair) return launch_gemm<256, false, kBmn, kTerms, kPromote, true>(A, s);
+    return bn == 256   ? launch_gemm<256, false, kBmn, kTerms, kPromote, false>(A, s)
            : bn == 128 ? launch_gemm<128, false, kBmn, kTerms, kPromote, false>(A, s)
                        : launch_gemm<64, false, kBmn, kTerms, kPromote, false>(A, s);
 }
@@ -1130,19 +1135,11 @@ dust_status launch_tokens(const GemmArgs& A, cudaStream_t s) {
                                         static_cast<int>(S::kSmem)) == cudaSuccess;
         }))
         return DUST_ERR_CUDA;
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = static_cast<unsigned>(A.splits);
-    at.val.clusterDim.y = 1;
-    at.val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(A.m_tiles * A.splits), static_cast<unsigned>(A.n_tiles), 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
-    cfg.dynamicSmemBytes = S::kSmem;
-    cfg.stream = s;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, linear_tokens_kernel<kTok>, A) == cudaSuccess ? DUST_OK : DUST_ERR_CUDA;
+    return dependent_launch(linear_tokens_kernel<kTok>,
+                            dim3(static_cast<unsigned>(A.m_tiles * A.splits), static_cast<unsigned>(A.n_tiles)), kThreads,
+                            S::kSmem, s, static_cast<unsigned>(A.splits), A)
+               ? DUST_OK
+               : DUST_ERR_CUDA;
 }
 
 // Whether the outputs are few enough for linear_tokens_kernel: at most as many 128-channel tiles as SMs.
@@ -1191,7 +1188,7 @@ dust_status gemm_rows(const void* a, int64_t ld_a, int terms, int K, const void*
     G.splits = 1;
     G.n_tiles = (n_out + bn - 1) / bn;
     if (m_tiles * G.n_tiles > 1 << 30) return DUST_ERR_UNSUPPORTED;
-    const bool pair = bn == 256;  // 256-row tiles, half of B's rows in each CTA's box
+    const bool pair = in_pairs(bn, G.k_blocks, G.e.out_bf16);  // 256-row tiles, half of B's columns in each CTA
     G.m_tiles = static_cast<int>(pair ? (m_tiles + 1) / 2 : m_tiles);
     if (!make_tmap_bf16_2d_ld(&G.ta, a, static_cast<uint64_t>(terms * M), K, ld_a, kBM, kBK)) return DUST_ERR_CUDA;
     if (b_mn ? !make_tmap_bf16_2d_ld(&G.tb, b, K, n_out, n_out, kBK, 64)
@@ -1200,16 +1197,17 @@ dust_status gemm_rows(const void* a, int64_t ld_a, int terms, int K, const void*
     prof_begin(s);
     dust_status st;
     if (b_mn)
-        st = G.e.out_bf16 ? launch_width<true, 1, false>(bn, G, s)
-             : terms == 2 ? launch_width<true, 2, true>(bn, G, s)
-                          : launch_width<true, 1, true>(bn, G, s);
+        st = G.e.out_bf16 ? launch_width<true, 1, false>(bn, pair, G, s)
+             : terms == 2 ? launch_width<true, 2, true>(bn, pair, G, s)
+                          : launch_width<true, 1, true>(bn, pair, G, s);
     else
-        st = G.e.out_bf16 ? launch_width<false, 1, false>(bn, G, s) : launch_width<false, 1, true>(bn, G, s);
+        st = G.e.out_bf16 ? launch_width<false, 1, false>(bn, pair, G, s) : launch_width<false, 1, true>(bn, pair, G, s);
     prof_end(s, name);
     return st;
 }
 
-// dW [d_out, d_in] (+)= dz^T x: 256 x 256 tiles, the tokens in as many splits as cost least: the waves of
+// dW [d_out, d_in] (+)= dz^T x: 128 x 256 tiles (in pairs they take as long: two terms already
+// load 64 KB for 1024 cycles of MMAs), the tokens in as many splits as cost least: the waves of
 // items over the SMs (about 0.45 us a block of 64 tokens and 2 us an item) and, with more than one, the
 // partials written and read back at about 6 GB/ms and one more launch.  The partials are added in order.
 constexpr int kMinBlocks = 4;
@@ -1219,7 +1217,7 @@ struct DwPlan {
 };
 DwPlan dw_plan(int64_t N, int32_t d_in, int32_t d_out) {
     DwPlan p;
-    p.m_tiles = (d_out + 2 * kBM - 1) / (2 * kBM);
+    p.m_tiles = (d_out + kBM - 1) / kBM;
     p.n_tiles = (d_in + 255) / 256;
     p.k_blocks = static_cast<int>((N + kBK - 1) / kBK);
     const int64_t tiles = static_cast<int64_t>(p.m_tiles) * p.n_tiles;
@@ -1227,7 +1225,7 @@ DwPlan dw_plan(int64_t N, int32_t d_in, int32_t d_out) {
     int64_t S = 1;
     double least = 0;
     for (int64_t k = 1; k <= kMaxSplits && (k == 1 || p.k_blocks / k >= kMinBlocks); ++k) {
-        const double waves = static_cast<double>((tiles * k + num_sms() / 2 - 1) / (num_sms() / 2));
+        const double waves = static_cast<double>((tiles * k + num_sms() - 1) / num_sms());
         const double cost = waves * (0.45 * static_cast<double>((p.k_blocks + k - 1) / k) + 2.0) +
                             (k > 1 ? 3.0 + k * bytes / 6e6 : 0.0);
         if (k == 1 || cost < least) {
@@ -1266,28 +1264,28 @@ dust_status gemm_dw(const void* dz, int64_t ld_dz, int terms, const void* x, int
         !make_tmap_bf16_2d_ld(&G.tb, x, static_cast<uint64_t>(N), d_in, ld_x, kBK, 64))
         return DUST_ERR_CUDA;
     prof_begin(s);
-    const dust_status st = terms == 2 ? launch_gemm<256, true, true, 2, true, true>(G, s)
-                                      : launch_gemm<256, true, true, 1, true, true>(G, s);
+    const dust_status st = terms == 2 ? launch_gemm<256, true, true, 2, true, false>(G, s)
+                                      : launch_gemm<256, true, true, 1, true, false>(G, s);
     prof_end(s, "linear_dw_tcgen05");
     if (st != DUST_OK || p.splits == 1) return st;
     const int64_t n4 = G.split_elems / 4;
     prof_begin(s);
-    linear_join_kernel<<<static_cast<unsigned>(std::min<int64_t>((n4 + 255) / 256, static_cast<int64_t>(num_sms()) * 16)),
-                         256, 0, s>>>(reinterpret_cast<const float4*>(part), p.splits, n4,
-                                      reinterpret_cast<float4*>(dW), accumulate);
+    const unsigned blocks = static_cast<unsigned>(std::min<int64_t>((n4 + 255) / 256, static_cast<int64_t>(num_sms()) * 16));
+    const bool ok = dependent_launch(linear_join_kernel, dim3(blocks), 256, 0, s, 1, reinterpret_cast<const float4*>(part),
+                                     p.splits, n4, reinterpret_cast<float4*>(dW), accumulate);
     prof_end(s, "linear_dw_join");
-    return DUST_OK;
+    return ok ? DUST_OK : DUST_ERR_CUDA;
 }
 
 template <typename T>
-void launch_dz(const DzArgs& A, int act, dim3 grid, cudaStream_t s) {
+bool launch_dz(const DzArgs& A, int act, dim3 grid, cudaStream_t s) {
     switch (act) {
-        case DUST_ACT_RELU: linear_dz_kernel<T, DUST_ACT_RELU><<<grid, kDThreads, 0, s>>>(A); return;
-        case DUST_ACT_GELU: linear_dz_kernel<T, DUST_ACT_GELU><<<grid, kDThreads, 0, s>>>(A); return;
-        case DUST_ACT_GELU_TANH: linear_dz_kernel<T, DUST_ACT_GELU_TANH><<<grid, kDThreads, 0, s>>>(A); return;
-        case DUST_ACT_SILU: linear_dz_kernel<T, DUST_ACT_SILU><<<grid, kDThreads, 0, s>>>(A); return;
+        case DUST_ACT_RELU: return dependent_launch(linear_dz_kernel<T, DUST_ACT_RELU>, grid, kDThreads, 0, s, 1, A);
+        case DUST_ACT_GELU: return dependent_launch(linear_dz_kernel<T, DUST_ACT_GELU>, grid, kDThreads, 0, s, 1, A);
+        case DUST_ACT_GELU_TANH: return dependent_launch(linear_dz_kernel<T, DUST_ACT_GELU_TANH>, grid, kDThreads, 0, s, 1, A);
+        case DUST_ACT_SILU: return dependent_launch(linear_dz_kernel<T, DUST_ACT_SILU>, grid, kDThreads, 0, s, 1, A);
     }
-    linear_dz_kernel<T, DUST_ACT_NONE><<<grid, kDThreads, 0, s>>>(A);
+    return dependent_launch(linear_dz_kernel<T, DUST_ACT_NONE>, grid, kDThreads, 0, s, 1, A);
 }
 
 size_t dz_bytes(int64_t N, int32_t d_out) { return align_up(static_cast<size_t>(2 * N) * d_out * 2, 256); }
@@ -1298,11 +1296,6 @@ size_t db_bytes(int64_t N, int32_t d_out) {
 
 // Tokens up to which W is streamed through the CUDA cores.
 constexpr int kFewTokens = 2;
-
-template <int kTok>
-void launch_rows(const RowsArgs& A, unsigned blocks, cudaStream_t s) {
-    linear_rows_kernel<kTok><<<blocks, kRThreads, 0, s>>>(A);
-}
 
 }  // namespace
 
@@ -1322,16 +1315,10 @@ dust_status linear_launch(const void* x, int64_t ld_x, const void* W, const floa
         const int per_cta = kRWarps / A.split;
         const unsigned blocks = static_cast<unsigned>((groups + per_cta - 1) / per_cta);
         prof_begin(s);
-        if (N == 1)
-            launch_rows<1>(A, blocks, s);
-        else if (N == 2)
-            launch_rows<2>(A, blocks, s);
-        else if (N <= 4)
-            launch_rows<4>(A, blocks, s);
-        else
-            launch_rows<8>(A, blocks, s);
+        const bool ok = N == 1 ? dependent_launch(linear_rows_kernel<1>, dim3(blocks), kRThreads, 0, s, 1, A)
+                               : dependent_launch(linear_rows_kernel<2>, dim3(blocks), kRThreads, 0, s, 1, A);
         prof_end(s, "linear_rows");
-        return cudaGetLastError() == cudaSuccess ? DUST_OK : DUST_ERR_CUDA;
+        return ok ? DUST_OK : DUST_ERR_CUDA;
     }
     GemmArgs G{};
     G.e = Epilogue{bias, res, y, static_cast<__nv_bfloat16*>(z), N, ld_res, ld_y, ld_z, d_out, act, out_bf16};
@@ -1366,16 +1353,15 @@ dust_status linear_backward_launch(const void* dy, int dy_bf16, int64_t ld_dy, c
         }
         const dim3 grid((d_out + kDCols - 1) / kDCols, chunks);
         prof_begin(s);
-        if (dy_bf16)
-            launch_dz<__nv_bfloat16>(A, act, grid, s);
-        else
-            launch_dz<float>(A, act, grid, s);
+        bool ok = dy_bf16 ? launch_dz<__nv_bfloat16>(A, act, grid, s) : launch_dz<float>(A, act, grid, s);
         prof_end(s, "linear_dz");
-        if (db) {
+        if (ok && db) {
             prof_begin(s);
-            linear_db_kernel<<<(d_out + 31) / 32, 256, 0, s>>>(part, chunks, d_out, db, accumulate);
+            ok = dependent_launch(linear_db_kernel, dim3((d_out + 31) / 32), 256, 0, s, 1, static_cast<const float*>(part),
+                                  chunks, d_out, db, accumulate);
             prof_end(s, "linear_db");
         }
+        if (!ok) return DUST_ERR_CUDA;
     }
     const void* op = direct ? dy : hi;
     const int64_t ld_op = direct ? ld_dy : d_out;
