@@ -533,8 +533,20 @@ def dust_weight_grad_step(r, x, d_out: int, K_total: int, sigma: float, key: Noi
 
 # ------------------------------------------------------------------ around the estimator
 
+# Host time counts in these calls (a lookup of a few tokens is 2 us on the device), so they take the
+# stream handle and the current device without the objects around them (3 us for a Stream) and check
+# each tensor once.
+_DT = {}  # torch dtype -> C code, filled at the first use
+
+
+def _dtypes() -> dict:
+    if not _DT:
+        torch = _torch()
+        _DT[torch.bfloat16], _DT[torch.float32] = DUST_BF16, DUST_F32
+    return _DT
+
+
 def _raw_stream(index: int) -> int:
-    """The handle of the device's current stream (without the Stream object around it, 3 us of host time)."""
     return _torch()._C._cuda_getCurrentRawStream(index)
 
 
@@ -544,25 +556,23 @@ def _scope(index: int, stream):
     torch = _torch()
     if index < 0:
         raise ValueError("the tensors must be CUDA tensors")
-    if stream is not None:
-        if stream.device.index != index:
-            raise ValueError(f"stream is on {stream.device}, the tensors are on cuda:{index}")
-        return torch.cuda.stream(stream)
-    if index != torch.cuda.current_device():
-        return torch.cuda.device(index)
-    return None
+    if stream is None:
+        return None if index == torch._C._cuda_getDevice() else torch.cuda.device(index)
+    if stream.device.index != index:
+        raise ValueError(f"stream is on {stream.device}, the tensors are on cuda:{index}")
+    return torch.cuda.stream(stream)
 
 
-def _rows(t, name: str, rows: int, cols: int, index: int, dtypes) -> int:
-    """Checks a CUDA matrix [rows, cols] with contiguous rows and returns its row stride."""
-    if t.get_device() != index or index < 0:
-        raise ValueError(f"{name} must be a CUDA tensor on cuda:{index}")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name} must be one of {dtypes}, not {t.dtype}")
-    shape, strides = t.shape, t.stride()
-    if shape != (rows, cols) or (cols > 1 and strides[1] != 1):
-        raise ValueError(f"{name} must be [{rows}, {cols}] with contiguous rows, got {tuple(shape)}, "
-                         f"strides {strides}")
+def _rows(t, name: str, rows: int, cols: int, index: int, only=None) -> int:
+    """Checks a CUDA matrix [rows, cols] of bf16 or fp32 (or of the type `only`) with contiguous rows and
+    returns its row stride."""
+    dtype = t.dtype
+    if dtype is not only and (only is not None or dtype not in _dtypes()):
+        raise TypeError(f"{name} must be {only or 'bf16 or fp32'}, not {dtype}")
+    strides = t.stride()
+    if t.get_device() != index or t.shape != (rows, cols) or (strides[1] != 1 and cols > 1):
+        raise ValueError(f"{name} must be a [{rows}, {cols}] matrix with contiguous rows on cuda:{index}, got "
+                         f"{tuple(t.shape)}, strides {strides}, on {t.device}")
     return strides[0] if rows > 1 else -(-cols // 8) * 8
 
 
@@ -573,19 +583,23 @@ def _flat(t, name: str, n: int, index: int, dtype):
 
 
 def _new_rows(like, rows: int, cols: int, dtype, vec: int):
-    """A new [rows, cols] matrix whose rows begin at multiples of `vec` elements."""
+    """A new [rows, cols] matrix whose rows begin at multiples of `vec` elements, and its row stride."""
     if cols % vec == 0:
-        return like.new_empty((rows, cols), dtype=dtype)
-    return like.new_empty((rows, -(-cols // vec) * vec), dtype=dtype)[:, :cols]
+        return like.new_empty((rows, cols), dtype=dtype), cols
+    ld = -(-cols // vec) * vec
+    return like.new_empty((rows, ld), dtype=dtype)[:, :cols], ld
 
 
 def _new_workspace(workspace, nbytes: int, like):
+    """(address, bytes, what keeps it alive) of a given workspace that suffices, or of a new one."""
     torch = _torch()
+    if nbytes == 0:
+        return None, 0, None
     if workspace is None or workspace.numel() * workspace.element_size() < nbytes:
-        workspace = like.new_empty(max(nbytes, 1), dtype=torch.uint8)
+        workspace = like.new_empty(nbytes, dtype=torch.uint8)
     elif workspace.get_device() != like.get_device() or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {like.device}")
-    return workspace, workspace.numel() * workspace.element_size()
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
 def _act_code(act: str) -> int:
@@ -613,7 +627,7 @@ def dust_linear(x, W, bias=None, act: str = "none", residual=None, y=None, z=Non
     d_out, k = W.shape
     if k != d_in:
         raise ValueError("x must be [N, d_in] and W [d_out, d_in]")
-    ld_x = _rows(x, "x", N, d_in, dev, (bf,))
+    ld_x = _rows(x, "x", N, d_in, dev, bf)
     _flat(W, "W", d_out * d_in, dev, bf)
     if bias is not None:
         _flat(bias, "bias", d_out, dev, f32)
@@ -623,14 +637,14 @@ def dust_linear(x, W, bias=None, act: str = "none", residual=None, y=None, z=Non
     else:
         if out_dtype is not None and y.dtype != out_dtype:
             raise TypeError(f"y is {y.dtype}, out_dtype {out_dtype}")
-        ld_y = _rows(y, "y", N, d_out, dev, (bf, f32))
-    ld_res = _rows(residual, "residual", N, d_out, dev, (y.dtype,)) if residual is not None else 0
+        ld_y = _rows(y, "y", N, d_out, dev)
+    ld_res = _rows(residual, "residual", N, d_out, dev, y.dtype) if residual is not None else 0
     keep = z is not None and z is not False
     if z is True:
         z = x.new_empty((N, d_out))
-    ld_z = _rows(z, "z", N, d_out, dev, (bf,)) if keep else 0
+    ld_z = _rows(z, "z", N, d_out, dev, bf) if keep else 0
     st = lib().dust_linear(x.data_ptr(), ld_x, W.data_ptr(), _ptr(bias), _act_code(act), _ptr(residual), ld_res,
-                           DUST_BF16, N, d_in, d_out, y.data_ptr(), _dtype_code(y), ld_y,
+                           DUST_BF16, N, d_in, d_out, y.data_ptr(), _dtypes()[y.dtype], ld_y,
                            z.data_ptr() if keep else None, ld_z, _raw_stream(dev))
     _check(st, "dust_linear")
     return (y, z) if keep else y
@@ -653,15 +667,15 @@ def dust_linear_backward(dy, x, W, act: str = "none", z=None, dx=True, dW=True, 
         raise ValueError("dy must be [N, d_out], x [N, d_in], W [d_out, d_in]")
     N, d_out = dy.shape
     d_in = x.shape[1]
-    ld_dy = _rows(dy, "dy", N, d_out, dev, (bf, f32))
-    ld_x = _rows(x, "x", N, d_in, dev, (bf,))
+    ld_dy = _rows(dy, "dy", N, d_out, dev)
+    ld_x = _rows(x, "x", N, d_in, dev, bf)
     if W.shape != (d_out, d_in):
         raise ValueError("dy must be [N, d_out], x [N, d_in], W [d_out, d_in]")
     _flat(W, "W", d_out * d_in, dev, bf)
     code = _act_code(act)
     if code and z is None:
         raise ValueError(f"act={act!r} needs the pre-activation z that dust_linear kept")
-    ld_z = _rows(z, "z", N, d_out, dev, (bf,)) if code else 0
+    ld_z = _rows(z, "z", N, d_out, dev, bf) if code else 0
     if accumulate and (dW is True or db is True):
         raise ValueError("accumulate adds to given dW and db tensors; pass them, or None to skip them")
     if dx is True:
@@ -673,24 +687,24 @@ def dust_linear_backward(dy, x, W, act: str = "none", z=None, dx=True, dW=True, 
     dx, dW, db = (None if t is False else t for t in (dx, dW, db))
     if dx is not None and dx_dtype is not None and dx.dtype != dx_dtype:
         raise TypeError(f"dx is {dx.dtype}, dx_dtype {dx_dtype}")
-    ld_dx = _rows(dx, "dx", N, d_in, dev, (bf, f32)) if dx is not None else 0
+    ld_dx = _rows(dx, "dx", N, d_in, dev) if dx is not None else 0
     if dW is not None:
         _flat(dW, "dW", d_out * d_in, dev, f32)
     if db is not None:
         _flat(db, "db", d_out, dev, f32)
-    ws, nb = _new_workspace(workspace, dust_workspace_size(DUST_OP_LINEAR_BACKWARD, DUST_BF16, N, d_in, d_out, 0), x)
-    st = lib().dust_linear_backward(dy.data_ptr(), _dtype_code(dy), ld_dy, z.data_ptr() if code else None, ld_z,
+    at, nb, ws = _new_workspace(workspace, dust_workspace_size(DUST_OP_LINEAR_BACKWARD, DUST_BF16, N, d_in, d_out, 0), x)
+    st = lib().dust_linear_backward(dy.data_ptr(), _dtypes()[dy.dtype], ld_dy, z.data_ptr() if code else None, ld_z,
                                     x.data_ptr(), ld_x, W.data_ptr(), code, DUST_BF16, N, d_in, d_out,
                                     int(g_terms), _ptr(dx),
                                     DUST_F32 if dx is not None and dx.dtype == f32 else DUST_BF16, ld_dx,
-                                    _ptr(dW), _ptr(db), 1 if accumulate else 0, ws.data_ptr(), nb, _raw_stream(dev))
+                                    _ptr(dW), _ptr(db), 1 if accumulate else 0, at, nb, _raw_stream(dev))
     _check(st, "dust_linear_backward")
     return dx, dW, db
 
 
 def _check_ids(ids) -> int:
     torch = _torch()
-    if ids.dtype != torch.int32:
+    if ids.dtype is not torch.int32:
         raise TypeError("ids must be int32")
     if ids.dim() != 1 or not ids.is_contiguous():
         raise ValueError("ids must be a contiguous CUDA vector")
@@ -700,8 +714,6 @@ def _check_ids(ids) -> int:
 def dust_embedding(ids, E, scale: float = 1.0, out=None, out_dtype=None, stream=None):
     """out[N, d] = scale E[ids] for int32 ids [N] and a bf16 or fp32 table E [V, d] (out of E's type, or
     out_dtype).  A negative id gives a zero row, an id >= V a NaN row."""
-    torch = _torch()
-    both = (torch.bfloat16, torch.float32)
     N = _check_ids(ids)
     dev = ids.get_device()
     scope = _scope(dev, stream)
@@ -711,15 +723,20 @@ def dust_embedding(ids, E, scale: float = 1.0, out=None, out_dtype=None, stream=
     if E.dim() != 2:
         raise ValueError("E must be [V, d]")
     V, d = E.shape
-    ld_E = _rows(E, "E", V, d, dev, both)
+    ld_E = _rows(E, "E", V, d, dev)
+    codes = _dtypes()
     if out is None:
-        out = _new_rows(E, N, d, out_dtype or E.dtype, 8)
+        out, ld_out = _new_rows(E, N, d, out_dtype or E.dtype, 8)
+        if out.dtype not in codes:
+            raise TypeError(f"out_dtype must be bf16 or fp32, not {out.dtype}")
     elif out_dtype is not None and out.dtype != out_dtype:
         raise TypeError(f"out is {out.dtype}, out_dtype {out_dtype}")
-    ld_out = _rows(out, "out", N, d, dev, both)
-    st = lib().dust_embedding(ids.data_ptr(), E.data_ptr(), _dtype_code(E), ld_E, N, V, d, float(scale),
-                              out.data_ptr(), _dtype_code(out), ld_out, _raw_stream(dev))
-    _check(st, "dust_embedding")
+    else:
+        ld_out = _rows(out, "out", N, d, dev)
+    st = lib().dust_embedding(ids.data_ptr(), E.data_ptr(), codes[E.dtype], ld_E, N, V, d, scale, out.data_ptr(),
+                              codes[out.dtype], ld_out, _raw_stream(dev))
+    if st:
+        _check(st, "dust_embedding")
     return out
 
 
@@ -737,17 +754,19 @@ def dust_embedding_grad(ids, g, V: int, scale: float = 1.0, G=None, accumulate: 
     if g.dim() != 2:
         raise ValueError("g must be [N, d]")
     d = g.shape[1]
-    ld_g = _rows(g, "g", N, d, dev, (torch.bfloat16, torch.float32))
-    if accumulate and G is None:
+    ld_g = _rows(g, "g", N, d, dev)
+    if G is not None:
+        ld_G = _rows(G, "G", V, d, dev, torch.float32)
+    elif accumulate:
         raise ValueError("accumulate adds to a given G")
-    if G is None:
-        G = _new_rows(g, V, d, torch.float32, 4)
-    ld_G = _rows(G, "G", V, d, dev, (torch.float32,))
-    dt = _dtype_code(g)
-    ws, nb = _new_workspace(workspace, dust_workspace_size(DUST_OP_EMBEDDING_GRAD, dt, N, V, d, 0), g)
-    st = lib().dust_embedding_grad(ids.data_ptr(), g.data_ptr(), dt, ld_g, N, V, d, float(scale), G.data_ptr(),
-                                   ld_G, 1 if accumulate else 0, ws.data_ptr(), nb, _raw_stream(dev))
-    _check(st, "dust_embedding_grad")
+    else:
+        G, ld_G = _new_rows(g, V, d, torch.float32, 4)
+    dt = _dtypes()[g.dtype]
+    at, nb, ws = _new_workspace(workspace, dust_workspace_size(DUST_OP_EMBEDDING_GRAD, dt, N, V, d, 0), g)
+    st = lib().dust_embedding_grad(ids.data_ptr(), g.data_ptr(), dt, ld_g, N, V, d, scale, G.data_ptr(), ld_G,
+                                   1 if accumulate else 0, at, nb, _raw_stream(dev))
+    if st:
+        _check(st, "dust_embedding_grad")
     return G
 
 
