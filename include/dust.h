@@ -123,8 +123,9 @@ dust_status dust_noisy_linear_output(const void* x, const void* W, dust_dtype dt
  * Row strides (elements) at least the row and a multiple of 16 bytes; all pointers 16-byte
  * aligned.  y may be the residual's buffer (with the same stride); other overlaps are undefined.
  * Sums in fp32; each output is rounded once.  Rows behind N and columns behind d_out are not
- * written.  Up to 8 tokens stream W through the CUDA cores, more go to the tensor cores, so the
- * last bit of a sum can depend on which.  Deterministic.
+ * written.  One and two tokens stream W through the CUDA cores, more go to the tensor cores, in forms
+ * chosen by the sizes, so the last bits of a token's sums can depend on how many tokens the call has.
+ * Deterministic.
  *   DUST_ACT_GELU: z Phi(z);  DUST_ACT_GELU_TANH: z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2;
  *   DUST_ACT_SILU: z / (1 + exp(-z));  DUST_ACT_RELU: max(z, 0).
  */
@@ -178,8 +179,8 @@ dust_status dust_embedding(const int32_t* ids, const void* E, dust_dtype dt, int
  * [V, ld_G].  accumulate == 0 overwrites all V rows (rows without tokens with zeros), accumulate != 0
  * adds to the rows that have tokens and leaves the others (for a table shared with the output layer).
  * Tokens whose id is outside [0, V) add nothing.  Sums in fp32, in token order within runs of sorted
- * tokens: deterministic.  N and V below 2^31 - 1.
- * workspace: dust_workspace_size(DUST_OP_EMBEDDING_GRAD, dt, N, V, d, 0) bytes.
+ * tokens: deterministic.  N <= 2^26, V < 2^31 - 1.
+ * workspace: dust_workspace_size(DUST_OP_EMBEDDING_GRAD, dt, N, V, d, 0) bytes (0 for up to 4096 tokens).
  */
 dust_status dust_embedding_grad(const int32_t* ids, const void* g, dust_dtype dt, int64_t ld_g, int64_t N,
                                 int32_t V, int32_t d, float scale, float* G, int64_t ld_G, int accumulate,

@@ -72,7 +72,7 @@ def _egrad(**kw):
 @pytest.mark.parametrize("kw,code", [
     (dict(ids=None), 1), (dict(g=None), 1), (dict(G=None), 1), (dict(N=0), 1), (dict(V=-1), 1), (dict(d=0), 1),
     (dict(g=P + 8), 1), (dict(G=P + 8), 1), (dict(ld=56), 1), (dict(ld=62), 1), (dict(ld_G=61), 1), (dict(dt=3), 1),
-    (dict(dt=z.DUST_BF16, ld=60), 1), (dict(V=2147483647), 2), (dict(N=1 << 31), 2), (dict(N=5000, ws=None), 5),
+    (dict(dt=z.DUST_BF16, ld=60), 1), (dict(V=2147483647), 2), (dict(N=(1 << 26) + 1), 2), (dict(N=1 << 40), 2), (dict(N=5000, ws=None), 5),
     (dict(N=5000, nb=64), 5),
 ])
 def test_embedding_grad_refuses(kw, code):

@@ -438,7 +438,8 @@ dust_status dust_embedding_grad(const int32_t* ids, const void* g, dust_dtype dt
     if ((reinterpret_cast<uintptr_t>(ids) & 3u) || !aligned16(g) || !aligned16(G) ||
         !valid_ld(ld_g, d, dt == DUST_BF16 ? 8 : 4) || !valid_ld(ld_G, d, 4))
         return DUST_ERR_INVALID_ARG;
-    if (N > 2147483647LL || V > 2147483646) return DUST_ERR_UNSUPPORTED;
+    // each tile of the sort reads the counts of all tiles: beyond 2^26 tokens that would take over
+    if (N > (1LL << 26) || V > 2147483646) return DUST_ERR_UNSUPPORTED;
     const dust_status st = check_ws(workspace, ws_bytes, embedding_grad_workspace_bytes(dt, N, V, d));
     if (st != DUST_OK) return st;
     return embedding_grad_launch(ids, g, dt, ld_g, N, V, d, scale, G, ld_G, accumulate, workspace,

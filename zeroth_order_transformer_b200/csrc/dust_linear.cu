@@ -1142,9 +1142,11 @@ dust_status launch_tokens(const GemmArgs& A, cudaStream_t s) {
                : DUST_ERR_CUDA;
 }
 
-// Whether the outputs are few enough for linear_tokens_kernel: at most as many 128-channel tiles as SMs.
+// Whether linear_tokens_kernel takes the product: with at most as many 128-channel tiles as SMs, and for up to 32
+// tokens with any number of them (24 tokens, 8192 -> 24576: 77 us against 93 in the persistent kernel, 2048 -> 65536
+// 63 against 67; with 64 tokens 81 against 56, its sums leaving through shared memory one by one).
 bool few_tiles(int64_t N, int n_out) {
-    return (N + 127) / 128 * ((n_out + kBM - 1) / kBM) <= num_sms();
+    return N <= 32 || (N + 127) / 128 * ((n_out + kBM - 1) / kBM) <= num_sms();
 }
 
 dust_status gemm_tokens(const void* x, int64_t ld_x, int K, const void* W, GemmArgs& G, cudaStream_t s) {
