@@ -86,7 +86,7 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const V8& r, int n) {
 
 // ------------------------------------------------------------------ the lookup
 constexpr int kFThreads = 256;
-constexpr int kFItems = 4;  // items of eight elements a thread holds at once
+constexpr int kFItems = 2;  // items of eight elements a thread holds at once
 
 template <typename TE, typename TO>
 __global__ void __launch_bounds__(kFThreads) embedding_kernel(const int32_t* __restrict__ ids,
@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(kSThreads) embed_scatter_kernel(
 // ------------------------------------------------------------------ the sums
 constexpr int kGThreads = 256;
 constexpr int kGWarps = kGThreads / 32;
-constexpr int kZeroRows = 64;  // table rows that one clearing CTA looks after
+constexpr int kZeroRows = 16;  // table rows that one clearing CTA looks after
 
 struct GradArgs {
     const uint32_t* key;  // sorted
@@ -504,7 +504,7 @@ __global__ void __launch_bounds__(kGThreads) embed_join_kernel(const __grid_cons
 
 // ------------------------------------------------------------------ small batches in one launch
 constexpr int kSmallTokens = 4096;
-constexpr int kIdsPerThread = kSmallTokens / kGThreads;
+constexpr int kRankTokens = 512;
 
 struct SmallArgs {
     const int32_t* ids;
@@ -522,55 +522,60 @@ __global__ void __launch_bounds__(kGThreads) embed_grad_small_kernel(const __gri
     constexpr int kN = Lane<T>::kN;
     extern __shared__ uint64_t list[];  // [kSmallTokens]
     __shared__ float first[kGWarps][32 * kN], last[kGWarps][32 * kN];
-    int32_t* sums = reinterpret_cast<int32_t*>(first);  // until the list is complete
+    int32_t* count = reinterpret_cast<int32_t*>(first);  // until the list is complete
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int32_t share = static_cast<int32_t>(blockIdx.x);
     pdl_trigger();
     pdl_wait();
 
-    // this share's tokens, in order: thread t looks at ids [16 t, 16 t + 16)
-    int32_t id[kIdsPerThread];
-    int count = 0;
-    const int at0 = threadIdx.x * kIdsPerThread;
-#pragma unroll
-    for (int j = 0; j < kIdsPerThread; ++j) {
-        id[j] = at0 + j < A.N ? __ldg(A.ids + at0 + j) : -1;
-        if (id[j] < 0 || id[j] >= A.V || (id[j] & (A.shares - 1)) != share) id[j] = -1;
-        count += id[j] >= 0;
-    }
-    int incl = count;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-        if (lane >= o) incl += v;
-    }
-    if (lane == 31) sums[warp] = incl;
+    // this share's tokens, in any order: the sort puts them right
+    if (threadIdx.x == 0) *count = 0;
     __syncthreads();
-    int base = incl - count, n = 0;
-    for (int w = 0; w < kGWarps; ++w) {
-        if (w < warp) base += sums[w];
-        n += sums[w];
+    for (int t0 = 0; t0 < A.N; t0 += kGThreads) {
+        const int t = t0 + threadIdx.x;
+        const int32_t id = t < A.N ? __ldg(A.ids + t) : -1;
+        const bool mine = id >= 0 && id < A.V && (id & (A.shares - 1)) == share;
+        const uint32_t vote = __ballot_sync(0xFFFFFFFFu, mine);
+        if (vote == 0) continue;  // uniform over the warp
+        int at = 0;
+        if (lane == 0) at = atomicAdd(count, __popc(vote));
+        at = __shfl_sync(0xFFFFFFFFu, at, 0) + __popc(vote & ((1u << lane) - 1u));
+        if (mine) list[at] = (static_cast<uint64_t>(id) << 32) | static_cast<uint32_t>(t);
     }
-#pragma unroll
-    for (int j = 0; j < kIdsPerThread; ++j)
-        if (id[j] >= 0) list[base++] = (static_cast<uint64_t>(id[j]) << 32) | static_cast<uint32_t>(at0 + j);
-    int size = 1;
-    while (size < n) size <<= 1;
-    for (int i = n + threadIdx.x; i < size; i += kGThreads) list[i] = ~0ull;  // sorts behind all
     __syncthreads();
-    // bitonic sort
-    for (int k = 2; k <= size; k <<= 1)
-        for (int j = k >> 1; j > 0; j >>= 1) {
-            for (int i = threadIdx.x; i < size / 2; i += kGThreads) {
-                const int a = 2 * i - (i & (j - 1)), b = a + j;
-                const uint64_t x = list[a], y = list[b];
-                if ((x > y) == ((a & k) == 0)) {
-                    list[a] = y;
-                    list[b] = x;
-                }
-            }
-            __syncthreads();
+    const int n = *count;
+    __syncthreads();  // count's memory is used again
+    const uint64_t* sorted = list;
+    if (n <= kRankTokens) {
+        // few keys: each one's place is the number of smaller ones
+        uint64_t* to = list + kSmallTokens / 2;
+        for (int i = threadIdx.x; i < n; i += kGThreads) {
+            const uint64_t k = list[i];
+            int place = 0;
+#pragma unroll 4
+            for (int j = 0; j < n; ++j) place += list[j] < k;
+            to[place] = k;
         }
+        sorted = to;
+        __syncthreads();
+    } else {  // bitonic
+        int size = 1;
+        while (size < n) size <<= 1;
+        for (int i = n + threadIdx.x; i < size; i += kGThreads) list[i] = ~0ull;  // sorts behind all
+        __syncthreads();
+        for (int k = 2; k <= size; k <<= 1)
+            for (int j = k >> 1; j > 0; j >>= 1) {
+                for (int i = threadIdx.x; i < size / 2; i += kGThreads) {
+                    const int a = 2 * i - (i & (j - 1)), b = a + j;
+                    const uint64_t x = list[a], y = list[b];
+                    if ((x > y) == ((a & k) == 0)) {
+                        list[a] = y;
+                        list[b] = x;
+                    }
+                }
+                __syncthreads();
+            }
+    }
 
     const int col = static_cast<int>(blockIdx.y) * (32 * kN) + kN * lane;
     const int left = A.d - col;
@@ -578,7 +583,7 @@ __global__ void __launch_bounds__(kGThreads) embed_grad_small_kernel(const __gri
     // warp w: positions [p0, p1) of the list
     const int per = (n + kGWarps - 1) / kGWarps;
     const int p0 = min(n, warp * per), p1 = min(n, p0 + per);
-    auto key = [&](int p) { return static_cast<int32_t>(list[p] >> 32); };
+    auto key = [&](int p) { return static_cast<int32_t>(sorted[p] >> 32); };
     if (p0 < p1) {
         int32_t cur = key(p0);
         bool began_before = p0 > 0 && key(p0 - 1) == cur;
@@ -589,7 +594,7 @@ __global__ void __launch_bounds__(kGThreads) embed_grad_small_kernel(const __gri
             for (int j = 0; j < 8; ++j) {
                 raw[j] = typename Lane<T>::Raw{};
                 if (p + j < p1) {
-                    const int64_t t = static_cast<uint32_t>(list[p + j]);
+                    const int64_t t = static_cast<uint32_t>(sorted[p + j]);
                     if (left >= kN)
                         raw[j] = __ldcs(reinterpret_cast<const typename Lane<T>::Raw*>(g + t * A.ld_g));
                     else if (left > 0)
@@ -651,12 +656,12 @@ __global__ void __launch_bounds__(kGThreads) embed_grad_small_kernel(const __gri
             int lo = 0, hi = n;
             while (lo < hi) {
                 const int mid = (lo + hi) >> 1;
-                if (list[mid] < v)
+                if (sorted[mid] < v)
                     lo = mid + 1;
                 else
                     hi = mid;
             }
-            absent = lo == n || (list[lo] >> 32) != (v >> 32);
+            absent = lo == n || (sorted[lo] >> 32) != (v >> 32);
         }
         uint32_t todo = __ballot_sync(0xFFFFFFFFu, absent);
         const float zero[kN] = {};
@@ -745,9 +750,9 @@ dust_status embedding_grad_launch(const int32_t* ids, const void* g, dust_dtype 
                                   void* ws, cudaStream_t s) {
     const GradPlan p = grad_plan(dt, N, V, d);
     if (N <= kSmallTokens) {
-        // about four CTAs an SM
+        // two to four CTAs an SM (2000 tokens onto 4096 x 768: 11.5 us, with one to two 12.0, with five to ten 14.4)
         int shares = 1;
-        while (shares < 512 && static_cast<int64_t>(shares) * p.slabs < static_cast<int64_t>(num_sms()) * 3) shares *= 2;
+        while (shares < 512 && static_cast<int64_t>(shares) * p.slabs < static_cast<int64_t>(num_sms()) * 2) shares *= 2;
         const SmallArgs A{ids, g, G, ld_g, ld_G, static_cast<int32_t>(N), V, d, shares, accumulate, scale};
         if (p.slabs > 65535) return DUST_ERR_UNSUPPORTED;
         prof_begin(s);
