@@ -239,7 +239,7 @@ def test_backward(z, act, terms, f32):
     back_case(z, 333, 208, 144, act, dt, dt, terms, False, 11)
 
 
-@pytest.mark.parametrize("N,d_in,d_out", [(1, 16, 16), (7, 48, 272), (128, 64, 64), (257, 528, 784), (2100, 272, 96), (1111, 1040, 1296)])
+@pytest.mark.parametrize("N,d_in,d_out", [(1, 16, 16), (7, 48, 272), (16, 208, 1040), (31, 64, 4112), (60, 336, 2064), (130, 272, 2320), (513, 144, 784), (128, 64, 64), (257, 528, 784), (2100, 272, 96), (1111, 1040, 1296)])
 def test_backward_sizes(z, N, d_in, d_out):
     import torch
     back_case(z, N, d_in, d_out, ["gelu", "none"][N & 1], torch.bfloat16, torch.bfloat16, 2, bool(N & 2), N)

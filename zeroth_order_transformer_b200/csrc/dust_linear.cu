@@ -785,8 +785,9 @@ struct CShape {
 static_assert(CShape<128>::kSmem <= 227 * 1024 && CShape<64>::kSmem <= 227 * 1024 && CShape<32>::kSmem <= 227 * 1024,
               "exceeds shared memory");
 
-// GemmArgs: ta is W (64 x 128 boxes), tb is x (64 x kTok), m tiles are of channels and n tiles of tokens.
-template <int kTok>
+// GemmArgs: ta is W (64 x 128 boxes; kAmn, for dx, where the output channels are W's columns: 64 x 64), tb is the
+// tokens (64 x kTok); m tiles are of channels and n tiles of tokens.
+template <int kTok, bool kAmn>
 __global__ void __launch_bounds__(kThreads, 1) linear_tokens_kernel(const __grid_constant__ GemmArgs A) {
     using S = CShape<kTok>;
     extern __shared__ uint8_t smem_raw[];
@@ -838,13 +839,18 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tokens_kernel(const __grid
                 if (i >= S::kStages && !mbar_wait_bounded(&empty[s], ((i / S::kStages) - 1) & 1, A.ew, 511)) break;
                 uint8_t* a = smem + s * S::kStageBytes;
                 mbar_arrive_expect_tx(&full[s], S::kStageBytes);
-                tma_load_2d(a, &A.ta, &full[s], kb * kBK, o0);
+                if (kAmn) {
+                    tma_load_2d(a, &A.ta, &full[s], o0, kb * kBK);
+                    tma_load_2d(a + kBox, &A.ta, &full[s], o0 + 64, kb * kBK);
+                } else {
+                    tma_load_2d(a, &A.ta, &full[s], kb * kBK, o0);
+                }
                 tma_load_2d(a + kABytes, &A.tb, &full[s], kb * kBK, t0);
             }
         }
     } else if (warp == 1) {
         if (elect_one()) {
-            constexpr uint32_t idesc = idesc_bf16_f32(kBM, kTok, 0, 0);
+            constexpr uint32_t idesc = idesc_bf16_f32(kBM, kTok, kAmn ? 1 : 0, 0);
             uint32_t ci = 0;
             bool ok = true;
             for (int k = kb0; k < kb1 && ok; k += kFlush, ++ci) {
@@ -859,10 +865,12 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tokens_kernel(const __grid
                     }
                     tc_fence_after();
                     const uint32_t a_addr = smem_u32(smem + s * S::kStageBytes);
-                    const uint64_t ad = sdesc_sw128(a_addr, 16, 1024), bd = sdesc_sw128(a_addr + kABytes, 16, 1024);
+                    const uint64_t ad = sdesc_sw128(a_addr, kAmn ? kBox : 16, 1024);
+                    const uint64_t bd = sdesc_sw128(a_addr + kABytes, 16, 1024);
+                    constexpr uint32_t kAStep = kAmn ? 2048 / 16 : 2;
 #pragma unroll
                     for (int kk = 0; kk < kBK / 16; ++kk)
-                        umma_bf16(tmem + buf * kTok, ad + 2 * kk, bd + 2 * kk, idesc, (kb > k || kk > 0) ? 1u : 0u);
+                        umma_bf16(tmem + buf * kTok, ad + kAStep * kk, bd + 2 * kk, idesc, (kb > k || kk > 0) ? 1u : 0u);
                     umma_commit(&empty[s]);
                 }
                 umma_commit(&acc_full[buf]);
@@ -1126,52 +1134,70 @@ dust_status launch_width(int bn, bool pair, const GemmArgs& A, cudaStream_t s) {
                        : launch_gemm<64, false, kBmn, kTerms, kPromote, false>(A, s);
 }
 
-template <int kTok>
+template <int kTok, bool kAmn>
 dust_status launch_tokens(const GemmArgs& A, cudaStream_t s) {
     using S = CShape<kTok>;
     static PerContextOnce attr;
     if (!attr.run([] {
-            return cudaFuncSetAttribute(linear_tokens_kernel<kTok>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+            return cudaFuncSetAttribute(linear_tokens_kernel<kTok, kAmn>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                         static_cast<int>(S::kSmem)) == cudaSuccess;
         }))
         return DUST_ERR_CUDA;
-    return dependent_launch(linear_tokens_kernel<kTok>,
+    return dependent_launch(linear_tokens_kernel<kTok, kAmn>,
                             dim3(static_cast<unsigned>(A.m_tiles * A.splits), static_cast<unsigned>(A.n_tiles)), kThreads,
                             S::kSmem, s, static_cast<unsigned>(A.splits), A)
                ? DUST_OK
                : DUST_ERR_CUDA;
 }
 
-// Whether linear_tokens_kernel takes the product: with at most as many 128-channel tiles as SMs, and for up to 32
-// tokens with any number of them (24 tokens, 8192 -> 24576: 77 us against 93 in the persistent kernel, 2048 -> 65536
-// 63 against 67; with 64 tokens 81 against 56, its sums leaving through shared memory one by one).
-bool few_tiles(int64_t N, int n_out) {
-    return N <= 32 || (N + 127) / 128 * ((n_out + kBM - 1) / kBM) <= num_sms();
+// How many CTAs share a tile's contraction in linear_tokens_kernel.  Clusters of four fit on the SMs about 33 at
+// a time (36 of them took two waves: 768 -> 2304 over 256 tokens 15.3 us, with clusters of two 10.3).
+int token_ranks(int64_t tiles, int k_blocks) {
+    return tiles * 4 <= 132 && k_blocks >= 8 ? 4 : tiles * 2 <= num_sms() && k_blocks >= 4 ? 2 : 1;
 }
 
-dust_status gemm_tokens(const void* x, int64_t ld_x, int K, const void* W, GemmArgs& G, cudaStream_t s) {
+int token_width(int64_t N) { return N <= 16 ? 16 : N <= 32 ? 32 : N <= 64 ? 64 : 128; }
+
+// Whether linear_tokens_kernel takes the product.  Up to 32 tokens always (24 tokens, 8192 -> 24576: 77 us against 93 in the
+// persistent kernel, 2048 -> 65536 63 against 67; with 64 tokens 81 against 56, its sums leaving through shared
+// memory one by one); more where a long contraction is shared (8192 -> 2048 over 512 tokens 31 us against 43, over
+// 1024, where the tiles fill the SMs, 56 against 47; 1024 -> 1024 over 1024 tokens 11.3 against 9.5).
+bool tokens_form(int64_t N, int n_out, int K) {
+    if (N <= 32) return true;
+    const int tok = token_width(N), k_blocks = (K + kBK - 1) / kBK;
+    const int r = token_ranks((N + tok - 1) / tok * ((n_out + kBM - 1) / kBM), k_blocks);
+    return r == 4 ? k_blocks >= 12 : r == 2 && k_blocks >= 32;
+}
+
+// y [N, n_out] = x W^T, or with w_mn x W (W [K, n_out]).
+dust_status gemm_tokens(const void* x, int64_t ld_x, int K, const void* W, bool w_mn, GemmArgs& G, const char* name,
+                        cudaStream_t s) {
     const int64_t N = G.e.M;
     const int n_out = G.e.n_out;
-    const int tok = N <= 16 ? 16 : N <= 32 ? 32 : N <= 64 ? 64 : 128;
+    const int tok = token_width(N);
     G.ew = device_error_word();
     G.k_blocks = (K + kBK - 1) / kBK;
     G.m_tiles = (n_out + kBM - 1) / kBM;
     G.n_tiles = static_cast<int>((N + tok - 1) / tok);
-    // ranks that share a tile's contraction, as many as there are SMs for while each keeps two blocks of 64
-    const int64_t tiles = static_cast<int64_t>(G.m_tiles) * G.n_tiles;
-    int r = 1;
-    while (r < 4 && tiles * r * 2 <= num_sms() && G.k_blocks >= 4 * r) r *= 2;
-    G.splits = r;
-    G.per_split = (G.k_blocks + r - 1) / r;
-    if (!make_tmap_bf16_2d_ld(&G.ta, W, n_out, K, K, kBM, kBK) ||
-        !make_tmap_bf16_2d_ld(&G.tb, x, static_cast<uint64_t>(N), K, ld_x, tok, kBK))
+    G.splits = token_ranks(static_cast<int64_t>(G.m_tiles) * G.n_tiles, G.k_blocks);
+    G.per_split = (G.k_blocks + G.splits - 1) / G.splits;
+    if (w_mn ? !make_tmap_bf16_2d_ld(&G.ta, W, K, n_out, n_out, kBK, 64)
+             : !make_tmap_bf16_2d_ld(&G.ta, W, n_out, K, K, kBM, kBK))
         return DUST_ERR_CUDA;
+    if (!make_tmap_bf16_2d_ld(&G.tb, x, static_cast<uint64_t>(N), K, ld_x, tok, kBK)) return DUST_ERR_CUDA;
     prof_begin(s);
-    const dust_status st = tok == 16   ? launch_tokens<16>(G, s)
-                           : tok == 32 ? launch_tokens<32>(G, s)
-                           : tok == 64 ? launch_tokens<64>(G, s)
-                                       : launch_tokens<128>(G, s);
-    prof_end(s, "linear_tokens_tcgen05");
+    dust_status st;
+    if (w_mn)
+        st = tok == 16   ? launch_tokens<16, true>(G, s)
+             : tok == 32 ? launch_tokens<32, true>(G, s)
+             : tok == 64 ? launch_tokens<64, true>(G, s)
+                         : launch_tokens<128, true>(G, s);
+    else
+        st = tok == 16   ? launch_tokens<16, false>(G, s)
+             : tok == 32 ? launch_tokens<32, false>(G, s)
+             : tok == 64 ? launch_tokens<64, false>(G, s)
+                         : launch_tokens<128, false>(G, s);
+    prof_end(s, name);
     return st;
 }
 
@@ -1324,8 +1350,9 @@ dust_status linear_launch(const void* x, int64_t ld_x, const void* W, const floa
     }
     GemmArgs G{};
     G.e = Epilogue{bias, res, y, static_cast<__nv_bfloat16*>(z), N, ld_res, ld_y, ld_z, d_out, act, out_bf16};
-    const dust_status st = few_tiles(N, d_out) ? gemm_tokens(x, ld_x, d_in, W, G, s)
-                                               : gemm_rows(x, ld_x, 1, d_in, W, false, G, "linear_tcgen05", s);
+    const dust_status st = tokens_form(N, d_out, d_in)
+                               ? gemm_tokens(x, ld_x, d_in, W, false, G, "linear_tokens_tcgen05", s)
+                               : gemm_rows(x, ld_x, 1, d_in, W, false, G, "linear_tcgen05", s);
     if (st != DUST_OK) return st;
     return cudaGetLastError() == cudaSuccess ? DUST_OK : DUST_ERR_CUDA;
 }
@@ -1375,7 +1402,10 @@ dust_status linear_backward_launch(const void* dy, int dy_bf16, int64_t ld_dy, c
         G.e.ld_y = ld_dx;
         G.e.out_bf16 = dx_bf16;
         // a bf16 dx is rounded as coarsely as one term of dz; an fp32 dx takes both terms
-        const dust_status st = gemm_rows(op, ld_op, dx_bf16 ? 1 : terms, d_out, W, true, G, "linear_dx_tcgen05", s);
+        const int dx_terms = dx_bf16 ? 1 : terms;
+        const dust_status st = dx_terms == 1 && tokens_form(N, d_in, d_out)
+                                   ? gemm_tokens(op, ld_op, d_out, W, true, G, "linear_dx_tokens_tcgen05", s)
+                                   : gemm_rows(op, ld_op, dx_terms, d_out, W, true, G, "linear_dx_tcgen05", s);
         if (st != DUST_OK) return st;
     }
     if (dW) {
