@@ -256,6 +256,13 @@ __global__ void __launch_bounds__(kRThreads) linear_rows_kernel(const __grid_con
 constexpr int kBM = 128;
 constexpr int kBK = 64;
 constexpr int kThreads = 320;  // TMA warp, MMA warp, eight epilogue warps
+// An fp32 output's kernel holds up to 128 sums a thread, and with the shared memory all taken a spilled
+// register goes to L2 (64 -> 2304 over 8192 tokens 39 us, of which a third waited for spills).  It launches three
+// warpgroups of 168 registers: the first (TMA, MMA, two idle warps) gives up 112 a thread, the two of
+// the epilogue take 56 more each: 128 x 56 + 256 x 224 = 384 x 168.
+constexpr int kPromoteThreads = 384;
+constexpr int kIssueRegs = 56, kSumRegs = 224;
+static_assert(128 * kIssueRegs + 256 * kSumRegs <= kPromoteThreads * 168, "more registers than the block has");
 constexpr uint32_t kABytes = kBM * kBK * 2;
 constexpr uint32_t kBox = kBK * 128;          // a 64-row x 64-element box of an MN-major operand
 // Each epilogue warp: 32 rows x 64 bytes of y and of z, and the biases of 32 columns.
@@ -583,6 +590,38 @@ __device__ __forceinline__ void finish(const Epilogue& E, void* y, float (&v)[kN
     __syncwarp();
 }
 
+// fp32 sums of kCols columns from o0 of the warp's rows t0 .. + 31 (lane: row), 16 columns at a time.
+template <int kCols>
+__device__ __forceinline__ void plain_out(const Epilogue& E, void* y, const float (&acc)[kCols], int64_t t0, int o0,
+                                          uint8_t* sy, int lane) {
+    const int piece = lane & 3, sub = lane >> 2;
+    float* to[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        to[i] = t0 + sub + 8 * i < E.M ? static_cast<float*>(y) + (t0 + sub + 8 * i) * E.ld_y + o0 + 4 * piece : nullptr;
+#pragma unroll
+    for (int c = 0; c < kCols / 16; ++c) {
+        if (o0 + c * 16 >= E.n_out) break;  // uniform over the warp; n_out is a multiple of 16
+#pragma unroll
+        for (int p = 0; p < 4; ++p)
+            *staged(sy, lane, p) = make_uint4(__float_as_uint(acc[16 * c + 4 * p]), __float_as_uint(acc[16 * c + 4 * p + 1]),
+                                              __float_as_uint(acc[16 * c + 4 * p + 2]), __float_as_uint(acc[16 * c + 4 * p + 3]));
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (to[i]) {
+                float4 v = *reinterpret_cast<const float4*>(staged(sy, sub + 8 * i, piece));
+                float4* at = reinterpret_cast<float4*>(to[i] + 16 * c);
+                if (E.res) {  // y itself, to be added to
+                    const float4 old = *at;
+                    v = make_float4(old.x + v.x, old.y + v.y, old.z + v.z, old.w + v.w);
+                }
+                *at = v;
+            }
+        __syncwarp();
+    }
+}
+
 // Tiles in groups of sixteen row tiles, columns slow within a group: the CTAs at work share few tiles of A and B.
 constexpr int kGroup = 16;
 __device__ __forceinline__ void tile_of(int tile, int m_tiles, int n_tiles, int& m, int& n) {
@@ -595,7 +634,7 @@ __device__ __forceinline__ void tile_of(int tile, int m_tiles, int n_tiles, int&
 // Persistent: one CTA per SM walks (tile, split) items; each accumulator (two of them) is read by the
 // epilogue warps while the MMAs fill the other.  kPromote: see kFlush.
 template <int kBN, bool kAmn, bool kBmn, int kTerms, bool kPromote, bool kPair>
-__global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_constant__ GemmArgs A) {
+__global__ void __launch_bounds__(kPromote ? kPromoteThreads : kThreads, 1) linear_gemm_kernel(const __grid_constant__ GemmArgs A) {
     using S = Shape<kBN, kTerms, kPair>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -610,55 +649,60 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_c
     const int tiles = A.m_tiles * A.n_tiles;
     const int items = tiles * A.splits;
     constexpr int kChunk = kPromote ? kFlush : 1 << 30;
+    constexpr int kFirst = kPromote ? 4 : 2;  // first epilogue warp
 
-    if (warp == 0) {
-        if (elect_one()) {
-            prefetch_tensormap(&A.ta);
-            prefetch_tensormap(&A.tb);
-            uint32_t kc = 0;
-            for (int it = first; it < items; it += step) {
-                int m, n;
-                tile_of(it % tiles, A.m_tiles, A.n_tiles, m, n);
-                const int kb0 = it / tiles * A.per_split, kb1 = min(A.k_blocks, kb0 + A.per_split);
-                const int m0 = kPair ? (2 * m + rank) * kBM : m * kBM;
-                const int n0 = n * kBN + (kPair ? rank * (kBN / 2) : 0);
-                if (!pipe_load<kBN, kAmn, kBmn, kTerms, kPair>(A, P, m0, n0, kb0, kb1, rank == 0, kc)) break;
+    if (warp < kFirst) {
+        if (kPromote) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
+        if (warp == 0) {
+            if (elect_one()) {
+                prefetch_tensormap(&A.ta);
+                prefetch_tensormap(&A.tb);
+                uint32_t kc = 0;
+                for (int it = first; it < items; it += step) {
+                    int m, n;
+                    tile_of(it % tiles, A.m_tiles, A.n_tiles, m, n);
+                    const int kb0 = it / tiles * A.per_split, kb1 = min(A.k_blocks, kb0 + A.per_split);
+                    const int m0 = kPair ? (2 * m + rank) * kBM : m * kBM;
+                    const int n0 = n * kBN + (kPair ? rank * (kBN / 2) : 0);
+                    if (!pipe_load<kBN, kAmn, kBmn, kTerms, kPair>(A, P, m0, n0, kb0, kb1, rank == 0, kc)) break;
+                }
+                if (kPair) {
+                    // the commits that free the last stages arrive here too: not before this CTA ends
+                    for (uint32_t c = kc > S::kStages ? kc - S::kStages : 0; c < kc; ++c)
+                        if (!mbar_wait_bounded(&P.empty[c % S::kStages], (c / S::kStages) & 1, A.ew, 506)) break;
+                }
             }
-            if (kPair) {
-                // the commits that free the last stages arrive here too: not before this CTA ends
-                for (uint32_t c = kc > S::kStages ? kc - S::kStages : 0; c < kc; ++c)
-                    if (!mbar_wait_bounded(&P.empty[c % S::kStages], (c / S::kStages) & 1, A.ew, 506)) break;
-            }
-        }
-    } else if (warp == 1) {
-        if (rank == 0 && elect_one()) {
-            uint32_t kc = 0;
-            uint32_t ci = 0;  // chunks so far: chunk ci goes to accumulator ci mod 2
-            bool ok = true;
-            for (int it = first; it < items && ok; it += step) {
-                const int kb0 = it / tiles * A.per_split, kb1 = min(A.k_blocks, kb0 + A.per_split);
-                for (int k = kb0; k < kb1 && ok; ++ci) {
-                    const int k2 = kb1 - k > kChunk ? k + kChunk : kb1;
-                    const uint32_t buf = ci & 1;
-                    // the epilogue of the chunk that last used this accumulator has read it
-                    if (ci >= 2 && !mbar_wait_bounded(&P.acc_empty[buf], ((ci >> 1) - 1) & 1, A.ew, 503)) {
-                        ok = false;
-                        break;
+        } else if (warp == 1) {
+            if (rank == 0 && elect_one()) {
+                uint32_t kc = 0;
+                uint32_t ci = 0;  // chunks so far: chunk ci goes to accumulator ci mod 2
+                bool ok = true;
+                for (int it = first; it < items && ok; it += step) {
+                    const int kb0 = it / tiles * A.per_split, kb1 = min(A.k_blocks, kb0 + A.per_split);
+                    for (int k = kb0; k < kb1 && ok; ++ci) {
+                        const int k2 = kb1 - k > kChunk ? k + kChunk : kb1;
+                        const uint32_t buf = ci & 1;
+                        // the epilogue of the chunk that last used this accumulator has read it
+                        if (ci >= 2 && !mbar_wait_bounded(&P.acc_empty[buf], ((ci >> 1) - 1) & 1, A.ew, 503)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        ok = pipe_mma<kBN, kAmn, kBmn, kTerms, kPair>(A, P, P.tmem + buf * kBN, k, k2, kc);
+                        commit<kPair>(&P.acc_full[buf]);
+                        k = k2;
                     }
-                    tc_fence_after();
-                    ok = pipe_mma<kBN, kAmn, kBmn, kTerms, kPair>(A, P, P.tmem + buf * kBN, k, k2, kc);
-                    commit<kPair>(&P.acc_full[buf]);
-                    k = k2;
                 }
             }
         }
     } else {
-        // epilogue warps 2 .. 9: tensor-memory lane quarter warp % 4 (32 rows), column half hf
+        if (kPromote) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
+        // eight epilogue warps: tensor-memory lane quarter warp % 4 (32 rows), column half hf
         const int q = warp & 3;
-        const int hf = (warp - 2) >> 2;
-        uint8_t* sy = P.staging + (warp - 2) * kWarpStaging;
+        const int hf = (warp - kFirst) >> 2;
+        uint8_t* sy = P.staging + (warp - kFirst) * kWarpStaging;
         uint8_t* sz = sy + 2048;
-        float4* sb = reinterpret_cast<float4*>(P.staging + 8 * kWarpStaging) + (warp - 2) * 8;
+        float4* sb = reinterpret_cast<float4*>(P.staging + 8 * kWarpStaging) + (warp - kFirst) * 8;
         constexpr int kCols = kBN / 2;
         const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
         auto release = [&](uint32_t buf) {  // the warp has read its part of the accumulator: it may be refilled
@@ -714,16 +758,25 @@ __global__ void __launch_bounds__(kThreads, 1) linear_gemm_kernel(const __grid_c
                     release(buf);
                 }
                 if (!ok) break;
-                if (A.e.res)
-                    rows_load(res, A.e.res, t0, A.e.M, A.e.ld_res * 4, static_cast<int64_t>(o0) * 4,
-                              static_cast<int64_t>(min(A.e.n_out, o0 + kCols)) * 4, lane);
-#pragma unroll
-                for (int c = 0; c < kCols / 16; ++c) {
-                    if (o0 + c * 16 < A.e.n_out) {  // uniform over the warp
+                if (kBmn) {
+                    // dW and dx: no more than the sums, added to what is there if A.e.res says so
+                    plain_out<kCols>(A.e, y, acc, t0, o0, sy, lane);
+                } else {
+                    if (A.e.res)
+                        rows_load(res, A.e.res, t0, A.e.M, A.e.ld_res * 4, static_cast<int64_t>(o0) * 4,
+                                  static_cast<int64_t>(min(A.e.n_out, o0 + kCols)) * 4, lane);
+                    // one copy of the epilogue's code, the chunk's registers picked by predicates
+#pragma unroll 1
+                    for (int c = 0; c < kCols / 16; ++c) {
+                        if (o0 + c * 16 >= A.e.n_out) break;  // uniform over the warp
                         float v[16];
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) v[j] = acc[c * 16 + j];
-                        finish<16, !kBmn>(A.e, y, v, t0, o0 + c * 16, o0 + kCols, sy, sz, sb, bias, res, c, lane);
+                        for (int k = 0; k < kCols / 16; ++k)
+                            if (k == c) {
+#pragma unroll
+                                for (int j = 0; j < 16; ++j) v[j] = acc[k * 16 + j];
+                            }
+                        finish<16, true>(A.e, y, v, t0, o0 + c * 16, o0 + kCols, sy, sz, sb, bias, res, c, lane);
                     }
                 }
             } else {
@@ -1097,8 +1150,8 @@ dust_status launch_gemm(const GemmArgs& A, cudaStream_t s) {
     const int64_t items = static_cast<int64_t>(A.m_tiles) * A.n_tiles * A.splits;
     const unsigned grid = static_cast<unsigned>(
         kPair ? 2 * std::min<int64_t>(items, num_sms() / 2) : std::min<int64_t>(items, num_sms()));
-    return dependent_launch(linear_gemm_kernel<kBN, kAmn, kBmn, kTerms, kPromote, kPair>, dim3(grid), kThreads, S::kSmem, s,
-                            kPair ? 2 : 1, A)
+    return dependent_launch(linear_gemm_kernel<kBN, kAmn, kBmn, kTerms, kPromote, kPair>, dim3(grid),
+                            kPromote ? kPromoteThreads : kThreads, S::kSmem, s, kPair ? 2 : 1, A)
                ? DUST_OK
                : DUST_ERR_CUDA;
 }
