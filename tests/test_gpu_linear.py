@@ -144,20 +144,31 @@ def test_more_tiles_than_ctas(z):
 
 
 def test_far_pre_activations(z):
-    """Infinities do not appear where the activation's limit is finite."""
+    """Far out the activations and their slopes are at their limits, at infinity too; a NaN stays one."""
     import torch
-    x = torch.zeros(20, 16, dtype=torch.bfloat16, device="cuda")
-    x[:, 0] = torch.tensor([-1e30, -1e4, -200, -90, -30, 0, 30, 90, 200, 1e4] * 2, device="cuda")
-    W = torch.eye(16, dtype=torch.bfloat16, device="cuda")
-    for N in (5, 20):
-        for act in ACTS:
-            y, pre = z.dust_linear(x[:N], W, act=act, out_dtype=torch.float32, z=True)
-            a, s = act64(x[:N].double(), act)
-            a = torch.where(torch.isnan(a), 0.0, a)  # the 64-bit forms' own infinity times zero
-            assert torch.allclose(y.double(), a, rtol=1e-5, atol=1e-5), act
-            dy = torch.ones(N, 16, device="cuda")
-            _, _, db = z.dust_linear_backward(dy, x[:N], W, act=act, z=pre, dx=None, dW=None)
-            assert bool(torch.isfinite(db).all()), act
+    inf = float("inf")
+    far = torch.tensor([-inf, -1e30, -1e4, -200, -90, -30, 0, 30, 90, 200, 1e4, 1e30, inf], device="cuda")
+    W = torch.eye(16, dtype=torch.bfloat16, device="cuda")[:, :16].contiguous()
+    for N in (1, 2, 13, 600):  # one for each form of the product
+        for k in range(0, 13, max(1, min(N, 13))):
+            x = torch.zeros(N, 16, dtype=torch.bfloat16, device="cuda")
+            # an infinite input times the zeros of W would be NaN: the bias brings the value
+            v = far[(torch.arange(N, device="cuda") + k) % 13]
+            for t in range(min(N, 13)):
+                b = torch.full((16,), float(v[t]), device="cuda")
+                for act in ACTS:
+                    y, pre = z.dust_linear(x, W, bias=b, act=act, out_dtype=torch.float32, z=True)
+                    lim = float(v[t])
+                    want = lim if act == "none" or lim > 20 else 0.0
+                    if lim == -30 or lim == 0:
+                        want = float(act64(v[t].double(), act)[0])
+                    assert torch.allclose(y, torch.full_like(y, want), rtol=1e-6, atol=1e-6), (N, act, lim, y[0, 0])
+                    dy = torch.ones(N, 16, device="cuda")
+                    _, _, db = z.dust_linear_backward(dy, x, W, act=act, z=pre, dx=None, dW=None)
+                    slope = 1.0 if act == "none" or lim > 20 else 0.0 if lim < -20 else float(act64(v[t].double(), act)[1])
+                    assert torch.allclose(db, torch.full_like(db, N * slope), rtol=1e-5, atol=1e-6), (N, act, lim, db[0])
+                if N > 2:
+                    break
 
 
 def test_residual_buffer_as_output(z):

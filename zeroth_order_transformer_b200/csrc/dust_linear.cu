@@ -4,16 +4,20 @@
 //   dz = dy act'(z),  db = sum_t dz_t,  dW = dz^T x,  dx = dz W
 //
 // Three forms of the product:
-//   linear_rows_kernel    few tokens (one sequence being extended): bound by reading W once.  A warp
-//                         holds four output rows of W against every token, 16 bytes a lane; where
-//                         there are few output rows the warps of a CTA split the contraction.
+//   linear_rows_kernel    one or two tokens: bound by reading W once.  A warp holds four output rows of W
+//                         against the tokens, 16 bytes a lane; where there are few output rows the
+//                         warps of a CTA split the contraction (8192 -> 8192 23 us, 134 MB at 5.8 TB/s).
 //   linear_gemm_kernel    tcgen05 GEMM, persistent and warp-specialised: one warp feeds a TMA ring, one
 //                         thread issues the MMAs of a 128-row tile into one of two accumulators in
 //                         tensor memory, eight warps run the epilogue of the previous tile from the other.
-//                         The forward product, dx and dW differ in which operands are MN-major.
+//                         The forward product, dx and dW differ in which operands are MN-major.  Long
+//                         contractions into bf16 take 256 x 256 tiles by pairs of CTAs (cta_group::2).
+//                         16384 tokens, 2048 <-> 8192: dx 331 us, 1.66 PFLOP/s; the forward product with GELU
+//                         and both outputs 373 us, 1.47; dW with two terms of dz 717 us, 1.53.  Run without a
+//                         pause the chip's power holds them to about 1.2 (a plain library product: 1.42).
 //   linear_tokens_kernel  the same pipeline for outputs of few tiles: W's rows are the 128 rows of an MMA, the
 //                         tokens its columns, the contraction cut over the CTAs of a cluster and
-//                         joined through distributed shared memory.
+//                         joined through distributed shared memory (24 tokens 8192 -> 8192 26 us, 5.2 TB/s).
 // dz is formed once (linear_dz_kernel) as a bf16 operand, or as hi + lo bf16 terms (dz = hi + lo to
 // about 16 bits), with the column sums for db on the way.
 #include <algorithm>
@@ -32,10 +36,76 @@ constexpr float kGeluB = 0.07135481282553578f;  // 0.044715 * 2 sqrt(2 / pi)
 constexpr float kSqrtHalf = 0.70710678118654752f;
 constexpr float kInvSqrt2Pi = 0.39894228040143268f;
 
-__device__ __forceinline__ float logistic(float u) { return __fdividef(1.0f, 1.0f + __expf(-u)); }
+__device__ __forceinline__ F2 both(float x) { return F2{x, x}; }
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float ex2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+constexpr float kLog2e = 1.4426950408889634f;
 
-// Phi(-|z|) = erfc(|z| / sqrt 2) / 2 by the rational approximation 7.1.26 of Abramowitz and Stegun
-// (error of erf at most 1.5e-7, falling with exp(-z^2 / 2)); e returns exp(-z^2 / 2), which the density shares.
+// The activations work on pairs with packed fp32 arithmetic: the GEMM epilogues have two warps to a scheduler
+// and pay for every instruction (the GELU with an exponential and a quotient an element took 4.7 us a 128 x
+// 256 tile, this one 2.1).  Infinities keep their limits: the factor that is 0 far out meets a finite number.
+//
+// z / (1 + 2^e), e = -u log2 of e
+__device__ __forceinline__ F2 gated(F2 z, F2 e) {
+    const F2 d = add2(F2{ex2_approx(e.x), ex2_approx(e.y)}, both(1.0f));
+    return mul2(F2{fmaxf(z.x, -3.0e38f), fmaxf(z.y, -3.0e38f)}, F2{rcp_approx(d.x), rcp_approx(d.y)});
+}
+template <int kAct>
+__device__ __forceinline__ F2 act_pair(F2 z) {
+    if (kAct == DUST_ACT_RELU) return F2{z.x <= 0.f ? 0.f : z.x, z.y <= 0.f ? 0.f : z.y};  // keeps a NaN
+    if (kAct == DUST_ACT_GELU) {
+        // z Phi(z) = max(z, 0) - |z| erfc(|z| / sqrt 2) / 2 with 7.1.28 of Abramowitz and Stegun, erfc(x) =
+        // (1 + a1 x + ... + a6 x^6)^-16 to 3e-7: one reciprocal, no exponential.  0 from |z| = 64 on.
+        const F2 az{fminf(fabsf(z.x), 64.0f), fminf(fabsf(z.y), 64.0f)};
+        const F2 x = mul2(az, both(kSqrtHalf));
+        F2 p = fma2(both(0.0000430638f), x, both(0.0002765672f));
+        p = fma2(p, x, both(0.0001520143f));
+        p = fma2(p, x, both(0.0092705272f));
+        p = fma2(p, x, both(0.0422820123f));
+        p = fma2(p, x, both(0.0705230784f));
+        p = fma2(p, x, both(1.0f));
+        p = mul2(p, p);
+        p = mul2(p, p);
+        p = mul2(p, p);
+        p = mul2(p, p);  // overflows to infinity far out: its reciprocal is 0
+        const F2 r{rcp_approx(p.x), rcp_approx(p.y)};
+        return fma2(mul2(az, both(-0.5f)), r, F2{z.x < 0.f ? 0.f : z.x, z.y < 0.f ? 0.f : z.y});
+    }
+    if (kAct == DUST_ACT_GELU_TANH)
+        return gated(z, mul2(z, fma2(mul2(z, z), both(-kGeluB * kLog2e), both(-kGeluA * kLog2e))));
+    if (kAct == DUST_ACT_SILU) return gated(z, mul2(z, both(-kLog2e)));
+    return z;
+}
+__device__ __forceinline__ float act_any(int act, float z) {
+    switch (act) {
+        case DUST_ACT_RELU: return act_pair<DUST_ACT_RELU>(both(z)).x;
+        case DUST_ACT_GELU: return act_pair<DUST_ACT_GELU>(both(z)).x;
+        case DUST_ACT_GELU_TANH: return act_pair<DUST_ACT_GELU_TANH>(both(z)).x;
+        case DUST_ACT_SILU: return act_pair<DUST_ACT_SILU>(both(z)).x;
+    }
+    return z;
+}
+template <int kAct, int kN>
+__device__ __forceinline__ void act_all(float (&v)[kN]) {
+#pragma unroll
+    for (int j = 0; j < kN; j += 2) {
+        const F2 y = act_pair<kAct>(F2{v[j], v[j + 1]});
+        v[j] = y.x;
+        v[j + 1] = y.y;
+    }
+}
+
+// Slopes, for the backward pass's HBM-bound sweep.  Phi(-|z|) = erfc(|z| / sqrt 2) / 2 by 7.1.26 of Abramowitz and
+// Stegun (error of erf at most 1.5e-7, falling with exp(-z^2 / 2)); e returns exp(-z^2 / 2), which the density shares.
+__device__ __forceinline__ float logistic(float u) { return __fdividef(1.0f, 1.0f + __expf(-u)); }
 __device__ __forceinline__ float lower_tail(float z, float& e) {
     const float x = fabsf(z) * kSqrtHalf;
     const float t = __fdividef(1.0f, fmaf(0.3275911f, x, 1.0f));
@@ -45,19 +115,6 @@ __device__ __forceinline__ float lower_tail(float z, float& e) {
     p = fmaf(p, t, -0.284496736f);
     p = fmaf(p, t, 0.254829592f);
     return 0.5f * p * t * e;
-}
-
-template <int kAct>
-__device__ __forceinline__ float act_fn(float z) {
-    if (kAct == DUST_ACT_RELU) return z <= 0.f ? 0.f : z;  // keeps a NaN
-    if (kAct == DUST_ACT_GELU) {
-        float e;
-        const float q = z * lower_tail(z, e);
-        return z > 0.f ? z - q : q;
-    }
-    if (kAct == DUST_ACT_GELU_TANH) return z * logistic(z * fmaf(kGeluB, z * z, kGeluA));
-    if (kAct == DUST_ACT_SILU) return z * logistic(z);
-    return z;
 }
 // Far from zero the slope's second term is 0 times something that may have overflowed: it is dropped.
 template <int kAct>
@@ -79,68 +136,6 @@ __device__ __forceinline__ float act_slope(float z) {
         return pq == 0.f ? p : fmaf(pq, z, p);
     }
     return 1.f;
-}
-__device__ __forceinline__ float act_any(int act, float z) {
-    switch (act) {
-        case DUST_ACT_RELU: return act_fn<DUST_ACT_RELU>(z);
-        case DUST_ACT_GELU: return act_fn<DUST_ACT_GELU>(z);
-        case DUST_ACT_GELU_TANH: return act_fn<DUST_ACT_GELU_TANH>(z);
-        case DUST_ACT_SILU: return act_fn<DUST_ACT_SILU>(z);
-    }
-    return z;
-}
-// The same on pairs with packed fp32 arithmetic, for the GEMM epilogues, which have two warps to a scheduler
-// and so pay for every instruction (a 128 x 256 tile with act_fn's GELU took 4.7 us longer than one without).
-__device__ __forceinline__ F2 both(float x) { return F2{x, x}; }
-__device__ __forceinline__ float rcp_approx(float x) {
-    float y;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ float ex2_approx(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-constexpr float kLog2e = 1.4426950408889634f;
-// z / (1 + 2^e); e = -u log2 of e
-__device__ __forceinline__ F2 gated(F2 z, F2 e) {
-    const F2 d = add2(F2{ex2_approx(e.x), ex2_approx(e.y)}, both(1.0f));
-    return mul2(z, F2{rcp_approx(d.x), rcp_approx(d.y)});
-}
-template <int kAct>
-__device__ __forceinline__ F2 act_pair(F2 z) {
-    if (kAct == DUST_ACT_GELU) {
-        // z Phi(z) = max(z, 0) - |z| erfc(|z| / sqrt 2) / 2 with 7.1.28 of Abramowitz and Stegun, erfc(x) =
-        // (1 + a1 x + ... + a6 x^6)^-16 to 3e-7: one reciprocal, no exponential
-        const F2 az{fabsf(z.x), fabsf(z.y)};
-        const F2 x = mul2(az, both(kSqrtHalf));
-        F2 p = fma2(both(0.0000430638f), x, both(0.0002765672f));
-        p = fma2(p, x, both(0.0001520143f));
-        p = fma2(p, x, both(0.0092705272f));
-        p = fma2(p, x, both(0.0422820123f));
-        p = fma2(p, x, both(0.0705230784f));
-        p = fma2(p, x, both(1.0f));
-        p = mul2(p, p);
-        p = mul2(p, p);
-        p = mul2(p, p);
-        p = mul2(p, p);  // overflows to infinity far out: its reciprocal is 0
-        const F2 r{rcp_approx(p.x), rcp_approx(p.y)};
-        return fma2(mul2(az, both(-0.5f)), r, F2{z.x < 0.f ? 0.f : z.x, z.y < 0.f ? 0.f : z.y});
-    }
-    if (kAct == DUST_ACT_GELU_TANH)
-        return gated(z, mul2(z, fma2(mul2(z, z), both(-kGeluB * kLog2e), both(-kGeluA * kLog2e))));
-    if (kAct == DUST_ACT_SILU) return gated(z, mul2(z, both(-kLog2e)));
-    return F2{act_fn<kAct>(z.x), act_fn<kAct>(z.y)};
-}
-template <int kAct, int kN>
-__device__ __forceinline__ void act_all(float (&v)[kN]) {
-#pragma unroll
-    for (int j = 0; j < kN; j += 2) {
-        const F2 y = act_pair<kAct>(F2{v[j], v[j + 1]});
-        v[j] = y.x;
-        v[j + 1] = y.y;
-    }
 }
 template <int kN>
 __device__ __forceinline__ void act_block(int act, float (&v)[kN]) {
@@ -521,8 +516,9 @@ __device__ __forceinline__ void rows_stage(const Rows& r, uint8_t* buf, int lane
 }
 
 // Bias, pre-activation, activation, residual and store of kN columns from o of the warp's rows t0 .. + 31 (lane:
-// row), chunk c of the warp's columns, which end at o_end; bias: those of its columns 4 lane .. + 3.  kN = 32 for a bf16 y, 16 for an fp32 one: 64 bytes of a row.  kLayer false: no bias, z or activation.
-// All lanes call it.
+// row), chunk c of the warp's columns, which end at o_end; bias: those of its columns 4 lane .. + 3; res: the
+// residual's rows of this chunk.  kN = 32 for a bf16 y, 16 for an fp32 one: 64 bytes of a row.  kLayer false: no
+// bias, z or activation.  All lanes call it.
 template <int kN, bool kLayer>
 __device__ __forceinline__ void finish(const Epilogue& E, void* y, float (&v)[kN], int64_t t0, int o, int o_end, uint8_t* sy,
                                        uint8_t* sz, float4* sb, float4 bias, Rows& res, int c, int lane) {
