@@ -122,6 +122,48 @@ def test_steps(z, bits, kind, grad, gs):
     steps(z, opt, decay, lrs, 3, kind, gs, 2)
 
 
+def test_eight_bit_codes_are_those_of_the_fp32_formulas(z):
+    """Codes and scales bit for bit, against the formulas evaluated with one fp32 rounding an operation (numpy's
+    fp32 arithmetic, and a conversion to e4m3 by rounding to its steps in 64 bits)."""
+    import numpy as np
+    import torch
+    f = np.float32
+    n = 256 * 2000
+    rng = np.random.default_rng(11)
+    size = np.exp(rng.standard_normal(n // 256).repeat(256)).astype(f)
+    W = [torch.zeros(n, device="cuda")]
+    G = torch.zeros(n, device="cuda")
+    opt = z.DustOptimizer(W, [G], bits=8)
+    gs = f(0.3)
+    m, r = np.zeros(n, f), np.zeros(n, f)
+
+    def hold(x, least):
+        b = x.reshape(-1, 256)
+        top = np.abs(b).max(1)
+        near = (b * (f(448) / top)[:, None]).astype(f)
+        near = np.where(near > 0, np.maximum(near, f(least)), near).astype(np.float64)
+        step = np.exp2(np.floor(np.log2(np.maximum(np.abs(near), 2.0 ** -6))) - 3)
+        code = np.rint(near / step) * step
+        scale = (top * (f(1) / f(448))).astype(f)
+        return code.astype(f), scale, (code.astype(f) * scale[:, None]).astype(f).reshape(-1)
+
+    for t in range(1, 5):
+        g = (rng.standard_normal(n).astype(f) * size).astype(f)
+        G.copy_(torch.from_numpy(g))
+        opt.step(z.adam(1e-3, t), g_scale=torch.tensor([float(gs)], device="cuda"))
+        g = (g * gs).astype(f)
+        m = m * f(0.9) + g * f(1 - 0.9)
+        r = np.sqrt((r * r) * f(0.999) + (g * g) * f(1 - 0.999))
+        for name, x, least in (("m", m, 0.0), ("v", r, 2.0 ** -9)):
+            code, scale, held_x = hold(x, least)
+            assert np.array_equal(getattr(opt, name + "_scale")[0].cpu().numpy(), scale), (name, t)
+            assert np.array_equal(getattr(opt, name)[0].float().cpu().numpy(), code.reshape(-1)), (name, t)
+            if name == "m":
+                m = held_x
+            else:
+                r = held_x
+
+
 @pytest.mark.parametrize("bits", [32, 8])
 @pytest.mark.parametrize("count", [32, 33, 256, 257, 300])
 def test_many_tensors(z, bits, count):

@@ -111,11 +111,15 @@ __device__ __forceinline__ F2 both(float x) { return F2{x, x}; }
 
 // Two elements of an 8-bit tensor: m and r = sqrt(v) in, m' and r' out.  The moments are formed with
 // one rounding for each product, sum and root, so that the codes are those of the formulas evaluated
-// step by step in fp32 (a contraction into a multiply-add moves one code in a million by a step).
+// step by step in fp32.  (Contracted into multiply-adds they move one code in a million by a step; packed
+// products and sums are contracted in spite of their rounding modifiers, the scalar intrinsics are not.)
+__device__ __forceinline__ float blend(float a, float b, float x, float c) {  // a b + x c
+    return __fadd_rn(__fmul_rn(a, b), __fmul_rn(x, c));
+}
 __device__ __forceinline__ void update8(const OptParams& o, const OptTensor& t, Bias b, F2 g, F2& w, F2& m, F2& r) {
-    m = add2(mul2(m, both(o.b1)), mul2(g, both(o.omb1)));
-    const F2 v = add2(mul2(mul2(r, r), both(o.b2)), mul2(mul2(g, g), both(o.omb2)));
-    r = F2{__fsqrt_rn(v.x), __fsqrt_rn(v.y)};
+    m = F2{blend(m.x, o.b1, g.x, o.omb1), blend(m.y, o.b1, g.y, o.omb1)};
+    r = F2{__fsqrt_rn(blend(__fmul_rn(r.x, r.x), o.b2, __fmul_rn(g.x, g.x), o.omb2)),
+           __fsqrt_rn(blend(__fmul_rn(r.y, r.y), o.b2, __fmul_rn(g.y, g.y), o.omb2))};
     w = fma2(both(-t.lr_wd), w, w);
     const F2 den = fma2(r, both(b.i2), both(o.eps)), num = mul2(m, both(b.i1));
     w = fma2(both(-t.lr), mul2(num, F2{rcp_approx(den.x), rcp_approx(den.y)}), w);
@@ -291,9 +295,9 @@ __device__ __forceinline__ void step_block(const OptParams& o, const OptTensor& 
     for (int h = 0; h < 2; ++h) {
         m[h] = from_e4m3(x.cm[h]);
         r[h] = from_e4m3(x.cr[h]);
-        const F2 g0 = mul2(F2{x.g[h].x, x.g[h].y}, both(gs)), g1 = mul2(F2{x.g[h].z, x.g[h].w}, both(gs));
-        F2 m0 = mul2(F2{m[h].x, m[h].y}, both(sm)), m1 = mul2(F2{m[h].z, m[h].w}, both(sm));
-        F2 r0 = mul2(F2{r[h].x, r[h].y}, both(sr)), r1 = mul2(F2{r[h].z, r[h].w}, both(sr));
+        const F2 g0{__fmul_rn(x.g[h].x, gs), __fmul_rn(x.g[h].y, gs)}, g1{__fmul_rn(x.g[h].z, gs), __fmul_rn(x.g[h].w, gs)};
+        F2 m0{__fmul_rn(m[h].x, sm), __fmul_rn(m[h].y, sm)}, m1{__fmul_rn(m[h].z, sm), __fmul_rn(m[h].w, sm)};
+        F2 r0{__fmul_rn(r[h].x, sr), __fmul_rn(r[h].y, sr)}, r1{__fmul_rn(r[h].z, sr), __fmul_rn(r[h].w, sr)};
         F2 w0{x.w[h].x, x.w[h].y}, w1{x.w[h].z, x.w[h].w};
         update8(o, t, b, g0, w0, m0, r0);
         update8(o, t, b, g1, w1, m1, r1);
