@@ -352,6 +352,7 @@ def test_binding_refuses(z):
         with pytest.raises(ValueError):
             bad()
     for bad in (lambda: z.dust_linear(x.float(), W), lambda: z.dust_linear(x, W, residual=y),
+                lambda: z.dust_linear(x, W, out_dtype=torch.float16), lambda: z.dust_linear_backward(y, x, W, dx_dtype=torch.float16),
                 lambda: z.dust_linear(x, W, y=y, out_dtype=torch.bfloat16),
                 lambda: z.dust_linear_backward(y.half(), x, W)):
         with pytest.raises(TypeError):

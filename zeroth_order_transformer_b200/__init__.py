@@ -634,6 +634,8 @@ def dust_linear(x, W, bias=None, act: str = "none", residual=None, y=None, z=Non
     if y is None:
         y = x.new_empty((N, d_out), dtype=out_dtype or bf)
         ld_y = d_out
+        if y.dtype not in _dtypes():
+            raise TypeError(f"out_dtype must be bf16 or fp32, not {out_dtype}")
     else:
         if out_dtype is not None and y.dtype != out_dtype:
             raise TypeError(f"y is {y.dtype}, out_dtype {out_dtype}")
