@@ -1283,40 +1283,54 @@ dust_status gemm_rows(const void* a, int64_t ld_a, int terms, int K, const void*
     return st;
 }
 
-// dW [d_out, d_in] (+)= dz^T x: 128 x 256 tiles (in pairs they take as long: two terms already
-// load 64 KB for 1024 cycles of MMAs), the tokens in as many splits as cost least: the waves of
-// items over the SMs (about 0.45 us a block of 64 tokens and 2 us an item) and, with more than one, the
-// partials written and read back at about 6 GB/ms and one more launch.  The partials are added in order.
+// dW [d_out, d_in] (+)= dz^T x: 128-row tiles (in pairs they take as long: two terms already load 64 KB for
+// 1024 cycles of MMAs).  Tile width and splits of the tokens are those that cost least: the waves of items over
+// the SMs, an item's blocks of 64 tokens and its epilogue (us, about as measured), and, with more than one
+// split, the partials written and read back at about 6 GB/ms and one more launch.  The partials are added in order.
+// (256 x 256 over 64 tokens 6.7 us with 256 columns a tile, 1024 x 1024 over 5001 18 us either way.)
 constexpr int kMinBlocks = 4;
 constexpr int kMaxSplits = 64;
 struct DwPlan {
-    int m_tiles, n_tiles, k_blocks, splits, per_split;
+    int bn, m_tiles, n_tiles, k_blocks, splits, per_split;
 };
 DwPlan dw_plan(int64_t N, int32_t d_in, int32_t d_out) {
-    DwPlan p;
+    DwPlan p{};
     p.m_tiles = (d_out + kBM - 1) / kBM;
-    p.n_tiles = (d_in + 255) / 256;
     p.k_blocks = static_cast<int>((N + kBK - 1) / kBK);
-    const int64_t tiles = static_cast<int64_t>(p.m_tiles) * p.n_tiles;
     const double bytes = 8.0 * d_out * d_in;
-    int64_t S = 1;
+    struct Width {
+        int bn;
+        double block, epilogue;
+    };
     double least = 0;
-    for (int64_t k = 1; k <= kMaxSplits && (k == 1 || p.k_blocks / k >= kMinBlocks); ++k) {
-        const double waves = static_cast<double>((tiles * k + num_sms() - 1) / num_sms());
-        const double cost = waves * (0.45 * static_cast<double>((p.k_blocks + k - 1) / k) + 2.0) +
-                            (k > 1 ? 3.0 + k * bytes / 6e6 : 0.0);
-        if (k == 1 || cost < least) {
-            least = cost;
-            S = k;
+    for (const Width w : {Width{256, 0.45, 4.2}, Width{128, 0.32, 2.4}, Width{64, 0.26, 1.5}}) {
+        const int n_tiles = (d_in + w.bn - 1) / w.bn;
+        const int64_t tiles = static_cast<int64_t>(p.m_tiles) * n_tiles;
+        for (int64_t k = 1; k <= kMaxSplits && (k == 1 || p.k_blocks / k >= kMinBlocks); ++k) {
+            const double waves = static_cast<double>((tiles * k + num_sms() - 1) / num_sms());
+            const int64_t per = (p.k_blocks + k - 1) / k;
+            const double cost = waves * (w.block * static_cast<double>(per) + w.epilogue) +
+                                (k > 1 ? 3.0 + static_cast<double>(k) * bytes / 6e6 : 0.0);
+            if (p.bn == 0 || cost < least) {
+                least = cost;
+                p.bn = w.bn;
+                p.n_tiles = n_tiles;
+                p.per_split = static_cast<int>(per);
+            }
         }
     }
-    p.per_split = static_cast<int>((p.k_blocks + S - 1) / S);
     p.splits = (p.k_blocks + p.per_split - 1) / p.per_split;  // none of them empty
     return p;
 }
 size_t dw_bytes(int64_t N, int32_t d_in, int32_t d_out) {
     const DwPlan p = dw_plan(N, d_in, d_out);
     return p.splits > 1 ? align_up(static_cast<size_t>(p.splits) * d_out * d_in * 4, 256) : 0;
+}
+template <int kTerms>
+dust_status launch_dw(int bn, const GemmArgs& A, cudaStream_t s) {
+    return bn == 256   ? launch_gemm<256, true, true, kTerms, true, false>(A, s)
+           : bn == 128 ? launch_gemm<128, true, true, kTerms, true, false>(A, s)
+                       : launch_gemm<64, true, true, kTerms, true, false>(A, s);
 }
 dust_status gemm_dw(const void* dz, int64_t ld_dz, int terms, const void* x, int64_t ld_x, int64_t N, int32_t d_in,
                     int32_t d_out, float* dW, int accumulate, float* part, cudaStream_t s) {
@@ -1341,8 +1355,7 @@ dust_status gemm_dw(const void* dz, int64_t ld_dz, int terms, const void* x, int
         !make_tmap_bf16_2d_ld(&G.tb, x, static_cast<uint64_t>(N), d_in, ld_x, kBK, 64))
         return DUST_ERR_CUDA;
     prof_begin(s);
-    const dust_status st = terms == 2 ? launch_gemm<256, true, true, 2, true, false>(G, s)
-                                      : launch_gemm<256, true, true, 1, true, false>(G, s);
+    const dust_status st = terms == 2 ? launch_dw<2>(p.bn, G, s) : launch_dw<1>(p.bn, G, s);
     prof_end(s, "linear_dw_tcgen05");
     if (st != DUST_OK || p.splits == 1) return st;
     const int64_t n4 = G.split_elems / 4;
