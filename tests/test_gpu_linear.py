@@ -112,7 +112,7 @@ def test_few_tokens(z, N, d_in, d_out):
 
 
 @pytest.mark.parametrize("N,d_in,d_out", [(9, 128, 64), (24, 2048, 512), (128, 4112, 80), (129, 784, 336), (100, 64, 4112), (17, 320, 1040),
-                                          (300, 1552, 16)])
+                                          (300, 1552, 16), (60, 1552, 400), (200, 2576, 1296), (513, 4112, 272)])
 def test_contraction_over_a_cluster(z, N, d_in, d_out):
     """Few output tiles and contractions of one to many blocks, shares that are short or empty among them."""
     for k, out in enumerate(("bf16", "f32")):

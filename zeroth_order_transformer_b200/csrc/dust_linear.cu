@@ -1152,18 +1152,23 @@ dust_status launch_gemm(const GemmArgs& A, cudaStream_t s) {
                : DUST_ERR_CUDA;
 }
 
-// Output tile width: the one whose waves of tiles over the SMs cost least, a tile of 128 x bn taking
-// about as long as the larger of its MMAs (bn) and its operand loads (bn + 128, at 0.6 each).
-int choose_bn(int64_t m_tiles, int n_out) {
+// Output tile width: the one that costs least, an SM's tiles one after the other, each as long as the longer of its
+// blocks of 64 and the epilogue of the one before it, and the last epilogue (us, about as measured).
+int choose_bn(int64_t m_tiles, int n_out, int k_blocks) {
+    struct Width {
+        int bn;
+        double block, epilogue;
+    };
     int best = 0;
     double least = 0;
-    for (int bn : {256, 128, 64}) {
-        const int64_t tiles = m_tiles * ((n_out + bn - 1) / bn);
+    for (const Width w : {Width{256, 0.41, 2.5}, Width{128, 0.28, 1.3}, Width{64, 0.23, 0.7}}) {
+        const int64_t tiles = m_tiles * ((n_out + w.bn - 1) / w.bn);
         const double cost = static_cast<double>((tiles + num_sms() - 1) / num_sms()) *
-                            std::max<double>(bn, 0.6 * (bn + 128));
+                                std::max(w.block * k_blocks, w.epilogue) +
+                            w.epilogue;
         if (best == 0 || cost < least) {
             least = cost;
-            best = bn;
+            best = w.bn;
         }
     }
     return best;
@@ -1209,13 +1214,13 @@ int token_width(int64_t N) { return N <= 16 ? 16 : N <= 32 ? 32 : N <= 64 ? 64 :
 
 // Whether linear_tokens_kernel takes the product.  Up to 32 tokens always (24 tokens, 8192 -> 24576: 77 us against 93 in the
 // persistent kernel, 2048 -> 65536 63 against 67; with 64 tokens 81 against 56, its sums leaving through shared
-// memory one by one); more where a long contraction is shared (8192 -> 2048 over 512 tokens 31 us against 43, over
-// 1024, where the tiles fill the SMs, 56 against 47; 1024 -> 1024 over 1024 tokens 11.3 against 9.5).
+// memory one by one); more where a long contraction is shared (here and in the persistent kernel: 64 tokens 2048 ->
+// 2048 6.1 and 7.8 us, 512 tokens 11.7 and 8.6; 512 tokens 8192 -> 2048 23 and 31; 64 tokens 2048 -> 8192 11.5 and 10.3).
 bool tokens_form(int64_t N, int n_out, int K) {
     if (N <= 32) return true;
     const int tok = token_width(N), k_blocks = (K + kBK - 1) / kBK;
     const int r = token_ranks((N + tok - 1) / tok * ((n_out + kBM - 1) / kBM), k_blocks);
-    return r == 4 ? k_blocks >= 12 : r == 2 && k_blocks >= 32;
+    return r == 4 ? k_blocks >= (N <= 64 ? 24 : 40) : r == 2 && k_blocks >= 64;
 }
 
 // y [N, n_out] = x W^T, or with w_mn x W (W [K, n_out]).
@@ -1256,7 +1261,7 @@ dust_status gemm_rows(const void* a, int64_t ld_a, int terms, int K, const void*
     const int64_t M = G.e.M;
     const int n_out = G.e.n_out;
     const int64_t m_tiles = (M + kBM - 1) / kBM;
-    const int bn = choose_bn(m_tiles, n_out);
+    const int bn = choose_bn(m_tiles, n_out, (K + kBK - 1) / kBK);
     G.ew = device_error_word();
     G.term_rows = M;
     G.split_elems = 0;
