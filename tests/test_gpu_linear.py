@@ -311,6 +311,53 @@ def test_backward_repeats_bit_for_bit(z):
     assert all(torch.equal(p, q) for p, q in zip(a, b))
 
 
+@pytest.mark.parametrize("act", ["none", "gelu"])
+@pytest.mark.parametrize("N,d", [(40, 256), (700, 512), (5001, 1024)])
+@pytest.mark.parametrize("outs", ["dx dW db", "dx db", "dx dW"])
+def test_calls_in_a_row_equal_calls_waited_for(z, act, N, d, outs):
+    """The kernels of a call overlap one another and those of the next call.  A chain in which dx is the next
+    call's dy and its x, dW accumulates and one workspace serves all of it gives the bits of a chain with a
+    wait after every call, launched eagerly and replayed from a graph."""
+    import torch
+    g = _gen(23)
+    dy0, x0, pre = _bf(g, N, d), _bf(g, N, d), _bf(g, N, d)
+    W = _bf(g, d, d, std=d ** -0.5)
+    ws = torch.empty(z.dust_workspace_size(z.DUST_OP_LINEAR_BACKWARD, z.DUST_BF16, N, d, d, 0), dtype=torch.uint8,
+                     device="cuda")
+    bufs = [torch.empty_like(dy0) for _ in range(6)]
+    dW = torch.zeros(d, d, device="cuda") if "dW" in outs else None
+    db = [torch.zeros(d, device="cuda") for _ in bufs] if "db" in outs else None
+
+    def chain(wait):
+        dy, x = dy0, x0
+        if dW is not None:
+            dW.zero_()
+        for i, out in enumerate(bufs):
+            if db is not None:
+                db[i].zero_()
+            z.dust_linear_backward(dy, x, W, act, z=pre if act != "none" else None, dx=out, dW=dW,
+                                   db=db[i] if db is not None else None, accumulate=True, workspace=ws)
+            if wait:
+                torch.cuda.synchronize()
+            x, dy = dy, out
+
+    def held():
+        return [t.clone() for t in bufs + (db or []) + ([dW] if dW is not None else [])]
+
+    chain(True)
+    want = held()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        chain(False)
+    for run in (lambda: chain(False), graph.replay) * 3:
+        for t in bufs:
+            t.zero_()
+        run()
+        for a, b in zip(held(), want):
+            assert torch.equal(a, b)
+
+
 def test_other_stream_and_graph(z):
     """On a stream of the caller's, and captured: a replay computes from what the buffers then hold."""
     import torch

@@ -430,7 +430,8 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void*
 
 // Programmatic dependent launch: a kernel launched with dependent_launch (dust_internal.h) may start while the one
 // before it on the stream still runs; pdl_wait returns when that one has completed and its writes are
-// visible.  Every thread calls it before its first access to global memory.  pdl_trigger lets the next kernel start.
+// visible.  Every thread calls it before its first access to global memory that the one before may write.
+// pdl_trigger lets the next kernel start.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 

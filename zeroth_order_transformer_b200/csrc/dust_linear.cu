@@ -298,7 +298,20 @@ struct GemmArgs {
     int64_t term_rows;   // rows of A from the first term to the second
     int64_t split_elems; // elements of y from one split's partial to the next
     int k_blocks, per_split, splits, m_tiles, n_tiles;
+    int late;  // dW only: see pdl_begin
 };
+
+// What late means: the kernel uses nothing that the one before it writes, so that it starts while that one still runs
+// and waits for it at its end only, for those that come after.  Each kernel here triggers behind its own wait: what
+// lies further back has then completed.  dW runs so beside the last tiles of dx, the column sums of a dz
+// that is dy itself beside all of dx (1024 -> 1024 over 5001 tokens, all three outputs in a graph: 33 us, one after the other 38).
+__device__ __forceinline__ void pdl_begin(int late) {
+    if (!late) pdl_wait();
+    pdl_trigger();
+}
+__device__ __forceinline__ void pdl_end(int late) {
+    if (late) pdl_wait();
+}
 
 // One thread of a converged warp.  The warps that issue TMA and MMAs take it in place of a lane test: with
 // it the compiler keeps descriptors in uniform registers (24 tokens 8192 -> 2048: 11.8 us from 15.9).
@@ -636,8 +649,7 @@ __global__ void __launch_bounds__(kPromote ? kPromoteThreads : kThreads, 1) line
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
     const Pipe P = pipe_setup<kBN, kTerms, kPair>(smem, 8);
-    pdl_trigger();
-    pdl_wait();
+    pdl_begin(kAmn && A.late);
     const int warp = warp_index(), lane = threadIdx.x & 31;
     const int rank = kPair ? static_cast<int>(blockIdx.x & 1) : 0;  // the clusters are CTAs 2 i, 2 i + 1
     const int first = kPair ? static_cast<int>(blockIdx.x >> 1) : static_cast<int>(blockIdx.x);
@@ -813,6 +825,7 @@ __global__ void __launch_bounds__(kPromote ? kPromoteThreads : kThreads, 1) line
         cluster_wait();
     }
     if (warp == 1) tmem_free<kPair>(P.tmem, S::kTmemCols);
+    pdl_end(kAmn && A.late);
 }
 
 // Few tokens, more than a handful: W streams through the tensor cores as the operand of 128 rows (output
@@ -868,8 +881,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tokens_kernel(const __grid
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *slot;
-    pdl_trigger();
-    pdl_wait();
+    pdl_begin(0);
     cluster_arrive();  // waited for before the first remote store: the peers are running by then
     const int ranks = A.splits, rank = static_cast<int>(blockIdx.x) % ranks;
     const int o0 = static_cast<int>(blockIdx.x) / ranks * kBM;
@@ -1005,23 +1017,6 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tokens_kernel(const __grid
     if (warp == 1) tmem_dealloc(tmem, S::kTmemCols);
 }
 
-// out (+)= the sum of S partials in order, four elements a thread.
-__global__ void __launch_bounds__(256) linear_join_kernel(const float4* __restrict__ part, int S, int64_t n4, float4* out,
-                                                          int accumulate) {
-    pdl_trigger();
-    pdl_wait();
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n4;
-         i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-        float4 s = accumulate ? out[i] : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-        for (int k = 0; k < S; ++k) {
-            const float4 v = __ldcs(part + static_cast<int64_t>(k) * n4 + i);
-            s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
-        }
-        out[i] = s;
-    }
-}
-
 // ------------------------------------------------------------------ dz and its column sums
 constexpr int kDThreads = 256;
 constexpr int kDWarps = kDThreads / 32;
@@ -1041,14 +1036,13 @@ struct DzArgs {
     __nv_bfloat16* lo;  // [N, d_out], or null
     float* part;        // [row chunks, d_out] column sums, or null
     int64_t N, ld_dy, ld_z;
-    int d_out, rows;
+    int d_out, rows, late;
 };
 
 template <typename T, int kAct>
 __global__ void __launch_bounds__(kDThreads) linear_dz_kernel(const __grid_constant__ DzArgs A) {
     __shared__ float sh[kDWarps][kDCols + 8];
-    pdl_trigger();
-    pdl_wait();
+    pdl_begin(A.late);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int col = blockIdx.x * kDCols + lane * 8;
     const int64_t r0 = static_cast<int64_t>(blockIdx.y) * A.rows;
@@ -1097,7 +1091,7 @@ __global__ void __launch_bounds__(kDThreads) linear_dz_kernel(const __grid_const
             }
         }
     }
-    if (!A.part) return;
+    if (!A.part) return;  // never late
 #pragma unroll
     for (int j = 0; j < 8; ++j) sh[warp][lane * 8 + j] = s[j];
     __syncthreads();
@@ -1107,28 +1101,50 @@ __global__ void __launch_bounds__(kDThreads) linear_dz_kernel(const __grid_const
         for (int w = 0; w < kDWarps; ++w) a += sh[w][threadIdx.x];
         A.part[static_cast<int64_t>(blockIdx.y) * A.d_out + c] = a;
     }
+    pdl_end(A.late);
 }
 
-// db (+)= the partial sums: 32 columns a CTA, its eight warps over consecutive runs of chunks.
-__global__ void __launch_bounds__(256) linear_db_kernel(const float* part, int chunks, int d_out, float* db,
-                                                        int accumulate) {
+// What the partial sums still lack, in one launch: db (+)= its chunks' sums, 32 columns a CTA, the CTA's eight warps over
+// consecutive runs of chunks; then dW (+)= the sum of its splits in order, four elements a thread.
+struct JoinArgs {
+    const float* db_part;
+    float* db;
+    const float4* dw_part;
+    float4* dW;
+    int64_t n4;
+    int chunks, d_out, db_blocks, splits, accumulate;
+};
+
+__global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant__ JoinArgs A) {
     __shared__ float sh[8][32];
-    pdl_trigger();
-    pdl_wait();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int c = blockIdx.x * 32 + lane;
-    const int per = (chunks + 7) / 8;
-    const int a = warp * per, b = min(chunks, a + per);
-    float s = 0.f;
-    if (c < d_out) {
+    pdl_begin(0);
+    if (static_cast<int>(blockIdx.x) < A.db_blocks) {
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        const int c = blockIdx.x * 32 + lane;
+        const int per = (A.chunks + 7) / 8;
+        const int a = warp * per, b = min(A.chunks, a + per);
+        float s = 0.f;
+        if (c < A.d_out) {
 #pragma unroll 4
-        for (int k = a; k < b; ++k) s += __ldg(part + static_cast<int64_t>(k) * d_out + c);
+            for (int k = a; k < b; ++k) s += __ldg(A.db_part + static_cast<int64_t>(k) * A.d_out + c);
+        }
+        sh[warp][lane] = s;
+        __syncthreads();
+        if (warp == 0 && c < A.d_out) {
+            for (int w = 1; w < 8; ++w) s += sh[w][lane];
+            A.db[c] = A.accumulate ? A.db[c] + s : s;
+        }
+        return;
     }
-    sh[warp][lane] = s;
-    __syncthreads();
-    if (warp == 0 && c < d_out) {
-        for (int w = 1; w < 8; ++w) s += sh[w][lane];
-        db[c] = accumulate ? db[c] + s : s;
+    const int64_t step = static_cast<int64_t>(gridDim.x - A.db_blocks) * blockDim.x;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x - A.db_blocks) * blockDim.x + threadIdx.x; i < A.n4; i += step) {
+        float4 s = A.accumulate ? A.dW[i] : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+        for (int k = 0; k < A.splits; ++k) {
+            const float4 v = __ldcs(A.dw_part + static_cast<int64_t>(k) * A.n4 + i);
+            s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
+        }
+        A.dW[i] = s;
     }
 }
 
@@ -1338,9 +1354,10 @@ dust_status launch_dw(int bn, const GemmArgs& A, cudaStream_t s) {
                        : launch_gemm<64, true, true, kTerms, true, false>(A, s);
 }
 dust_status gemm_dw(const void* dz, int64_t ld_dz, int terms, const void* x, int64_t ld_x, int64_t N, int32_t d_in,
-                    int32_t d_out, float* dW, int accumulate, float* part, cudaStream_t s) {
+                    int32_t d_out, float* dW, int accumulate, float* part, int late, JoinArgs& join, cudaStream_t s) {
     const DwPlan p = dw_plan(N, d_in, d_out);
     GemmArgs G{};
+    G.late = late;
     G.e.M = d_out;
     G.e.n_out = d_in;
     G.e.y = p.splits > 1 ? part : dW;
@@ -1362,14 +1379,13 @@ dust_status gemm_dw(const void* dz, int64_t ld_dz, int terms, const void* x, int
     prof_begin(s);
     const dust_status st = terms == 2 ? launch_dw<2>(p.bn, G, s) : launch_dw<1>(p.bn, G, s);
     prof_end(s, "linear_dw_tcgen05");
-    if (st != DUST_OK || p.splits == 1) return st;
-    const int64_t n4 = G.split_elems / 4;
-    prof_begin(s);
-    const unsigned blocks = static_cast<unsigned>(std::min<int64_t>((n4 + 255) / 256, static_cast<int64_t>(num_sms()) * 16));
-    const bool ok = dependent_launch(linear_join_kernel, dim3(blocks), 256, 0, s, 1, reinterpret_cast<const float4*>(part),
-                                     p.splits, n4, reinterpret_cast<float4*>(dW), accumulate);
-    prof_end(s, "linear_dw_join");
-    return ok ? DUST_OK : DUST_ERR_CUDA;
+    if (p.splits > 1) {
+        join.dw_part = reinterpret_cast<const float4*>(part);
+        join.dW = reinterpret_cast<float4*>(dW);
+        join.n4 = G.split_elems / 4;
+        join.splits = p.splits;
+    }
+    return st;
 }
 
 template <typename T>
@@ -1440,25 +1456,30 @@ dust_status linear_backward_launch(const void* dy, int dy_bf16, int64_t ld_dy, c
     const bool direct = act == DUST_ACT_NONE && dy_bf16;
     const bool products = dx || dW;
     if (direct) terms = 1;
-    if (db || (products && !direct)) {
+    JoinArgs join{};
+    join.accumulate = accumulate;
+    const auto sweep = [&](int late) {
         const int rows = dz_rows(N, d_out), chunks = static_cast<int>((N + rows - 1) / rows);
-        DzArgs A{dy, static_cast<const __nv_bfloat16*>(z), nullptr, nullptr, db ? part : nullptr, N, ld_dy, ld_z, d_out, rows};
+        DzArgs A{dy,    static_cast<const __nv_bfloat16*>(z), nullptr, nullptr, db ? part : nullptr, N, ld_dy, ld_z, d_out,
+                 rows, late};
         if (products && !direct) {
             A.hi = hi;
             A.lo = terms == 2 ? hi + N * d_out : nullptr;
         }
+        if (db) {
+            join.db_part = part;
+            join.db = db;
+            join.chunks = chunks;
+            join.d_out = d_out;
+            join.db_blocks = (d_out + 31) / 32;
+        }
         const dim3 grid((d_out + kDCols - 1) / kDCols, chunks);
         prof_begin(s);
-        bool ok = dy_bf16 ? launch_dz<__nv_bfloat16>(A, act, grid, s) : launch_dz<float>(A, act, grid, s);
+        const bool ok = dy_bf16 ? launch_dz<__nv_bfloat16>(A, act, grid, s) : launch_dz<float>(A, act, grid, s);
         prof_end(s, "linear_dz");
-        if (ok && db) {
-            prof_begin(s);
-            ok = dependent_launch(linear_db_kernel, dim3((d_out + 31) / 32), 256, 0, s, 1, static_cast<const float*>(part),
-                                  chunks, d_out, db, accumulate);
-            prof_end(s, "linear_db");
-        }
-        if (!ok) return DUST_ERR_CUDA;
-    }
+        return ok;
+    };
+    if (products && !direct && !sweep(0)) return DUST_ERR_CUDA;
     const void* op = direct ? dy : hi;
     const int64_t ld_op = direct ? ld_dy : d_out;
     if (dx) {
@@ -1475,9 +1496,20 @@ dust_status linear_backward_launch(const void* dy, int dy_bf16, int64_t ld_dy, c
                                    : gemm_rows(op, ld_op, dx_terms, d_out, W, true, G, "linear_dx_tcgen05", s);
         if (st != DUST_OK) return st;
     }
+    if (db && (direct || !products) && !sweep(dx != nullptr)) return DUST_ERR_CUDA;
     if (dW) {
-        const dust_status st = gemm_dw(op, ld_op, terms, x, ld_x, N, d_in, d_out, dW, accumulate, split, s);
+        // dz is complete once dx has begun, or is dy
+        const int late = dx || (direct && db);
+        const dust_status st = gemm_dw(op, ld_op, terms, x, ld_x, N, d_in, d_out, dW, accumulate, split, late, join, s);
         if (st != DUST_OK) return st;
+    }
+    if (join.db || join.dW) {
+        const unsigned blocks =
+            static_cast<unsigned>(std::min<int64_t>((join.n4 + 255) / 256, static_cast<int64_t>(num_sms()) * 16));
+        prof_begin(s);
+        const bool ok = dependent_launch(linear_join_kernel, dim3(blocks + join.db_blocks), 256, 0, s, 1, join);
+        prof_end(s, "linear_join");
+        if (!ok) return DUST_ERR_CUDA;
     }
     return cudaGetLastError() == cudaSuccess ? DUST_OK : DUST_ERR_CUDA;
 }
