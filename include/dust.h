@@ -172,6 +172,8 @@ dust_status dust_linear_backward(const void* dy, dust_dtype dy_dt, int64_t ld_dy
 dust_status dust_embedding(const int32_t* ids, const void* E, dust_dtype dt, int64_t ld_E, int64_t N, int32_t V,
                            int32_t d, float scale, void* out, dust_dtype out_dt, int64_t ld_out, void* stream);
 
+#define DUST_EMBEDDING_SMALL 4096
+
 /*
  * The gradient of the embedding table, the weight estimate of a layer whose input is one-hot:
  *   G[v] (+)= scale sum_{t: ids_t = v} g_t
@@ -180,7 +182,8 @@ dust_status dust_embedding(const int32_t* ids, const void* E, dust_dtype dt, int
  * adds to the rows that have tokens and leaves the others (for a table shared with the output layer).
  * Tokens whose id is outside [0, V) add nothing.  Sums in fp32, in token order within runs of sorted
  * tokens: deterministic.  N <= 2^26, V < 2^31 - 1.
- * workspace: dust_workspace_size(DUST_OP_EMBEDDING_GRAD, dt, N, V, d, 0) bytes (0 for up to 4096 tokens).
+ * workspace: dust_workspace_size(DUST_OP_EMBEDDING_GRAD, dt, N, V, d, 0) bytes (0 for up to
+ * DUST_EMBEDDING_SMALL tokens).
  */
 dust_status dust_embedding_grad(const int32_t* ids, const void* g, dust_dtype dt, int64_t ld_g, int64_t N,
                                 int32_t V, int32_t d, float scale, float* G, int64_t ld_G, int accumulate,

@@ -47,6 +47,7 @@ DUST_ACTS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 DUST_STATE_F32 = 0
 DUST_STATE_E4M3 = 1
 DUST_STATE_BLOCK = 256
+DUST_EMBEDDING_SMALL = 4096
 
 EXPORTED_SYMBOLS = (
     "dust_noisy_linear_fwd", "dust_credit", "dust_weight_grad", "dust_workspace_size",
@@ -546,21 +547,32 @@ def _dtypes() -> dict:
     return _DT
 
 
+_HOST: list = []
+
+
+def _host():
+    """(current device, raw handle of a device's current stream), as functions, looked up once: the smallest calls take
+    as long as the host's part of them."""
+    if not _HOST:
+        C = _torch()._C
+        _HOST[:] = C._cuda_getDevice, C._cuda_getCurrentRawStream
+    return _HOST
+
+
 def _raw_stream(index: int) -> int:
-    return _torch()._C._cuda_getCurrentRawStream(index)
+    return _host()[1](index)
 
 
 def _scope(index: int, stream):
     """What a call has to run under: its tensors' device, and its stream, so that outputs and workspaces
     that the call allocates belong to the stream that uses them.  None if it is current already."""
-    torch = _torch()
     if index < 0:
         raise ValueError("the tensors must be CUDA tensors")
     if stream is None:
-        return None if index == torch._C._cuda_getDevice() else torch.cuda.device(index)
+        return None if index == _host()[0]() else _torch().cuda.device(index)
     if stream.device.index != index:
         raise ValueError(f"stream is on {stream.device}, the tensors are on cuda:{index}")
-    return torch.cuda.stream(stream)
+    return _torch().cuda.stream(stream)
 
 
 def _rows(t, name: str, rows: int, cols: int, index: int, only=None) -> int:
@@ -585,7 +597,7 @@ def _flat(t, name: str, n: int, index: int, dtype):
 def _new_rows(like, rows: int, cols: int, dtype, vec: int):
     """A new [rows, cols] matrix whose rows begin at multiples of `vec` elements, and its row stride."""
     if cols % vec == 0:
-        return like.new_empty((rows, cols), dtype=dtype), cols
+        return like.new_empty(rows, cols, dtype=dtype), cols
     ld = -(-cols // vec) * vec
     return like.new_empty((rows, ld), dtype=dtype)[:, :cols], ld
 
@@ -632,7 +644,7 @@ def dust_linear(x, W, bias=None, act: str = "none", residual=None, y=None, z=Non
     if bias is not None:
         _flat(bias, "bias", d_out, dev, f32)
     if y is None:
-        y = x.new_empty((N, d_out), dtype=out_dtype or bf)
+        y = x.new_empty(N, d_out, dtype=out_dtype)  # x's, bf16, by default
         ld_y = d_out
         if y.dtype not in _dtypes():
             raise TypeError(f"out_dtype must be bf16 or fp32, not {out_dtype}")
@@ -643,7 +655,7 @@ def dust_linear(x, W, bias=None, act: str = "none", residual=None, y=None, z=Non
     ld_res = _rows(residual, "residual", N, d_out, dev, y.dtype) if residual is not None else 0
     keep = z is not None and z is not False
     if z is True:
-        z = x.new_empty((N, d_out))
+        z = x.new_empty(N, d_out)
     ld_z = _rows(z, "z", N, d_out, dev, bf) if keep else 0
     st = lib().dust_linear(x.data_ptr(), ld_x, W.data_ptr(), _ptr(bias), _act_code(act), _ptr(residual), ld_res,
                            DUST_BF16, N, d_in, d_out, y.data_ptr(), _dtypes()[y.dtype], ld_y,
@@ -681,9 +693,9 @@ def dust_linear_backward(dy, x, W, act: str = "none", z=None, dx=True, dW=True, 
     if accumulate and (dW is True or db is True):
         raise ValueError("accumulate adds to given dW and db tensors; pass them, or None to skip them")
     if dx is True:
-        dx = x.new_empty((N, d_in), dtype=dx_dtype or bf)
+        dx = x.new_empty(N, d_in, dtype=dx_dtype)
     if dW is True:
-        dW = x.new_empty((d_out, d_in), dtype=f32)
+        dW = x.new_empty(d_out, d_in, dtype=f32)
     if db is True:
         db = x.new_empty(d_out, dtype=f32)
     dx, dW, db = (None if t is False else t for t in (dx, dW, db))
@@ -764,7 +776,8 @@ def dust_embedding_grad(ids, g, V: int, scale: float = 1.0, G=None, accumulate: 
     else:
         G, ld_G = _new_rows(g, V, d, torch.float32, 4)
     dt = _dtypes()[g.dtype]
-    at, nb, ws = _new_workspace(workspace, dust_workspace_size(DUST_OP_EMBEDDING_GRAD, dt, N, V, d, 0), g)
+    nb = 0 if N <= DUST_EMBEDDING_SMALL else dust_workspace_size(DUST_OP_EMBEDDING_GRAD, dt, N, V, d, 0)
+    at, nb, ws = _new_workspace(workspace, nb, g)
     st = lib().dust_embedding_grad(ids.data_ptr(), g.data_ptr(), dt, ld_g, N, V, d, scale, G.data_ptr(), ld_G,
                                    1 if accumulate else 0, at, nb, _raw_stream(dev))
     if st:

@@ -505,7 +505,7 @@ __global__ void __launch_bounds__(kGThreads) embed_join_kernel(const __grid_cons
 }
 
 // ------------------------------------------------------------------ small batches in one launch
-constexpr int kSmallTokens = 4096;
+constexpr int kSmallTokens = DUST_EMBEDDING_SMALL;
 constexpr int kRankTokens = 512;  // up to which a share is sorted by rank (2000 tokens 10.0 us, bitonic 11.5)
 
 struct SmallArgs {
