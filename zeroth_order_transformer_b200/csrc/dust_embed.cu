@@ -21,7 +21,8 @@
 //
 // Both are HBM-bound: the rows read and written once.  Measured: the lookup above 5.3 TB/s of the bytes it cannot do
 // without (every row is read from L2, 537 MB, where 137 MB of them differ); the gradient of 65536 tokens onto
-// 65536 x 2048 156 us, 800 MB and so 5.1 TB/s with the sort, its sums alone 141 us.
+// 65536 x 2048 153 us, 800 MB and so 5.2 TB/s with the sort, its sums alone 126 us.  Clearing in the sort's launches
+// instead, which leave HBM idle, took 203 us: writes alone run at about half the rate of reads and writes together.
 #include <algorithm>
 
 #include "dust_device.cuh"
