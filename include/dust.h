@@ -121,7 +121,7 @@ dust_status dust_noisy_linear_output(const void* x, const void* W, dust_dtype dt
  * NULL; residual: [N, ld_res] of type out_dt or NULL; y: [N, ld_y] of type out_dt (fp32 or bf16);
  * z: optional bf16 [N, ld_z], the pre-activation for dust_linear_backward (NULL to skip).
  * Row strides (elements) at least the row and a multiple of 16 bytes; all pointers 16-byte
- * aligned.  y may be the residual's buffer (with the same stride); other overlaps are undefined.
+ * aligned.  y may be the residual's buffer (with the same stride); other overlaps are not allowed.
  * Sums in fp32; each output is rounded once.  Rows behind N and columns behind d_out are not
  * written.  One and two tokens stream W through the CUDA cores, more go to the tensor cores, in forms
  * chosen by the sizes, so the last bits of a token's sums can depend on how many tokens the call has.
@@ -152,8 +152,8 @@ dust_status dust_linear(const void* x, int64_t ld_x, const void* W, const float*
  * fp32 [d_out, d_in]; db: fp32 [d_out]; each NULL to skip, not all three.  accumulate != 0 adds to
  * dW and db (dx is always overwritten).
  * dz enters the tensor cores as g_terms bf16 terms (as g in dust_weight_grad) in dW and in an fp32
- * dx; a bf16 dx takes one term.  A bf16 dy without an activation is exact in one.  dx may not
- * overlap an input.  N <= 8388607.
+ * dx; a bf16 dx takes one term.  A bf16 dy without an activation is exact in one.  No output
+ * may overlap an input or another output.  N <= 8388607.
  * workspace: dust_workspace_size(DUST_OP_LINEAR_BACKWARD, DUST_BF16, N, d_in, d_out, 0) bytes.
  * Deterministic.
  */

@@ -122,6 +122,23 @@ def test_workspace_sizes():
     assert eg(10, 10, 0) == 0
 
 
+def test_outputs_that_are_inputs_are_refused():
+    """Each buffer at an address of its own but for one pair."""
+    q = [P * (i + 1) for i in range(10)]
+    at = dict(x=q[0], W=q[1], bias=q[2], res=q[3], y=q[4], zz=q[5])
+    for out, others in (("y", ("x", "W", "bias")), ("zz", ("x", "W", "bias", "res", "y"))):
+        for o in others:
+            assert _linear(**{**at, out: at[o]}) == 1, (out, o)
+    assert _linear(**{**at, "y": at["res"], "ld_y": 72}) == 1
+    at = dict(dy=q[0], zz=q[1], x=q[2], W=q[3], dx=q[4], dW=q[5], db=q[6])
+    for out in ("dx", "dW", "db"):
+        for o in at:
+            if o != out:
+                assert _back(**{**at, out: at[o]}) == 1, (out, o)
+    assert _emb(ids=q[0], E=q[1], out=q[1]) == 1 and _emb(ids=q[0], E=q[1], out=q[0]) == 1
+    assert _egrad(ids=q[0], g=q[1], G=q[1]) == 1 and _egrad(ids=q[0], g=q[1], G=q[0]) == 1
+
+
 def test_binding_refuses_cpu_tensors():
     import torch
     x, W = torch.zeros(4, 16, dtype=torch.bfloat16), torch.zeros(16, 16, dtype=torch.bfloat16)

@@ -5,6 +5,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cmath>
+#include <initializer_list>
 #include <mutex>
 #include <vector>
 
@@ -264,6 +265,14 @@ bool valid_ld(int64_t ld, int64_t cols, int64_t vec) {
     return ld >= cols && ld % vec == 0 && ld < (1LL << 38);
 }
 
+// Whether an output begins where one of the other buffers does (rows of several matrices may lie between one another,
+// so that ranges that meet are not a mistake).
+bool same_start(const void* out, std::initializer_list<const void*> others) {
+    for (const void* p : others)
+        if (out && out == p) return true;
+    return false;
+}
+
 dust_status check_ws(void* ws, size_t have, size_t need) {
     if (need == 0) return DUST_OK;
     if (!ws || !aligned256(ws) || have < need) return DUST_ERR_WORKSPACE;
@@ -392,6 +401,8 @@ dust_status dust_linear(const void* x, int64_t ld_x, const void* W, const float*
         (residual && !valid_ld(ld_res, d_out, out_vec)) || (z && !valid_ld(ld_z, d_out, 8)))
         return DUST_ERR_INVALID_ARG;
     if (dt != DUST_BF16 || d_in % 16 != 0 || d_out % 16 != 0 || N > 1073741823LL) return DUST_ERR_UNSUPPORTED;
+    if (same_start(y, {x, W, bias}) || same_start(z, {x, W, bias, residual, y}) || (residual == y && ld_res != ld_y))
+        return DUST_ERR_INVALID_ARG;
     return linear_launch(x, ld_x, W, bias, act, residual, ld_res, N, d_in, d_out, y, out_dt == DUST_BF16 ? 1 : 0,
                          ld_y, z, ld_z, static_cast<cudaStream_t>(stream));
 }
@@ -414,6 +425,8 @@ dust_status dust_linear_backward(const void* dy, dust_dtype dy_dt, int64_t ld_dy
     if (dt != DUST_BF16 || d_in % 16 != 0 || d_out % 16 != 0 || N > 8388607LL) return DUST_ERR_UNSUPPORTED;
     const dust_status st = check_ws(workspace, ws_bytes, linear_backward_workspace_bytes(N, d_in, d_out));
     if (st != DUST_OK) return st;
+    if (same_start(dx, {dy, z, x, W}) || same_start(dW, {dy, z, x, W, dx}) || same_start(db, {dy, z, x, W, dx, dW}))
+        return DUST_ERR_INVALID_ARG;
     return linear_backward_launch(dy, dy_dt == DUST_BF16 ? 1 : 0, ld_dy, z, ld_z, x, ld_x, W, act, N, d_in, d_out,
                                   g_terms, dx, dx_dt == DUST_BF16 ? 1 : 0, ld_dx, dW, db, accumulate, workspace,
                                   static_cast<cudaStream_t>(stream));
@@ -427,6 +440,7 @@ dust_status dust_embedding(const int32_t* ids, const void* E, dust_dtype dt, int
         !valid_ld(ld_E, d, dt == DUST_BF16 ? 8 : 4) || !valid_ld(ld_out, d, out_dt == DUST_BF16 ? 8 : 4))
         return DUST_ERR_INVALID_ARG;
     if (N > 2147483647LL) return DUST_ERR_UNSUPPORTED;
+    if (same_start(out, {ids, E})) return DUST_ERR_INVALID_ARG;
     return embedding_launch(ids, E, dt, ld_E, N, V, d, scale, out, out_dt, ld_out,
                             static_cast<cudaStream_t>(stream));
 }
@@ -442,6 +456,7 @@ dust_status dust_embedding_grad(const int32_t* ids, const void* g, dust_dtype dt
     if (N > (1LL << 26) || V > 2147483646) return DUST_ERR_UNSUPPORTED;
     const dust_status st = check_ws(workspace, ws_bytes, embedding_grad_workspace_bytes(dt, N, V, d));
     if (st != DUST_OK) return st;
+    if (same_start(G, {ids, g})) return DUST_ERR_INVALID_ARG;
     return embedding_grad_launch(ids, g, dt, ld_g, N, V, d, scale, G, ld_G, accumulate, workspace,
                                  static_cast<cudaStream_t>(stream));
 }
