@@ -108,6 +108,26 @@ def test_gradient_of_special_batches(z, kind, N):
         grad_case(z, ids, V, d, dt, 0.5, accumulate, 5)
 
 
+@pytest.mark.parametrize("N", [4097, 8192, 8193, 12345, 16384, 16385])
+@pytest.mark.parametrize("V", [1, 5, 511, 512, 70001, 1 << 20])
+def test_sort_of_middle_batches(z, N, V):
+    """Whole-number gradients below 2^24 in sum: every order of the sums gives the same bits, a lost, doubled or
+    misplaced token does not."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(N + V)
+    d = 12
+    ids = torch.randint(-3, V + 3, (N,), device="cuda", dtype=torch.int32, generator=g)
+    ids[N // 3: N // 2] = min(V - 1, 77)  # a long run
+    gr = torch.randint(-500, 500, (N, d), device="cuda", generator=g).float()
+    want = torch.zeros(V, d, dtype=torch.float64, device="cuda")
+    ok = (ids >= 0) & (ids < V)
+    want.index_add_(0, ids[ok].long(), gr[ok].double())
+    for acc in (False, True):
+        G = torch.full((V, d), 7.0, device="cuda")
+        z.dust_embedding_grad(ids, gr, V, G=G, accumulate=acc)
+        assert torch.equal(G.double(), want + (7.0 if acc else 0.0))
+
+
 def test_long_chunks(z):
     """Enough tokens for chunks longer than 32, with ids that cross many of them."""
     import torch

@@ -9,8 +9,8 @@
 // The gradient is a sum over the tokens of each row, and the tokens of a row are scattered over
 // the batch.  They are brought together by a stable radix sort of the token indices by id
 // (least significant digit first, up to nine bits a pass: a vocabulary of 2^18 takes two), which
-// moves 8 bytes a token where a row is hundreds to thousands.  The sorted positions are cut into
-// chunks of equal length; one warp sums a chunk's rows over 128 (fp32) or 256 (bf16) columns,
+// moves 8 bytes a token where a row is hundreds to thousands; up to 16384 tokens are sorted by one cluster in
+// one launch.  The sorted positions are cut into chunks of equal length; one warp sums a chunk's rows over 128 (fp32) or 256 (bf16) columns,
 // sixteen bytes a lane, eight rows in flight, and writes a table row whenever the id changes.  An id
 // that crosses a chunk border leaves partial sums, which a last kernel adds in chunk order: no
 // sum depends on the order of atomics, and every run gives the same result.  Rows that no token names are
@@ -209,7 +209,8 @@ __device__ __forceinline__ void tile_ranks(const uint32_t (&digit)[kSRounds], in
     __syncthreads();
 }
 
-// Exclusive prefix sum over the kBins threads of the CTA.
+// Exclusive prefix sum over the CTA's 32 kWarps threads.
+template <int kWarps>
 __device__ __forceinline__ int32_t scan_bins(int32_t x, int32_t* sh) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int32_t s = x;
@@ -221,13 +222,13 @@ __device__ __forceinline__ int32_t scan_bins(int32_t x, int32_t* sh) {
     if (lane == 31) sh[warp] = s;
     __syncthreads();
     if (warp == 0) {
-        int32_t w = lane < kSWarps ? sh[lane] : 0;
+        int32_t w = lane < kWarps ? sh[lane] : 0;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int32_t y = __shfl_up_sync(0xFFFFFFFFu, w, o);
             if (lane >= o) w += y;
         }
-        if (lane < kSWarps) sh[lane] = w;
+        if (lane < kWarps) sh[lane] = w;
     }
     __syncthreads();
     const int32_t r = s - x + (warp > 0 ? sh[warp - 1] : 0);
@@ -254,7 +255,7 @@ __global__ void __launch_bounds__(kSThreads) embed_scatter_kernel(
         all += c;
         if (t < tile) earlier += c;
     }
-    const int32_t base = scan_bins(all, sh) + earlier;
+    const int32_t base = scan_bins<kSWarps>(all, sh) + earlier;
     constexpr int kTile = kSThreads * kSRounds;
     const int64_t p0 = static_cast<int64_t>(tile) * kTile;
     const int n = static_cast<int>(min(static_cast<int64_t>(kTile), N - p0));
@@ -281,6 +282,125 @@ __global__ void __launch_bounds__(kSThreads) embed_scatter_kernel(
             idx_out[pos[r]] = val[r];
         }
     }
+}
+
+// The same sort of up to kClusterTokens tokens in one launch: a cluster of eight CTAs, each with an eighth of the list
+// in shared memory.  A pass counts, exchanges the counts, and sends each key to its place in the CTA that holds it.
+// (8000 tokens onto 4096 x 768, added: 23.2 us in a graph, with the launches above 25.6; 16000 29.0 and 30.8; 32000, eight
+// keys a thread, 46.1 and 42.7.)
+constexpr int kCCtas = 8, kCThreads = kBins, kCWarps = kCThreads / 32;  // a thread for each bin
+constexpr int kCMost = 4;  // keys of a thread
+constexpr int64_t kClusterTokens = static_cast<int64_t>(kCCtas) * kCThreads * kCMost;
+template <int kKeys>
+constexpr size_t cluster_smem() {
+    return kCWarps * kBins * 4 + kBins * 4 + 2ull * kCThreads * kKeys * 8;
+}
+
+template <int kKeys>
+__global__ void __launch_bounds__(kCThreads) embed_sort_kernel(const int32_t* __restrict__ ids, int32_t N, int32_t V, int bits,
+                                                               int passes, uint32_t* keys_out, int32_t* idx_out) {
+    extern __shared__ uint64_t csm[];
+    constexpr int kTile = kCThreads * kKeys;
+    uint64_t* list = csm;  // [2][kTile] key and token
+    int32_t(*wh)[kBins] = reinterpret_cast<int32_t(*)[kBins]>(csm + 2 * kTile);
+    int32_t* count = reinterpret_cast<int32_t*>(wh + kCWarps);
+    __shared__ int32_t sh[32];
+    pdl_trigger();
+    pdl_wait();
+    const int rank = static_cast<int>(blockIdx.x), warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t mask = (1u << bits) - 1u, below = (1u << lane) - 1u;
+    const int n = max(0, min(kTile, N - rank * kTile));  // of this CTA's part
+    for (int pass = 0; pass < passes; ++pass) {
+        uint64_t item[kKeys];
+        int32_t digit[kKeys], pos[kKeys];
+#pragma unroll
+        for (int r = 0; r < kKeys; ++r) {
+            const int at = (warp * kKeys + r) * 32 + lane;
+            item[r] = 0;
+            if (at < n) {
+                const int32_t t = rank * kTile + at;
+                item[r] = pass == 0 ? static_cast<uint64_t>(key_of(__ldg(ids + t), V)) << 32 | static_cast<uint32_t>(t)
+                                    : list[(pass & 1) * kTile + at];
+            }
+            digit[r] = static_cast<int32_t>(static_cast<uint32_t>(item[r] >> 32) >> (pass * bits) & mask);
+        }
+        // each key's place among its warp's keys of its digit
+#pragma unroll
+        for (int w = 0; w < kCWarps; ++w) wh[w][threadIdx.x] = 0;
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < kKeys; ++r) {
+            const bool mine = (warp * kKeys + r) * 32 + lane < n;
+            const uint32_t same = __match_any_sync(0xFFFFFFFFu, mine ? digit[r] : -1);
+            int before = 0;
+            if (mine) before = wh[warp][digit[r]];
+            __syncwarp();
+            pos[r] = before + __popc(same & below);
+            if (mine && (same & below) == 0) wh[warp][digit[r]] = before + __popc(same);
+            __syncwarp();
+        }
+        __syncthreads();
+        const int bin = threadIdx.x;
+        int32_t have[kCWarps], all = 0, earlier = 0;
+#pragma unroll
+        for (int w = 0; w < kCWarps; ++w) have[w] = wh[w][bin];
+#pragma unroll
+        for (int w = 0; w < kCWarps; ++w) all += have[w];
+        count[bin] = all;
+        cluster_arrive();
+        cluster_wait();
+        int32_t c[kCCtas];
+#pragma unroll
+        for (int k = 0; k < kCCtas; ++k) {
+            uint32_t from;
+            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(from) : "r"(smem_u32(count + bin)), "r"(k));
+            asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(c[k]) : "r"(from) : "memory");
+        }
+        all = 0;
+#pragma unroll
+        for (int k = 0; k < kCCtas; ++k) {
+            all += c[k];
+            if (k < rank) earlier += c[k];
+        }
+        int32_t run = scan_bins<kCWarps>(all, sh) + earlier;
+#pragma unroll
+        for (int w = 0; w < kCWarps; ++w) {
+            wh[w][bin] = run;
+            run += have[w];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < kKeys; ++r) {
+            if ((warp * kKeys + r) * 32 + lane >= n) continue;
+            const int32_t to = pos[r] + wh[warp][digit[r]];
+            if (pass + 1 == passes) {
+                keys_out[to] = static_cast<uint32_t>(item[r] >> 32);
+                idx_out[to] = static_cast<int32_t>(static_cast<uint32_t>(item[r]));
+            } else {
+                uint32_t there;
+                asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                             : "=r"(there)
+                             : "r"(smem_u32(list + ((pass + 1) & 1) * kTile + to % kTile)), "r"(to / kTile));
+                asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(there), "l"(item[r]) : "memory");
+            }
+        }
+        // the keys are in place, and the counts have been read
+        cluster_arrive();
+        cluster_wait();
+    }
+}
+
+template <int kKeys>
+bool launch_cluster_sort(const int32_t* ids, int64_t N, int32_t V, int bits, int passes, uint32_t* keys, int32_t* idx,
+                         cudaStream_t s) {
+    static PerContextOnce attr;
+    if (!attr.run([] {
+            return cudaFuncSetAttribute(embed_sort_kernel<kKeys>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        static_cast<int>(cluster_smem<kKeys>())) == cudaSuccess;
+        }))
+        return false;
+    return dependent_launch(embed_sort_kernel<kKeys>, dim3(kCCtas), kCThreads, cluster_smem<kKeys>(), s, kCCtas, ids,
+                            static_cast<int32_t>(N), V, bits, passes, keys, idx);
 }
 
 // ------------------------------------------------------------------ the sums
@@ -507,7 +627,7 @@ __global__ void __launch_bounds__(kGThreads) embed_join_kernel(const __grid_cons
 
 // ------------------------------------------------------------------ small batches in one launch
 constexpr int kSmallTokens = DUST_EMBEDDING_SMALL;
-constexpr int kRankTokens = 512;  // up to which a share is sorted by rank (2000 tokens 10.0 us, bitonic 11.5)
+constexpr int kRankTokens = 512;  // up to which a share is sorted by rank (2000 tokens 9.1 us in a graph; before, 10.0 and bitonic 11.5)
 
 struct SmallArgs {
     const int32_t* ids;
@@ -534,16 +654,24 @@ __global__ void __launch_bounds__(kGThreads) embed_grad_small_kernel(const __gri
     // this share's tokens, in any order: the sort puts them right
     if (threadIdx.x == 0) *count = 0;
     __syncthreads();
-    for (int t0 = 0; t0 < A.N; t0 += kGThreads) {
-        const int t = t0 + threadIdx.x;
-        const int32_t id = t < A.N ? __ldg(A.ids + t) : -1;
-        const bool mine = id >= 0 && id < A.V && (id & (A.shares - 1)) == share;
-        const uint32_t vote = __ballot_sync(0xFFFFFFFFu, mine);
-        if (vote == 0) continue;  // uniform over the warp
-        int at = 0;
-        if (lane == 0) at = atomicAdd(count, __popc(vote));
-        at = __shfl_sync(0xFFFFFFFFu, at, 0) + __popc(vote & ((1u << lane) - 1u));
-        if (mine) list[at] = (static_cast<uint64_t>(id) << 32) | static_cast<uint32_t>(t);
+    for (int t0 = 0; t0 < A.N; t0 += 4 * kGThreads) {
+        int32_t id[4];  // on their way together (2000 tokens 9.2 us in a graph, one at a time 10.2)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int t = t0 + j * kGThreads + threadIdx.x;
+            id[j] = t < A.N ? __ldg(A.ids + t) : -1;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const bool mine = id[j] >= 0 && id[j] < A.V && (id[j] & (A.shares - 1)) == share;
+            const uint32_t vote = __ballot_sync(0xFFFFFFFFu, mine);
+            if (vote == 0) continue;  // uniform over the warp
+            int at = 0;
+            if (lane == 0) at = atomicAdd(count, __popc(vote));
+            at = __shfl_sync(0xFFFFFFFFu, at, 0) + __popc(vote & ((1u << lane) - 1u));
+            if (mine)
+                list[at] = (static_cast<uint64_t>(id[j]) << 32) | static_cast<uint32_t>(t0 + j * kGThreads + threadIdx.x);
+        }
     }
     __syncthreads();
     const int n = *count;
@@ -552,13 +680,23 @@ __global__ void __launch_bounds__(kGThreads) embed_grad_small_kernel(const __gri
     if (n <= kRankTokens) {
         // few keys: each one's place is the number of smaller ones
         uint64_t* to = list + kSmallTokens / 2;
-        for (int i = threadIdx.x; i < n; i += kGThreads) {
-            const uint64_t k = list[i];
-            int place = 0;
-#pragma unroll 4
+        static_assert(kRankTokens == 2 * kGThreads, "up to two keys a thread");
+        const int i = threadIdx.x, i2 = i + kGThreads;
+        const uint64_t k = i < n ? list[i] : 0, k2 = i2 < n ? list[i2] : 0;
+        int place = 0, place2 = 0;
+        if (n <= kGThreads) {
+#pragma unroll 8
             for (int j = 0; j < n; ++j) place += list[j] < k;
-            to[place] = k;
+        } else {  // both in one go (3000 tokens 15.0 us, one after the other 16.6)
+#pragma unroll 4
+            for (int j = 0; j < n; ++j) {
+                const uint64_t other = list[j];
+                place += other < k;
+                place2 += other < k2;
+            }
         }
+        if (i < n) to[place] = k;
+        if (i2 < n) to[place2] = k2;
         sorted = to;
         __syncthreads();
     } else {  // bitonic
@@ -773,7 +911,15 @@ dust_status embedding_grad_launch(const int32_t* ids, const void* g, dust_dtype 
     float* tail = reinterpret_cast<float*>(w + 4 * p.keys + p.hist + p.part);
     const uint32_t mask = (1u << p.bits) - 1u;
     int at = 1;  // where the sorted list ends up
-    for (int pass = 0; pass < p.passes; ++pass) {
+    if (N <= kClusterTokens) {
+        const int per = kCCtas * kCThreads;
+        prof_begin(s);
+        const bool ok = N <= 2 * per ? launch_cluster_sort<2>(ids, N, V, p.bits, p.passes, key[at], idx[at], s)
+                                     : launch_cluster_sort<kCMost>(ids, N, V, p.bits, p.passes, key[at], idx[at], s);
+        prof_end(s, "embedding_sort");
+        if (!ok) return DUST_ERR_CUDA;
+    }
+    for (int pass = 0; N > kClusterTokens && pass < p.passes; ++pass) {
         const int32_t* first = pass == 0 ? ids : nullptr;
         const int to = at ^ 1, shift = pass * p.bits;
         const bool few = N < kManyTokens;

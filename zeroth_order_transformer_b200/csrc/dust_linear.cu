@@ -333,8 +333,6 @@ struct Pipe {
 // the sums, and half of B's columns, so that an SM loads 32 KB a block where one alone loads 48.  The even CTA
 // issues the MMAs for both; its full barriers take the bytes of both CTAs' loads, its commits free the
 // stages and announce the sums in both.
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 __device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
     uint32_t r;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
