@@ -286,8 +286,8 @@ __global__ void __launch_bounds__(kSThreads) embed_scatter_kernel(
 
 // The same sort of up to kClusterTokens tokens in one launch: a cluster of eight CTAs, each with an eighth of the list
 // in shared memory.  A pass counts, exchanges the counts, and sends each key to its place in the CTA that holds it.
-// (8000 tokens onto 4096 x 768, added: 23.2 us in a graph, with the launches above 25.6; 16000 29.0 and 30.8; 32000, eight
-// keys a thread, 46.1 and 42.7.)
+// (8000 tokens onto 4096 x 768, added: 2.4 us less than with the launches above, 16000 1.8; 32000, eight keys a thread,
+// 3.4 more.)
 constexpr int kCCtas = 8, kCThreads = kBins, kCWarps = kCThreads / 32;  // a thread for each bin
 constexpr int kCMost = 4;  // keys of a thread
 constexpr int64_t kClusterTokens = static_cast<int64_t>(kCCtas) * kCThreads * kCMost;
@@ -585,9 +585,11 @@ __global__ void __launch_bounds__(kGThreads) embed_grad_kernel(const __grid_cons
         put_row(A.G + static_cast<int64_t>(cur) * A.ld_G + col, acc, n, A.scale, A.accumulate != 0);
 }
 
-// CTA (chunk, 512 columns): if an id begins in the chunk and goes on past its end, adds its partial
-// sums.  Two halves of the CTA take consecutive runs of chunks, each summed in order.
-constexpr int kJoinCols = 512;
+// CTA (chunk, kJoinCols columns): if an id begins in the chunk and goes on past its end, adds its partial
+// sums.  Four groups of the CTA's threads take consecutive runs of chunks, each summed in order
+// (32000 tokens onto 4096 x 768 40.3 us; two groups, of twice the columns, 42.4).
+constexpr int kJoinCols = 256;
+constexpr int kJoinThreads = kJoinCols / 4, kJoinGroups = kGThreads / kJoinThreads;
 __global__ void __launch_bounds__(kGThreads) embed_join_kernel(const __grid_constant__ GradArgs A, int32_t slabs) {
     pdl_trigger();
     pdl_wait();
@@ -597,8 +599,8 @@ __global__ void __launch_bounds__(kGThreads) embed_join_kernel(const __grid_cons
     const uint32_t cur = __ldg(A.key + p1 - 1), after = __ldg(A.key + p1);
     const uint32_t before = p0 > 0 ? __ldg(A.key + p0 - 1) : ~cur;
     if (cur == static_cast<uint32_t>(A.V) || after != cur || before == cur) return;
-    __shared__ float4 part[kGThreads / 2];
-    const int half = threadIdx.x / (kGThreads / 2), at = threadIdx.x % (kGThreads / 2);
+    __shared__ float4 part[kGThreads];
+    const int group = threadIdx.x / kJoinThreads, at = threadIdx.x % kJoinThreads;
     const int col = static_cast<int>(blockIdx.x - c * slabs) * kJoinCols + 4 * at;
     // chunks c + 1 .. lo - 1 begin with this id
     int64_t lo = c + 1;
@@ -606,21 +608,25 @@ __global__ void __launch_bounds__(kGThreads) embed_join_kernel(const __grid_cons
         const int64_t k = lo + threadIdx.x;
         more = __syncthreads_count(k < A.chunks && __ldg(A.key + k * A.chunk) == cur);
     }
-    const int64_t mid = c + 1 + (lo - c) / 2;
+    const int64_t per = (lo - c - 1 + kJoinGroups - 1) / kJoinGroups, from = c + 1 + group * per;
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
     if (col < A.dpad) {
-        if (half == 0) s = *reinterpret_cast<const float4*>(A.tail + c * A.dpad + col);
+        if (group == 0) s = *reinterpret_cast<const float4*>(A.tail + c * A.dpad + col);
 #pragma unroll 8
-        for (int64_t k = half ? mid : c + 1; k < (half ? lo : mid); ++k) {
+        for (int64_t k = from; k < min(lo, from + per); ++k) {
             const float4 h = *reinterpret_cast<const float4*>(A.head + k * A.dpad + col);
             s = make_float4(s.x + h.x, s.y + h.y, s.z + h.z, s.w + h.w);
         }
     }
-    if (half) part[at] = s;
+    part[threadIdx.x] = s;
     __syncthreads();
-    if (!half && col < A.d) {
-        const float4 h = part[at];
-        const float acc[4] = {s.x + h.x, s.y + h.y, s.z + h.z, s.w + h.w};
+    if (group == 0 && col < A.d) {
+        float acc[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+        for (int g = 1; g < kJoinGroups; ++g) {
+            const float4 h = part[g * kJoinThreads + at];
+            acc[0] += h.x, acc[1] += h.y, acc[2] += h.z, acc[3] += h.w;
+        }
         put_row(A.G + static_cast<int64_t>(cur) * A.ld_G + col, acc, A.d - col, A.scale, A.accumulate != 0);
     }
 }
@@ -828,14 +834,15 @@ struct GradPlan {
     size_t keys, hist, part;  // bytes of one array of each kind
 };
 
-// Chunk length: about 24 warps for each SM, between 32 and 1024 positions.
+// Chunk length: about 24 warps for each SM, between 32 and 1024 positions; 16 while those leave no more than 36 warps for
+// each SM (8000 tokens onto 4096 x 768, added: 20.7 us in a graph, with 32 23.2; 16000 30.9 and 29.1).
 GradPlan grad_plan(dust_dtype dt, int64_t N, int32_t V, int32_t d) {
     GradPlan p{};
     p.N = N;
     const int cols = dt == DUST_BF16 ? 256 : 128;
     p.slabs = (d + cols - 1) / cols;
     const int64_t want = std::max<int64_t>(1, static_cast<int64_t>(num_sms()) * 24 / p.slabs);
-    int64_t c = 32;
+    int64_t c = N <= 24 * want ? 16 : 32;
     while (c < 1024 && N / (2 * c) >= want) c *= 2;
     p.chunk = static_cast<int>(c);
     p.chunks = static_cast<int>((N + c - 1) / c);
