@@ -655,8 +655,9 @@ def dust_linear(x, W, bias=None, act: str = "none", residual=None, y=None, z=Non
     ld_res = _rows(residual, "residual", N, d_out, dev, y.dtype) if residual is not None else 0
     keep = z is not None and z is not False
     if z is True:
-        z = x.new_empty(N, d_out)
-    ld_z = _rows(z, "z", N, d_out, dev, bf) if keep else 0
+        z, ld_z = x.new_empty(N, d_out), d_out
+    else:
+        ld_z = _rows(z, "z", N, d_out, dev, bf) if keep else 0
     st = lib().dust_linear(x.data_ptr(), ld_x, W.data_ptr(), _ptr(bias), _act_code(act), _ptr(residual), ld_res,
                            DUST_BF16, N, d_in, d_out, y.data_ptr(), _dtypes()[y.dtype], ld_y,
                            z.data_ptr() if keep else None, ld_z, _raw_stream(dev))
@@ -693,18 +694,26 @@ def dust_linear_backward(dy, x, W, act: str = "none", z=None, dx=True, dW=True, 
     if accumulate and (dW is True or db is True):
         raise ValueError("accumulate adds to given dW and db tensors; pass them, or None to skip them")
     if dx is True:
-        dx = x.new_empty(N, d_in, dtype=dx_dtype)
+        dx, ld_dx = x.new_empty(N, d_in, dtype=dx_dtype), d_in  # x's type, bf16, by default
+        if dx.dtype not in _dtypes():
+            raise TypeError(f"dx_dtype must be bf16 or fp32, not {dx_dtype}")
+    elif dx is None or dx is False:
+        dx, ld_dx = None, 0
+    else:
+        if dx_dtype is not None and dx.dtype != dx_dtype:
+            raise TypeError(f"dx is {dx.dtype}, dx_dtype {dx_dtype}")
+        ld_dx = _rows(dx, "dx", N, d_in, dev)
     if dW is True:
         dW = x.new_empty(d_out, d_in, dtype=f32)
+    elif dW is None or dW is False:
+        dW = None
+    else:
+        _flat(dW, "dW", d_out * d_in, dev, f32)
     if db is True:
         db = x.new_empty(d_out, dtype=f32)
-    dx, dW, db = (None if t is False else t for t in (dx, dW, db))
-    if dx is not None and dx_dtype is not None and dx.dtype != dx_dtype:
-        raise TypeError(f"dx is {dx.dtype}, dx_dtype {dx_dtype}")
-    ld_dx = _rows(dx, "dx", N, d_in, dev) if dx is not None else 0
-    if dW is not None:
-        _flat(dW, "dW", d_out * d_in, dev, f32)
-    if db is not None:
+    elif db is None or db is False:
+        db = None
+    else:
         _flat(db, "db", d_out, dev, f32)
     at, nb, ws = _new_workspace(workspace, dust_workspace_size(DUST_OP_LINEAR_BACKWARD, DUST_BF16, N, d_in, d_out, 0), x)
     st = lib().dust_linear_backward(dy.data_ptr(), _dtypes()[dy.dtype], ld_dy, z.data_ptr() if code else None, ld_z,

@@ -1307,8 +1307,8 @@ dust_status gemm_rows(const void* a, int64_t ld_a, int terms, int K, const void*
 // the SMs, an item's blocks of 64 tokens and its epilogue (us, about as measured), and, with more than one
 // split, the partials written and read back at about 6 GB/ms and one more launch.  The partials are added in order.
 // (256 x 256 over 64 tokens 3.4 us, with 256 columns a tile 6.7; 1024 x 1024 over 5001 14.5 and 18.)
-constexpr int kMinBlocks = 4;
-constexpr int kMaxSplits = 64;
+constexpr uint32_t kMinBlocks = 4;
+constexpr uint32_t kMaxSplits = 64;
 struct DwPlan {
     int bn, m_tiles, n_tiles, k_blocks, splits, per_split;
 };
@@ -1316,7 +1316,9 @@ DwPlan dw_plan(int64_t N, int32_t d_in, int32_t d_out) {
     DwPlan p{};
     p.m_tiles = (d_out + kBM - 1) / kBM;
     p.k_blocks = static_cast<int>((N + kBK - 1) / kBK);
-    const double bytes = 8.0 * d_out * d_in;
+    const double join = 8.0 * d_out * d_in / 6e6;
+    const uint32_t blocks = static_cast<uint32_t>(p.k_blocks);  // at most 2^17
+    const int64_t sms = num_sms();
     struct Width {
         int bn;
         double block, epilogue;
@@ -1325,11 +1327,10 @@ DwPlan dw_plan(int64_t N, int32_t d_in, int32_t d_out) {
     for (const Width w : {Width{256, 0.45, 4.2}, Width{128, 0.32, 2.4}, Width{64, 0.26, 1.5}}) {
         const int n_tiles = (d_in + w.bn - 1) / w.bn;
         const int64_t tiles = static_cast<int64_t>(p.m_tiles) * n_tiles;
-        for (int64_t k = 1; k <= kMaxSplits && (k == 1 || p.k_blocks / k >= kMinBlocks); ++k) {
-            const double waves = static_cast<double>((tiles * k + num_sms() - 1) / num_sms());
-            const int64_t per = (p.k_blocks + k - 1) / k;
-            const double cost = waves * (w.block * static_cast<double>(per) + w.epilogue) +
-                                (k > 1 ? 3.0 + static_cast<double>(k) * bytes / 6e6 : 0.0);
+        for (uint32_t k = 1; k <= kMaxSplits && (k == 1 || k * kMinBlocks <= blocks); ++k) {
+            const uint32_t per = (blocks + k - 1) / k;
+            const double cost = static_cast<double>((tiles * k + sms - 1) / sms) * (w.block * per + w.epilogue) +
+                                (k > 1 ? 3.0 + k * join : 0.0);
             if (p.bn == 0 || cost < least) {
                 least = cost;
                 p.bn = w.bn;
