@@ -1123,8 +1123,20 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant_
         const int a = warp * per, b = min(A.chunks, a + per);
         float s = 0.f;
         if (c < A.d_out) {
+            int k = a;
+            for (; b - k > 8; k += 16) {
+                // sixteen loads on their way together (768 columns over 16384 tokens: the call takes 2 us less); a
+                // condition around each, or none of min, and they were made one after the other
+                float v[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    v[j] = __ldg(A.db_part + static_cast<int64_t>(min(k + j, b - 1)) * A.d_out + c);
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    if (k + j < b) s += v[j];
+            }
 #pragma unroll 4
-            for (int k = a; k < b; ++k) s += __ldg(A.db_part + static_cast<int64_t>(k) * A.d_out + c);
+            for (; k < b; ++k) s += __ldg(A.db_part + static_cast<int64_t>(k) * A.d_out + c);
         }
         sh[warp][lane] = s;
         __syncthreads();
