@@ -431,9 +431,24 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void*
 // Programmatic dependent launch: a kernel launched with dependent_launch (dust_internal.h) may start while the one
 // before it on the stream still runs; pdl_wait returns when that one has completed and its writes are
 // visible.  Every thread calls it before its first access to global memory that the one before may write.
-// pdl_trigger lets the next kernel start.
+// pdl_trigger lets the next kernel start.  A kernel so launched lives while others still write, so it reads global memory by
+// ordinary loads or the two below, never by __ldg or through const __restrict__ pointers: the read-only path is
+// specified for memory that nobody writes during the kernel's life, and its loads may be moved ahead of the wait.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// 16 bytes that are read once, and that the kernel itself does not write: kept short in the caches, or taken from L2 past L1 (for
+// kernels that read before their pdl_wait what a kernel further back has written).  As volatile as the wait, so they stay behind it.
+__device__ __forceinline__ uint4 load_once(const void* p) {
+    uint4 v;
+    asm volatile("ld.global.cs.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint4 load_l2(const void* p) {
+    uint4 v;
+    asm volatile("ld.global.cg.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
 
 // The barrier of a cluster's threads.
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }

@@ -43,19 +43,19 @@ __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 
 __device__ __forceinline__ V8 load8(const float* p, int n) {
     V8 r;
     if (n >= 8) {
-        const float4 a = __ldg(reinterpret_cast<const float4*>(p));
-        const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+        const float4 a = *reinterpret_cast<const float4*>(p);
+        const float4 b = reinterpret_cast<const float4*>(p)[1];
         r = V8{{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
     } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) r.v[j] = j < n ? __ldg(p + j) : 0.f;
+        for (int j = 0; j < 8; ++j) r.v[j] = j < n ? p[j] : 0.f;
     }
     return r;
 }
 __device__ __forceinline__ V8 load8(const __nv_bfloat16* p, int n) {
     V8 r;
     if (n >= 8) {
-        const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
+        const uint4 a = *reinterpret_cast<const uint4*>(p);
         r = V8{{bf_lo(a.x), bf_hi(a.x), bf_lo(a.y), bf_hi(a.y), bf_lo(a.z), bf_hi(a.z), bf_lo(a.w),
                 bf_hi(a.w)}};
     } else {
@@ -92,9 +92,8 @@ constexpr int kFThreads = 256;
 constexpr int kFItems = 2;  // items of eight elements a thread holds at once
 
 template <typename TE, typename TO>
-__global__ void __launch_bounds__(kFThreads) embedding_kernel(const int32_t* __restrict__ ids,
-                                                              const TE* __restrict__ E, int64_t ld_E,
-                                                              int64_t N, int32_t V, int32_t d, int32_t nv,
+__global__ void __launch_bounds__(kFThreads) embedding_kernel(const int32_t* ids, const TE* E,
+                                                              int64_t ld_E, int64_t N, int32_t V, int32_t d, int32_t nv,
                                                               uint64_t nv_magic, float scale, TO* out,
                                                               int64_t ld_out) {
     pdl_trigger();
@@ -111,7 +110,7 @@ __global__ void __launch_bounds__(kFThreads) embedding_kernel(const int32_t* __r
         if (f < total) {
             const int64_t t = div_by_magic(f, nv, nv_magic);
             const int c = 8 * static_cast<int>(f - t * nv);
-            const int32_t id = __ldg(ids + t);
+            const int32_t id = ids[t];
             left[j] = d - c;
             at[j] = t * ld_out + c;
             if (id >= 0 && id < V) {
@@ -149,9 +148,8 @@ __device__ __forceinline__ uint32_t key_of(int32_t id, int32_t V) {
 
 // Digit counts of each tile: hist[tile][bin].
 template <int kSRounds>
-__global__ void __launch_bounds__(kSThreads) embed_hist_kernel(const int32_t* __restrict__ ids,
-                                                               const uint32_t* __restrict__ keys, int64_t N,
-                                                               int32_t V, int shift, uint32_t mask,
+__global__ void __launch_bounds__(kSThreads) embed_hist_kernel(const int32_t* ids, const uint32_t* keys,
+                                                               int64_t N, int32_t V, int shift, uint32_t mask,
                                                                int32_t* hist) {
     __shared__ int32_t cnt[kBins];
     pdl_trigger();
@@ -240,8 +238,8 @@ __device__ __forceinline__ int32_t scan_bins(int32_t x, int32_t* sh) {
 // the order of the pass's digit.  Each CTA sums the other tiles' counts itself.
 template <int kSRounds>
 __global__ void __launch_bounds__(kSThreads) embed_scatter_kernel(
-    const int32_t* __restrict__ ids, const uint32_t* __restrict__ keys, const int32_t* __restrict__ idx,
-    int64_t N, int32_t V, int shift, uint32_t mask, const int32_t* __restrict__ hist, int tiles,
+    const int32_t* ids, const uint32_t* keys, const int32_t* idx,
+    int64_t N, int32_t V, int shift, uint32_t mask, const int32_t* hist, int tiles,
     uint32_t* keys_out, int32_t* idx_out) {
     __shared__ int32_t wh[kSWarps][kBins];
     __shared__ int32_t sh[32];
@@ -251,7 +249,7 @@ __global__ void __launch_bounds__(kSThreads) embed_scatter_kernel(
     const int tile = blockIdx.x;
 #pragma unroll 8
     for (int t = 0; t < tiles; ++t) {
-        const int32_t c = __ldg(hist + static_cast<int64_t>(t) * kBins + threadIdx.x);
+        const int32_t c = hist[static_cast<int64_t>(t) * kBins + threadIdx.x];
         all += c;
         if (t < tile) earlier += c;
     }
@@ -297,7 +295,7 @@ constexpr size_t cluster_smem() {
 }
 
 template <int kKeys>
-__global__ void __launch_bounds__(kCThreads) embed_sort_kernel(const int32_t* __restrict__ ids, int32_t N, int32_t V, int bits,
+__global__ void __launch_bounds__(kCThreads) embed_sort_kernel(const int32_t* ids, int32_t N, int32_t V, int bits,
                                                                int passes, uint32_t* keys_out, int32_t* idx_out) {
     extern __shared__ uint64_t csm[];
     constexpr int kTile = kCThreads * kKeys;
@@ -319,7 +317,7 @@ __global__ void __launch_bounds__(kCThreads) embed_sort_kernel(const int32_t* __
             item[r] = 0;
             if (at < n) {
                 const int32_t t = rank * kTile + at;
-                item[r] = pass == 0 ? static_cast<uint64_t>(key_of(__ldg(ids + t), V)) << 32 | static_cast<uint32_t>(t)
+                item[r] = pass == 0 ? static_cast<uint64_t>(key_of(ids[t], V)) << 32 | static_cast<uint32_t>(t)
                                     : list[(pass & 1) * kTile + at];
             }
             digit[r] = static_cast<int32_t>(static_cast<uint32_t>(item[r] >> 32) >> (pass * bits) & mask);
@@ -426,6 +424,9 @@ template <>
 struct Lane<float> {
     static constexpr int kN = 4;
     using Raw = float4;
+    static __device__ __forceinline__ Raw raw(const uint4& w) {
+        return make_float4(__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w));
+    }
     static __device__ __forceinline__ void add(float (&a)[4], const Raw& r) {
         a[0] += r.x;
         a[1] += r.y;
@@ -440,6 +441,7 @@ template <>
 struct Lane<__nv_bfloat16> {
     static constexpr int kN = 8;
     using Raw = uint4;
+    static __device__ __forceinline__ Raw raw(const uint4& w) { return w; }
     static __device__ __forceinline__ void add(float (&a)[8], const Raw& r) {
         const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
@@ -491,7 +493,7 @@ template <typename T>
 __device__ __forceinline__ void load_rows(typename Lane<T>::Raw (&raw)[8], const T* g, const int32_t (&t)[8], int64_t ld, int n) {
     if (n >= Lane<T>::kN) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) raw[j] = __ldcs(reinterpret_cast<const typename Lane<T>::Raw*>(g + t[j] * ld));
+        for (int j = 0; j < 8; ++j) raw[j] = Lane<T>::raw(load_once(g + t[j] * ld));
     } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j) raw[j] = n > 0 ? Lane<T>::tail(g + t[j] * ld, n) : typename Lane<T>::Raw{};
@@ -514,12 +516,12 @@ __global__ void __launch_bounds__(kGThreads) embed_grad_kernel(const __grid_cons
             int64_t lo = 0, hi = A.N;  // first position whose key is >= v
             while (lo < hi) {
                 const int64_t mid = (lo + hi) >> 1;
-                if (__ldg(A.key + mid) < v)
+                if (A.key[mid] < v)
                     lo = mid + 1;
                 else
                     hi = mid;
             }
-            absent[threadIdx.x] = r0 + threadIdx.x < A.V && (lo == A.N || __ldg(A.key + lo) != v);
+            absent[threadIdx.x] = r0 + threadIdx.x < A.V && (lo == A.N || A.key[lo] != v);
         }
         __syncthreads();
         for (int r = warp; r < kZeroRows; r += kGWarps) {
@@ -541,8 +543,8 @@ __global__ void __launch_bounds__(kGThreads) embed_grad_kernel(const __grid_cons
     const int n = A.d - col;  // columns left, this lane's own among them
     const int64_t p0 = c * A.chunk, p1 = min(A.N, p0 + A.chunk);
     const uint32_t none = static_cast<uint32_t>(A.V);
-    uint32_t cur = __ldg(A.key + p0);
-    bool began_before = p0 > 0 && __ldg(A.key + p0 - 1) == cur;
+    uint32_t cur = A.key[p0];
+    bool began_before = p0 > 0 && A.key[p0 - 1] == cur;
     const T* g = static_cast<const T*>(A.g) + col;
     float acc[kN] = {};
     for (int64_t q = p0; q < p1 && cur != none; q += 32) {
@@ -550,8 +552,8 @@ __global__ void __launch_bounds__(kGThreads) embed_grad_kernel(const __grid_cons
         uint32_t my_key = none;
         int32_t my_idx = 0;
         if (lane < cnt) {
-            my_key = __ldg(A.key + q + lane);
-            my_idx = __ldg(A.idx + q + lane);
+            my_key = A.key[q + lane];
+            my_idx = A.idx[q + lane];
         }
         for (int b = 0; b < cnt; b += 8) {
             typename Lane<T>::Raw raw[8];
@@ -581,7 +583,7 @@ __global__ void __launch_bounds__(kGThreads) embed_grad_kernel(const __grid_cons
         }
     }
     if (cur == none || n <= 0) return;
-    const bool goes_on = p1 < A.N && __ldg(A.key + p1) == cur;
+    const bool goes_on = p1 < A.N && A.key[p1] == cur;
     if (began_before)
         put_partial(A.head + c * A.dpad + col, acc);
     else if (goes_on)
@@ -601,8 +603,8 @@ __global__ void __launch_bounds__(kGThreads) embed_join_kernel(const __grid_cons
     const int64_t c = blockIdx.x / slabs;
     const int64_t p0 = c * A.chunk, p1 = p0 + A.chunk;
     if (p1 >= A.N) return;
-    const uint32_t cur = __ldg(A.key + p1 - 1), after = __ldg(A.key + p1);
-    const uint32_t before = p0 > 0 ? __ldg(A.key + p0 - 1) : ~cur;
+    const uint32_t cur = A.key[p1 - 1], after = A.key[p1];
+    const uint32_t before = p0 > 0 ? A.key[p0 - 1] : ~cur;
     if (cur == static_cast<uint32_t>(A.V) || after != cur || before == cur) return;
     __shared__ float4 part[kGThreads];
     const int group = threadIdx.x / kJoinThreads, at = threadIdx.x % kJoinThreads;
@@ -611,7 +613,7 @@ __global__ void __launch_bounds__(kGThreads) embed_join_kernel(const __grid_cons
     int64_t lo = c + 1;
     for (int more = kGThreads; more == kGThreads; lo += more) {
         const int64_t k = lo + threadIdx.x;
-        more = __syncthreads_count(k < A.chunks && __ldg(A.key + k * A.chunk) == cur);
+        more = __syncthreads_count(k < A.chunks && A.key[k * A.chunk] == cur);
     }
     const int64_t per = (lo - c - 1 + kJoinGroups - 1) / kJoinGroups, from = c + 1 + group * per;
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -670,7 +672,7 @@ __global__ void __launch_bounds__(kGThreads) embed_grad_small_kernel(const __gri
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int t = t0 + j * kGThreads + threadIdx.x;
-            id[j] = t < A.N ? __ldg(A.ids + t) : -1;
+            id[j] = t < A.N ? A.ids[t] : -1;
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {

@@ -191,11 +191,11 @@ __global__ void __launch_bounds__(kRThreads) linear_rows_kernel(const __grid_con
         for (int v = share * 32 + lane; v < nv; v += A.split * 32) {
             uint4 ww[kRRows];
 #pragma unroll
-            for (int r = 0; r < kRRows; ++r) ww[r] = __ldg(w[r] + v);
+            for (int r = 0; r < kRRows; ++r) ww[r] = w[r][v];
 #pragma unroll
             for (int t = 0; t < kTok; ++t) {
                 if (t >= A.N) break;
-                const uint4 xx = __ldg(reinterpret_cast<const uint4*>(A.x + t * A.ld_x) + v);
+                const uint4 xx = reinterpret_cast<const uint4*>(A.x + t * A.ld_x)[v];
                 const float xf[8] = {bf_lo(xx.x), bf_hi(xx.x), bf_lo(xx.y), bf_hi(xx.y),
                                      bf_lo(xx.z), bf_hi(xx.z), bf_lo(xx.w), bf_hi(xx.w)};
 #pragma unroll
@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(kRThreads) linear_rows_kernel(const __grid_con
         float a = 0.f;
         for (int k = 0; k < A.split; ++k) a += part[warp + k][e];
         const int o = o0 + r;
-        if (A.bias) a += __ldg(A.bias + o);
+        if (A.bias) a += A.bias[o];
         if (A.z) A.z[t * A.ld_z + o] = __float2bfloat16_rn(a);
         float v = act_any(A.act, a);
         if (A.out_bf16) {
@@ -735,7 +735,7 @@ __global__ void __launch_bounds__(kPromote ? kPromoteThreads : kThreads, 1) line
             void* y = static_cast<uint8_t*>(A.e.y) + split * A.split_elems * (A.e.out_bf16 ? 2 : 4);
             float4 bias = make_float4(0.f, 0.f, 0.f, 0.f);  // on its way before the wait for the tile
             if (!kBmn && A.e.bias && 4 * lane < kCols && o0 + 4 * lane < A.e.n_out)
-                bias = __ldg(reinterpret_cast<const float4*>(A.e.bias + o0) + lane);
+                bias = reinterpret_cast<const float4*>(A.e.bias + o0)[lane];
             Rows res;
             if (!kPromote && A.e.res)
                 rows_load(res, A.e.res, t0, A.e.M, A.e.ld_res * 2, static_cast<int64_t>(o0) * 2,
@@ -988,7 +988,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tokens_kernel(const __grid
         }
         const int64_t t = t0 + row;
         if (A.e.bias) {
-            const float4 b = __ldg(reinterpret_cast<const float4*>(A.e.bias + o));
+            const float4 b = *reinterpret_cast<const float4*>(A.e.bias + o);
             a = make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
         }
         if (A.e.z)
@@ -1046,47 +1046,62 @@ __global__ void __launch_bounds__(kDThreads) linear_dz_kernel(const __grid_const
     const int64_t r0 = static_cast<int64_t>(blockIdx.y) * A.rows;
     const int64_t r1 = min(A.N, r0 + A.rows);
     float s[8] = {};
+    constexpr int kRaw = sizeof(T) / 2;  // 16-byte pieces of eight elements of dy
+    struct Row {
+        uint4 dy[kRaw], z;
+    };
+    auto load = [&](Row& r, int64_t t) {
+        const T* p = static_cast<const T*>(A.dy) + t * A.ld_dy + col;
+#pragma unroll
+        for (int j = 0; j < kRaw; ++j) r.dy[j] = load_l2(p + 8 / kRaw * j);
+        if (kAct != DUST_ACT_NONE) r.z = load_l2(A.z + t * A.ld_z + col);
+    };
+    auto take = [&](const Row& r, int64_t t) {
+        float g[8];
+        if (sizeof(T) == 2) {
+            const uint32_t ww[4] = {r.dy[0].x, r.dy[0].y, r.dy[0].z, r.dy[0].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                g[2 * j] = bf_lo(ww[j]);
+                g[2 * j + 1] = bf_hi(ww[j]);
+            }
+        } else {
+            const uint4 a = r.dy[0], b = r.dy[kRaw - 1];
+            const uint32_t ww[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+            for (int j = 0; j < 8; ++j) g[j] = __uint_as_float(ww[j]);
+        }
+        if (kAct != DUST_ACT_NONE) {
+            const uint32_t ww[4] = {r.z.x, r.z.y, r.z.z, r.z.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                g[2 * j] *= act_slope<kAct>(bf_lo(ww[j]));
+                g[2 * j + 1] *= act_slope<kAct>(bf_hi(ww[j]));
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[j] += g[j];
+        if (A.hi) {
+            uint32_t h[4], l[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                h[j] = pack2(g[2 * j], g[2 * j + 1]);
+                // the remainder is exact in fp32
+                l[j] = pack2(g[2 * j] - bf_lo(h[j]), g[2 * j + 1] - bf_hi(h[j]));
+            }
+            const int64_t at = t * A.d_out + col;
+            *reinterpret_cast<uint4*>(A.hi + at) = make_uint4(h[0], h[1], h[2], h[3]);
+            if (A.lo) *reinterpret_cast<uint4*>(A.lo + at) = make_uint4(l[0], l[1], l[2], l[3]);
+        }
+    };
     if (col < A.d_out) {
-#pragma unroll 2
-        for (int64_t t = r0 + warp; t < r1; t += kDWarps) {
-            float g[8];
-            if (sizeof(T) == 2) {
-                const uint4 w = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(A.dy) + t * A.ld_dy + col));
-                const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    g[2 * j] = bf_lo(ww[j]);
-                    g[2 * j + 1] = bf_hi(ww[j]);
-                }
-            } else {
-                const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(A.dy) + t * A.ld_dy + col);
-                const float4 a = __ldg(p), b = __ldg(p + 1);
-                g[0] = a.x, g[1] = a.y, g[2] = a.z, g[3] = a.w;
-                g[4] = b.x, g[5] = b.y, g[6] = b.z, g[7] = b.w;
-            }
-            if (kAct != DUST_ACT_NONE) {
-                const uint4 w = __ldg(reinterpret_cast<const uint4*>(A.z + t * A.ld_z + col));
-                const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    g[2 * j] *= act_slope<kAct>(bf_lo(ww[j]));
-                    g[2 * j + 1] *= act_slope<kAct>(bf_hi(ww[j]));
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) s[j] += g[j];
-            if (A.hi) {
-                uint32_t h[4], l[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    h[j] = pack2(g[2 * j], g[2 * j + 1]);
-                    // the remainder is exact in fp32
-                    l[j] = pack2(g[2 * j] - bf_lo(h[j]), g[2 * j + 1] - bf_hi(h[j]));
-                }
-                const int64_t at = t * A.d_out + col;
-                *reinterpret_cast<uint4*>(A.hi + at) = make_uint4(h[0], h[1], h[2], h[3]);
-                if (A.lo) *reinterpret_cast<uint4*>(A.lo + at) = make_uint4(l[0], l[1], l[2], l[3]);
-            }
+        for (int64_t t = r0 + warp; t < r1; t += 2 * kDWarps) {  // two rows on their way together
+            const bool two = t + kDWarps < r1;
+            Row a, b;
+            load(a, t);
+            load(b, two ? t + kDWarps : t);
+            take(a, t);
+            if (two) take(b, t + kDWarps);
         }
     }
     if (!A.part) return;  // never late
@@ -1130,13 +1145,13 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant_
                 float v[16];
 #pragma unroll
                 for (int j = 0; j < 16; ++j)
-                    v[j] = __ldg(A.db_part + static_cast<int64_t>(min(k + j, b - 1)) * A.d_out + c);
+                    v[j] = A.db_part[static_cast<int64_t>(min(k + j, b - 1)) * A.d_out + c];
 #pragma unroll
                 for (int j = 0; j < 16; ++j)
                     if (k + j < b) s += v[j];
             }
 #pragma unroll 4
-            for (; k < b; ++k) s += __ldg(A.db_part + static_cast<int64_t>(k) * A.d_out + c);
+            for (; k < b; ++k) s += A.db_part[static_cast<int64_t>(k) * A.d_out + c];
         }
         sh[warp][lane] = s;
         __syncthreads();
@@ -1151,7 +1166,7 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant_
         float4 s = A.accumulate ? A.dW[i] : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
         for (int k = 0; k < A.splits; ++k) {
-            const float4 v = __ldcs(A.dw_part + static_cast<int64_t>(k) * A.n4 + i);
+            const float4 v = A.dw_part[static_cast<int64_t>(k) * A.n4 + i];
             s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
         }
         A.dW[i] = s;
