@@ -152,8 +152,10 @@ dust_status dust_linear(const void* x, int64_t ld_x, const void* W, const float*
  * fp32 [d_out, d_in]; db: fp32 [d_out]; each NULL to skip, not all three.  accumulate != 0 adds to
  * dW and db (dx is always overwritten).
  * dz enters the tensor cores as g_terms bf16 terms (as g in dust_weight_grad) in dW and in an fp32
- * dx; a bf16 dx takes one term.  A bf16 dy without an activation is exact in one.  No output
- * may overlap an input or another output.  N <= 8388607.
+ * dx; a bf16 dx takes one term (an fp32 dx is there for callers that need more).  A bf16 dy without an
+ * activation is exact in one.  An infinite dz gives what the formula gives; an infinite x (in dW) or W (in an
+ * fp32 dx) against two terms gives NaN where the formula may have an infinity.  No output may overlap an
+ * input or another output.  N <= 8388607.
  * workspace: dust_workspace_size(DUST_OP_LINEAR_BACKWARD, DUST_BF16, N, d_in, d_out, 0) bytes.
  * Deterministic.
  */

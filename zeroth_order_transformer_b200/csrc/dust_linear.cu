@@ -19,7 +19,7 @@
 //                         tokens its columns, the contraction cut over the CTAs of a cluster and
 //                         joined through distributed shared memory (24 tokens 8192 -> 8192 26 us, 5.2 TB/s).
 // dz is formed once (linear_dz_kernel) as a bf16 operand, or as hi + lo bf16 terms (dz = hi + lo to
-// about 16 bits), with the column sums for db on the way.
+// about 16 bits; lo = 0 where hi is infinite), with the column sums for db on the way.
 #include <algorithm>
 
 #include "dust_device.cuh"
@@ -1086,8 +1086,9 @@ __global__ void __launch_bounds__(kDThreads) linear_dz_kernel(const __grid_const
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 h[j] = pack2(g[2 * j], g[2 * j + 1]);
-                // the remainder is exact in fp32
-                l[j] = pack2(g[2 * j] - bf_lo(h[j]), g[2 * j + 1] - bf_hi(h[j]));
+                // the remainder is exact in fp32; an infinite value has none
+                const float r0 = g[2 * j] - bf_lo(h[j]), r1 = g[2 * j + 1] - bf_hi(h[j]);
+                l[j] = pack2(fabsf(bf_lo(h[j])) == INFINITY ? 0.f : r0, fabsf(bf_hi(h[j])) == INFINITY ? 0.f : r1);
             }
             const int64_t at = t * A.d_out + col;
             *reinterpret_cast<uint4*>(A.hi + at) = make_uint4(h[0], h[1], h[2], h[3]);
