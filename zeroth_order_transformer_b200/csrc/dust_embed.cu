@@ -414,7 +414,7 @@ struct GradArgs {
     float* head;  // [chunks, dpad]: sums of ids that began in an earlier chunk
     float* tail;  // [chunks, dpad]: sums of ids that begin in the chunk and go on past its end
     int64_t ld_g, ld_G, N, units;
-    int32_t V, d, dpad, slabs, chunk, chunks, zero_blocks, accumulate;
+    int32_t V, d, dpad, slabs, chunk, chunks, accumulate;
     float scale;
 };
 
@@ -963,8 +963,8 @@ dust_status embedding_grad_launch(const int32_t* ids, const void* g, dust_dtype 
     A.units = static_cast<int64_t>(p.chunks) * p.slabs;
     A.accumulate = accumulate;
     A.scale = scale;
-    A.zero_blocks = accumulate ? 0 : (V + kZeroRows - 1) / kZeroRows;
-    const int64_t blocks = (A.units + kGWarps - 1) / kGWarps + A.zero_blocks;
+    const int64_t zero_blocks = accumulate ? 0 : (static_cast<int64_t>(V) + kZeroRows - 1) / kZeroRows;
+    const int64_t blocks = (A.units + kGWarps - 1) / kGWarps + zero_blocks;
     const int join_slabs = (d + kJoinCols - 1) / kJoinCols;
     if (blocks > 2147483647LL || static_cast<int64_t>(p.chunks) * join_slabs > 2147483647LL)
         return DUST_ERR_UNSUPPORTED;
