@@ -117,7 +117,7 @@ dust_status dust_noisy_linear_output(const void* x, const void* W, dust_dtype dt
  * The linear layer itself with its epilogue: the clean forward of a block's layer, and the
  * recomputation of the layers behind a perturbed one.
  *   z_t = W x_t + bias,   y_t = act(z_t) + residual_t
- * x: bf16 [N, ld_x], W: bf16 [d_out, d_in] (d_in, d_out multiples of 16); bias: fp32 [d_out] or
+ * x: bf16 [N, ld_x], W: bf16 [d_out, d_in] (d_in, d_out multiples of 16 up to 2^31 - 1024); bias: fp32 [d_out] or
  * NULL; residual: [N, ld_res] of type out_dt or NULL; y: [N, ld_y] of type out_dt (fp32 or bf16);
  * z: optional bf16 [N, ld_z], the pre-activation for dust_linear_backward (NULL to skip).
  * Row strides (elements) at least the row and a multiple of 16 bytes; all pointers 16-byte
@@ -167,8 +167,8 @@ dust_status dust_linear_backward(const void* dy, dust_dtype dy_dt, int64_t ld_dy
 
 /*
  * Token embedding: out_t = scale E[ids_t].  ids: DEVICE int32 [N]; E: [V, ld_E] of type dt, out:
- * [N, ld_out] of type out_dt, both with d valid columns (any d >= 1; columns behind d are not
- * written).  A negative id is padding and gives a zero row; an id >= V gives a NaN row (as an
+ * [N, ld_out] of type out_dt, both with d valid columns (any d from 1 to 2^31 - 1024; columns behind d are
+ * not written).  A negative id is padding and gives a zero row; an id >= V gives a NaN row (as an
  * invalid target does in dust_noisy_logits_ce).  Row strides at least d and a multiple of 16 bytes.
  */
 dust_status dust_embedding(const int32_t* ids, const void* E, dust_dtype dt, int64_t ld_E, int64_t N, int32_t V,
@@ -183,7 +183,7 @@ dust_status dust_embedding(const int32_t* ids, const void* E, dust_dtype dt, int
  * [V, ld_G].  accumulate == 0 overwrites all V rows (rows without tokens with zeros), accumulate != 0
  * adds to the rows that have tokens and leaves the others (for a table shared with the output layer).
  * Tokens whose id is outside [0, V) add nothing.  Sums in fp32, in token order within runs of sorted
- * tokens: deterministic.  N <= 2^26, V < 2^31 - 1.
+ * tokens: deterministic.  N <= 2^26, V < 2^31 - 1, d <= 2^31 - 1024.
  * workspace: dust_workspace_size(DUST_OP_EMBEDDING_GRAD, dt, N, V, d, 0) bytes (0 for up to
  * DUST_EMBEDDING_SMALL tokens).
  */

@@ -265,6 +265,9 @@ bool valid_ld(int64_t ld, int64_t cols, int64_t vec) {
     return ld >= cols && ld % vec == 0 && ld < (1LL << 38);
 }
 
+// The widest layer or table row of the calls around the estimator: counts of tiles and columns stay within 32 bits.
+constexpr int32_t kWidest = 2147483647 - 1023;
+
 // Whether an output begins where one of the other buffers does (rows of several matrices may lie between one another,
 // so that ranges that meet are not a mistake).
 bool same_start(const void* out, std::initializer_list<const void*> others) {
@@ -400,7 +403,8 @@ dust_status dust_linear(const void* x, int64_t ld_x, const void* W, const float*
     if (!valid_ld(ld_x, d_in, 8) || !valid_ld(ld_y, d_out, out_vec) ||
         (residual && !valid_ld(ld_res, d_out, out_vec)) || (z && !valid_ld(ld_z, d_out, 8)))
         return DUST_ERR_INVALID_ARG;
-    if (dt != DUST_BF16 || d_in % 16 != 0 || d_out % 16 != 0 || N > 1073741823LL) return DUST_ERR_UNSUPPORTED;
+    if (dt != DUST_BF16 || d_in % 16 != 0 || d_out % 16 != 0 || N > 1073741823LL || d_in > kWidest || d_out > kWidest)
+        return DUST_ERR_UNSUPPORTED;
     if (same_start(y, {x, W, bias}) || same_start(z, {x, W, bias, residual, y}) || (residual == y && ld_res != ld_y))
         return DUST_ERR_INVALID_ARG;
     return linear_launch(x, ld_x, W, bias, act, residual, ld_res, N, d_in, d_out, y, out_dt == DUST_BF16 ? 1 : 0,
@@ -422,7 +426,8 @@ dust_status dust_linear_backward(const void* dy, dust_dtype dy_dt, int64_t ld_dy
     if (!valid_ld(ld_dy, d_out, dy_dt == DUST_BF16 ? 8 : 4) || (act != DUST_ACT_NONE && !valid_ld(ld_z, d_out, 8)) ||
         (dW && !valid_ld(ld_x, d_in, 8)) || (dx && !valid_ld(ld_dx, d_in, dx_dt == DUST_BF16 ? 8 : 4)))
         return DUST_ERR_INVALID_ARG;
-    if (dt != DUST_BF16 || d_in % 16 != 0 || d_out % 16 != 0 || N > 8388607LL) return DUST_ERR_UNSUPPORTED;
+    if (dt != DUST_BF16 || d_in % 16 != 0 || d_out % 16 != 0 || N > 8388607LL || d_in > kWidest || d_out > kWidest)
+        return DUST_ERR_UNSUPPORTED;
     const dust_status st = check_ws(workspace, ws_bytes, linear_backward_workspace_bytes(N, d_in, d_out));
     if (st != DUST_OK) return st;
     if (same_start(dx, {dy, z, x, W}) || same_start(dW, {dy, z, x, W, dx}) || same_start(db, {dy, z, x, W, dx, dW}))
@@ -439,7 +444,7 @@ dust_status dust_embedding(const int32_t* ids, const void* E, dust_dtype dt, int
     if ((reinterpret_cast<uintptr_t>(ids) & 3u) || !aligned16(E) || !aligned16(out) ||
         !valid_ld(ld_E, d, dt == DUST_BF16 ? 8 : 4) || !valid_ld(ld_out, d, out_dt == DUST_BF16 ? 8 : 4))
         return DUST_ERR_INVALID_ARG;
-    if (N > 2147483647LL) return DUST_ERR_UNSUPPORTED;
+    if (N > 2147483647LL || d > kWidest) return DUST_ERR_UNSUPPORTED;
     if (same_start(out, {ids, E})) return DUST_ERR_INVALID_ARG;
     return embedding_launch(ids, E, dt, ld_E, N, V, d, scale, out, out_dt, ld_out,
                             static_cast<cudaStream_t>(stream));
@@ -453,7 +458,7 @@ dust_status dust_embedding_grad(const int32_t* ids, const void* g, dust_dtype dt
         !valid_ld(ld_g, d, dt == DUST_BF16 ? 8 : 4) || !valid_ld(ld_G, d, 4))
         return DUST_ERR_INVALID_ARG;
     // each tile of the sort reads the counts of all tiles: beyond 2^26 tokens that would take over
-    if (N > (1LL << 26) || V > 2147483646) return DUST_ERR_UNSUPPORTED;
+    if (N > (1LL << 26) || V > 2147483646 || d > kWidest) return DUST_ERR_UNSUPPORTED;
     const dust_status st = check_ws(workspace, ws_bytes, embedding_grad_workspace_bytes(dt, N, V, d));
     if (st != DUST_OK) return st;
     if (same_start(G, {ids, g})) return DUST_ERR_INVALID_ARG;
