@@ -383,7 +383,8 @@ dust_status dust_optimizer_step(const dust_opt_params* opt, const float* G, floa
  * scales are the initial state.  Codes are rounded to nearest even from the step's fp32
  * moments; the weights use the unrounded ones.
  * tensors: HOST array of descriptors; the pointers inside are DEVICE pointers, all 16-byte
- *   aligned, and no tensor may overlap another (or be listed twice).  n = 0 tensors are skipped.
+ *   aligned, and no buffer that is written may overlap another or a G, or be listed twice (tensors may
+ *   share a G).  n = 0 tensors are skipped.
  * g_dt: type of every G.  g_scale: optional DEVICE fp32 scalar that multiplies every G (a batch
  *   normalisation or clipping factor computed on the device); NULL is 1.
  * step: optional DEVICE int32 scalar with Adam's step count t, read by the kernels (values

@@ -17,6 +17,7 @@ and around the estimator, for the rest of a training step:
 """
 from __future__ import annotations
 
+import bisect
 import ctypes
 import os
 from typing import NamedTuple, Optional, Tuple
@@ -838,9 +839,9 @@ class DustOptimizer:
         self.m_scale = take(m_scale, "m_scale", f32, blocks, zeros=True) if bits == 8 else None
         self.v_scale = take(v_scale, "v_scale", f32, blocks, zeros=True) if bits == 8 else None
         held = [t for ts in (self.W, self.W_bf16, self.m, self.v, self.m_scale, self.v_scale) if ts is not None
-                for t in ts if t is not None and t.numel()]
-        spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in held)
-        if any(b[0] < a[1] for a, b in zip(spans, spans[1:])):
+                for t in ts if t is not None]
+        self._written = self._spans(held)
+        if any(b[0] < a[1] for a, b in zip(self._written, self._written[1:])):
             raise ValueError("weights and moments must not share memory")
         self._desc = (dust_opt_tensor * k)()
         for i, d in enumerate(self._desc):
@@ -852,8 +853,14 @@ class DustOptimizer:
             d.decay_scale = 1.0 if decay is None else float(decay[i])
         self.set_gradients(G)
 
+    @staticmethod
+    def _spans(tensors):
+        """(first byte, byte behind the last) of each tensor that has elements, by address."""
+        return sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in tensors if t.numel())
+
     def set_gradients(self, G) -> None:
-        """Takes other gradient tensors for the steps that follow."""
+        """Takes other gradient tensors for the steps that follow.  They may share memory with one another, not with
+        the weights and moments."""
         torch = _torch()
         G = list(G)
         if len(G) != len(self.W):
@@ -863,6 +870,12 @@ class DustOptimizer:
             raise TypeError(f"gradients are fp32 or bf16, not {dtype}")
         for i, (g, w) in enumerate(zip(G, self.W)):
             _flat(g, f"G[{i}]", w.numel(), self._index, dtype)
+        # by address, the last span that begins before a gradient's end is the one that can reach into it
+        begins = [a for a, _ in self._written]
+        for a, b in self._spans(G):
+            at = bisect.bisect_left(begins, b) - 1
+            if at >= 0 and self._written[at][1] > a:
+                raise ValueError("gradients must not share memory with weights or moments")
         self.G, self._g_dt = G, DUST_F32 if dtype == torch.float32 else DUST_BF16
         for d, g in zip(self._desc, G):
             d.G = g.data_ptr()
