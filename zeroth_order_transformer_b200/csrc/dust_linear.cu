@@ -1246,6 +1246,24 @@ dust_status launch_tokens(const GemmArgs& A, cudaStream_t s) {
                : DUST_ERR_CUDA;
 }
 
+// What a launch is called in the profile: the product and its form.
+const char* form_name(const char* const (&names)[4], int bn, bool pair) {
+    return names[pair ? 3 : bn == 256 ? 2 : bn == 128 ? 1 : 0];
+}
+const char* token_form_name(const char* const (&names)[4], int tok) {
+    return names[tok == 16 ? 0 : tok == 32 ? 1 : tok == 64 ? 2 : 3];
+}
+constexpr const char* kForward[4] = {"linear_tcgen05_64", "linear_tcgen05_128", "linear_tcgen05_256", "linear_tcgen05_256_pair"};
+constexpr const char* kDx[4] = {"linear_dx_tcgen05_64", "linear_dx_tcgen05_128", "linear_dx_tcgen05_256",
+                                "linear_dx_tcgen05_256_pair"};
+constexpr const char* kDw[3] = {"linear_dw_tcgen05_64", "linear_dw_tcgen05_128", "linear_dw_tcgen05_256"};
+constexpr const char* kDw2[3] = {"linear_dw_tcgen05_64_two_terms", "linear_dw_tcgen05_128_two_terms",
+                                 "linear_dw_tcgen05_256_two_terms"};
+constexpr const char* kTokens[4] = {"linear_tokens_tcgen05_16", "linear_tokens_tcgen05_32", "linear_tokens_tcgen05_64",
+                                    "linear_tokens_tcgen05_128"};
+constexpr const char* kDxTokens[4] = {"linear_dx_tokens_tcgen05_16", "linear_dx_tokens_tcgen05_32",
+                                      "linear_dx_tokens_tcgen05_64", "linear_dx_tokens_tcgen05_128"};
+
 // How many CTAs share a tile's contraction in linear_tokens_kernel.  Clusters of four fit on the SMs about 33 at
 // a time (36 of them took two waves: 768 -> 2304 over 256 tokens 15.3 us, with clusters of two 10.3).
 int token_ranks(int64_t tiles, int k_blocks) {
@@ -1266,7 +1284,7 @@ bool tokens_form(int64_t N, int n_out, int K) {
 }
 
 // y [N, n_out] = x W^T, or with w_mn x W (W [K, n_out]).
-dust_status gemm_tokens(const void* x, int64_t ld_x, int K, const void* W, bool w_mn, GemmArgs& G, const char* name,
+dust_status gemm_tokens(const void* x, int64_t ld_x, int K, const void* W, bool w_mn, GemmArgs& G,
                         cudaStream_t s) {
     const int64_t N = G.e.M;
     const int n_out = G.e.n_out;
@@ -1293,13 +1311,13 @@ dust_status gemm_tokens(const void* x, int64_t ld_x, int K, const void* W, bool 
              : tok == 32 ? launch_tokens<32, false>(G, s)
              : tok == 64 ? launch_tokens<64, false>(G, s)
                          : launch_tokens<128, false>(G, s);
-    prof_end(s, name);
+    prof_end(s, token_form_name(w_mn ? kDxTokens : kTokens, tok));
     return st;
 }
 
 // y [M, n_out] = A [terms M, K] B with the epilogue of G.e; B K-major [n_out, K] or MN-major [K, n_out].
 dust_status gemm_rows(const void* a, int64_t ld_a, int terms, int K, const void* b, bool b_mn, GemmArgs& G,
-                      const char* name, cudaStream_t s) {
+                      cudaStream_t s) {
     const int64_t M = G.e.M;
     const int n_out = G.e.n_out;
     const int64_t m_tiles = (M + kBM - 1) / kBM;
@@ -1326,7 +1344,7 @@ dust_status gemm_rows(const void* a, int64_t ld_a, int terms, int K, const void*
                           : launch_width<true, 1, true>(bn, pair, G, s);
     else
         st = G.e.out_bf16 ? launch_width<false, 1, false>(bn, pair, G, s) : launch_width<false, 1, true>(bn, pair, G, s);
-    prof_end(s, name);
+    prof_end(s, form_name(b_mn ? kDx : kForward, bn, pair));
     return st;
 }
 
@@ -1405,7 +1423,7 @@ dust_status gemm_dw(const void* dz, int64_t ld_dz, int terms, const void* x, int
         return DUST_ERR_CUDA;
     prof_begin(s);
     const dust_status st = terms == 2 ? launch_dw<2>(p.bn, G, s) : launch_dw<1>(p.bn, G, s);
-    prof_end(s, "linear_dw_tcgen05");
+    prof_end(s, (terms == 2 ? kDw2 : kDw)[p.bn == 256 ? 2 : p.bn == 128 ? 1 : 0]);
     if (p.splits > 1) {
         join.dw_part = reinterpret_cast<const float4*>(part);
         join.dW = reinterpret_cast<float4*>(dW);
@@ -1461,8 +1479,8 @@ dust_status linear_launch(const void* x, int64_t ld_x, const void* W, const floa
     GemmArgs G{};
     G.e = Epilogue{bias, res, y, static_cast<__nv_bfloat16*>(z), N, ld_res, ld_y, ld_z, d_out, act, out_bf16};
     const dust_status st = tokens_form(N, d_out, d_in)
-                               ? gemm_tokens(x, ld_x, d_in, W, false, G, "linear_tokens_tcgen05", s)
-                               : gemm_rows(x, ld_x, 1, d_in, W, false, G, "linear_tcgen05", s);
+                               ? gemm_tokens(x, ld_x, d_in, W, false, G, s)
+                               : gemm_rows(x, ld_x, 1, d_in, W, false, G, s);
     if (st != DUST_OK) return st;
     return cudaGetLastError() == cudaSuccess ? DUST_OK : DUST_ERR_CUDA;
 }
@@ -1519,8 +1537,8 @@ dust_status linear_backward_launch(const void* dy, int dy_bf16, int64_t ld_dy, c
         // a bf16 dx is rounded as coarsely as one term of dz; an fp32 dx takes both terms
         const int dx_terms = dx_bf16 ? 1 : terms;
         const dust_status st = dx_terms == 1 && tokens_form(N, d_in, d_out)
-                                   ? gemm_tokens(op, ld_op, d_out, W, true, G, "linear_dx_tokens_tcgen05", s)
-                                   : gemm_rows(op, ld_op, dx_terms, d_out, W, true, G, "linear_dx_tcgen05", s);
+                                   ? gemm_tokens(op, ld_op, d_out, W, true, G, s)
+                                   : gemm_rows(op, ld_op, dx_terms, d_out, W, true, G, s);
         if (st != DUST_OK) return st;
     }
     if (db && (direct || !products) && !sweep(dx != nullptr)) return DUST_ERR_CUDA;
