@@ -122,7 +122,8 @@ dust_status dust_noisy_linear_output(const void* x, const void* W, dust_dtype dt
  * z: optional bf16 [N, ld_z], the pre-activation for dust_linear_backward (NULL to skip).
  * Row strides (elements) at least the row and a multiple of 16 bytes; all pointers 16-byte
  * aligned.  y may be the residual's buffer (with the same stride); other overlaps are not allowed.
- * Sums in fp32; each output is rounded once.  Rows behind N and columns behind d_out are not
+ * Sums in fp32, handed over every 512 products for fp32 outputs and beyond d_in = 16384 (the tensor cores
+ * truncate as they add: up to 6e-9 of the sum for each product in between); each output is rounded once.  Rows behind N and columns behind d_out are not
  * written.  One and two tokens stream W through the CUDA cores, more go to the tensor cores, in forms
  * chosen by the sizes, so the last bits of a token's sums can depend on how many tokens the call has.
  * Deterministic.

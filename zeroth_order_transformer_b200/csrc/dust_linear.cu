@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(kRThreads) linear_rows_kernel(const __grid_con
 constexpr int kBM = 128;
 constexpr int kBK = 64;
 constexpr int kThreads = 320;  // TMA warp, MMA warp, eight epilogue warps
-// An fp32 output's kernel holds up to 128 sums a thread, and with the shared memory all taken a spilled
+// A kernel that collects its sums holds up to 128 of them a thread, and with the shared memory all taken a spilled
 // register goes to L2 (64 -> 2304 over 8192 tokens 39 us, of which a third waited for spills).  It launches three
 // warpgroups of 168 registers: the first (TMA, MMA, two idle warps) gives up 112 a thread, the two of
 // the epilogue take 56 more each: 128 x 56 + 256 x 224 = 384 x 168.
@@ -263,11 +263,16 @@ constexpr uint32_t kBox = kBK * 128;          // a 64-row x 64-element box of an
 // Each epilogue warp: 32 rows x 64 bytes of y and of z, and the biases of 32 columns.
 constexpr uint32_t kWarpStaging = 2 * 2048;
 constexpr uint32_t kStaging = 8 * (kWarpStaging + 128);
-// The tensor cores truncate as they add to the accumulator: a sum of K products is off by about K 1.1e-9 of
-// its size toward zero (measured: 4.7e-7 at K = 512, 9.1e-6 at K = 8192).  An fp32 output is therefore collected
-// in registers, rounded to nearest, after every 8 blocks (512 products) in the accumulator; a bf16 output's own
-// rounding is 200 times the largest error of K = 8192, and it is not.
+// The tensor cores truncate as they add to the accumulator: a sum of K products is off toward zero by about K 1.1e-9 of
+// its size where the products' signs are mixed (measured: 4.7e-7 at K = 512, 9.1e-6 at K = 8192), by up to K 6e-9
+// where all have one (3.3e-5 at K = 8192, 7.8e-4 at 131072).  An fp32 output is therefore collected in registers,
+// rounded to nearest, after every 8 blocks (512 products) in the accumulator.  A bf16 output is so from K > 16384 on: up to
+// there its own rounding (2^-9 of its size on average) is 20 times the largest of these errors, and the chain is
+// faster (8192 tokens, 16384 -> 4096: 712 us, collected 746).
 constexpr int kFlush = 8;
+constexpr int kLongest = 256;  // blocks of one chain into a bf16 output
+// How a tile's sums leave: straight from the accumulator (bf16), or collected in registers, into fp32 or bf16.
+enum Sums { kChain = 0, kToF32 = 1, kToBf16 = 2 };
 
 template <int kBN, int kTerms, bool kPair>
 struct Shape {
@@ -639,10 +644,11 @@ __device__ __forceinline__ void tile_of(int tile, int m_tiles, int n_tiles, int&
 }
 
 // Persistent: one CTA per SM walks (tile, split) items; each accumulator (two of them) is read by the
-// epilogue warps while the MMAs fill the other.  kPromote: see kFlush.
-template <int kBN, bool kAmn, bool kBmn, int kTerms, bool kPromote, bool kPair>
-__global__ void __launch_bounds__(kPromote ? kPromoteThreads : kThreads, 1) linear_gemm_kernel(const __grid_constant__ GemmArgs A) {
+// epilogue warps while the MMAs fill the other.  kSums: see kFlush.
+template <int kBN, bool kAmn, bool kBmn, int kTerms, int kSums, bool kPair>
+__global__ void __launch_bounds__(kSums != kChain ? kPromoteThreads : kThreads, 1) linear_gemm_kernel(const __grid_constant__ GemmArgs A) {
     using S = Shape<kBN, kTerms, kPair>;
+    constexpr bool kPromote = kSums != kChain;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
@@ -764,7 +770,21 @@ __global__ void __launch_bounds__(kPromote ? kPromoteThreads : kThreads, 1) line
                     release(buf);
                 }
                 if (!ok) break;
-                if (kBmn) {
+                if (kSums == kToBf16) {
+                    if (A.e.res)
+                        rows_load(res, A.e.res, t0, A.e.M, A.e.ld_res * 2, static_cast<int64_t>(o0) * 2,
+                                  static_cast<int64_t>(min(A.e.n_out, o0 + kCols)) * 2, lane);
+                    // a copy of the epilogue for each chunk, in its own registers: picked by predicates, 32 at a time
+                    // beside 128 sums spill into the loop over the blocks (8192 tokens, 16384 -> 4096: 872 us, so 746)
+#pragma unroll
+                    for (int c = 0; c < kCols / 32; ++c) {
+                        if (o0 + c * 32 >= A.e.n_out) break;  // uniform over the warp
+                        float v[32];
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] = acc[c * 32 + j];
+                        finish<32, !kBmn>(A.e, y, v, t0, o0 + c * 32, o0 + kCols, sy, sz, sb, bias, res, c, lane);
+                    }
+                } else if (kBmn) {
                     // dW and dx: no more than the sums, added to what is there if A.e.res says so
                     plain_out<kCols>(A.e, y, acc, t0, o0, sy, lane);
                 } else {
@@ -1175,12 +1195,12 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant_
 }
 
 // ------------------------------------------------------------------ host side
-template <int kBN, bool kAmn, bool kBmn, int kTerms, bool kPromote, bool kPair>
+template <int kBN, bool kAmn, bool kBmn, int kTerms, int kSums, bool kPair>
 dust_status launch_gemm(const GemmArgs& A, cudaStream_t s) {
     using S = Shape<kBN, kTerms, kPair>;
     static PerContextOnce attr;
     if (!attr.run([] {
-            return cudaFuncSetAttribute(linear_gemm_kernel<kBN, kAmn, kBmn, kTerms, kPromote, kPair>,
+            return cudaFuncSetAttribute(linear_gemm_kernel<kBN, kAmn, kBmn, kTerms, kSums, kPair>,
                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
                                         static_cast<int>(S::kSmem)) == cudaSuccess;
         }))
@@ -1188,8 +1208,8 @@ dust_status launch_gemm(const GemmArgs& A, cudaStream_t s) {
     const int64_t items = static_cast<int64_t>(A.m_tiles) * A.n_tiles * A.splits;
     const unsigned grid = static_cast<unsigned>(
         kPair ? 2 * std::min<int64_t>(items, num_sms() / 2) : std::min<int64_t>(items, num_sms()));
-    return dependent_launch(linear_gemm_kernel<kBN, kAmn, kBmn, kTerms, kPromote, kPair>, dim3(grid),
-                            kPromote ? kPromoteThreads : kThreads, S::kSmem, s, kPair ? 2 : 1, A)
+    return dependent_launch(linear_gemm_kernel<kBN, kAmn, kBmn, kTerms, kSums, kPair>, dim3(grid),
+                            kSums != kChain ? kPromoteThreads : kThreads, S::kSmem, s, kPair ? 2 : 1, A)
                ? DUST_OK
                : DUST_ERR_CUDA;
 }
@@ -1218,16 +1238,16 @@ int choose_bn(int64_t m_tiles, int n_out, int k_blocks) {
 
 // 256-column tiles of a bf16 output go to pairs of CTAs where the contraction is long enough to pay for
 // the pair's set-up (2304 columns over 8192 tokens, alone and in pairs: K = 256 15.5 and 18.5 us, 768 25.8 and
-// 23.9, 1536 43.1 and 40.9).  An fp32 output's sums change hands every 512 products, and a pair's do so more slowly.
-bool in_pairs(int bn, int k_blocks, int out_bf16) { return bn == 256 && out_bf16 && k_blocks >= 12; }
+// 23.9, 1536 43.1 and 40.9).  Sums that change hands every 512 products do so more slowly in a pair.
+bool in_pairs(int bn, int k_blocks, int out_bf16) { return bn == 256 && out_bf16 && k_blocks >= 12 && k_blocks <= kLongest; }
 
-template <bool kBmn, int kTerms, bool kPromote>
+template <bool kBmn, int kTerms, int kSums>
 dust_status launch_width(int bn, bool pair, const GemmArgs& A, cudaStream_t s) {
-    if constexpr (!kPromote)
-        if (pair) return launch_gemm<256, false, kBmn, kTerms, kPromote, true>(A, s);
-    return bn == 256   ? launch_gemm<256, false, kBmn, kTerms, kPromote, false>(A, s)
-           : bn == 128 ? launch_gemm<128, false, kBmn, kTerms, kPromote, false>(A, s)
-                       : launch_gemm<64, false, kBmn, kTerms, kPromote, false>(A, s);
+    if constexpr (kSums == kChain)
+        if (pair) return launch_gemm<256, false, kBmn, kTerms, kSums, true>(A, s);
+    return bn == 256   ? launch_gemm<256, false, kBmn, kTerms, kSums, false>(A, s)
+           : bn == 128 ? launch_gemm<128, false, kBmn, kTerms, kSums, false>(A, s)
+                       : launch_gemm<64, false, kBmn, kTerms, kSums, false>(A, s);
 }
 
 template <int kTok, bool kAmn>
@@ -1330,6 +1350,7 @@ dust_status gemm_rows(const void* a, int64_t ld_a, int terms, int K, const void*
     G.splits = 1;
     G.n_tiles = (n_out + bn - 1) / bn;
     if (m_tiles * G.n_tiles > 1 << 30) return DUST_ERR_UNSUPPORTED;
+    const int sums = !G.e.out_bf16 ? kToF32 : G.k_blocks > kLongest ? kToBf16 : kChain;
     const bool pair = in_pairs(bn, G.k_blocks, G.e.out_bf16);  // 256-row tiles, half of B's columns in each CTA
     G.m_tiles = static_cast<int>(pair ? (m_tiles + 1) / 2 : m_tiles);
     if (!make_tmap_bf16_2d_ld(&G.ta, a, static_cast<uint64_t>(terms * M), K, ld_a, kBM, kBK)) return DUST_ERR_CUDA;
@@ -1339,11 +1360,14 @@ dust_status gemm_rows(const void* a, int64_t ld_a, int terms, int K, const void*
     prof_begin(s);
     dust_status st;
     if (b_mn)
-        st = G.e.out_bf16 ? launch_width<true, 1, false>(bn, pair, G, s)
-             : terms == 2 ? launch_width<true, 2, true>(bn, pair, G, s)
-                          : launch_width<true, 1, true>(bn, pair, G, s);
+        st = sums == kChain      ? launch_width<true, 1, kChain>(bn, pair, G, s)
+             : sums == kToBf16   ? launch_width<true, 1, kToBf16>(bn, pair, G, s)
+             : terms == 2        ? launch_width<true, 2, kToF32>(bn, pair, G, s)
+                                 : launch_width<true, 1, kToF32>(bn, pair, G, s);
     else
-        st = G.e.out_bf16 ? launch_width<false, 1, false>(bn, pair, G, s) : launch_width<false, 1, true>(bn, pair, G, s);
+        st = sums == kChain    ? launch_width<false, 1, kChain>(bn, pair, G, s)
+             : sums == kToBf16 ? launch_width<false, 1, kToBf16>(bn, pair, G, s)
+                               : launch_width<false, 1, kToF32>(bn, pair, G, s);
     prof_end(s, form_name(b_mn ? kDx : kForward, bn, pair));
     return st;
 }
@@ -1394,9 +1418,9 @@ size_t dw_bytes(int64_t N, int32_t d_in, int32_t d_out) {
 }
 template <int kTerms>
 dust_status launch_dw(int bn, const GemmArgs& A, cudaStream_t s) {
-    return bn == 256   ? launch_gemm<256, true, true, kTerms, true, false>(A, s)
-           : bn == 128 ? launch_gemm<128, true, true, kTerms, true, false>(A, s)
-                       : launch_gemm<64, true, true, kTerms, true, false>(A, s);
+    return bn == 256   ? launch_gemm<256, true, true, kTerms, kToF32, false>(A, s)
+           : bn == 128 ? launch_gemm<128, true, true, kTerms, kToF32, false>(A, s)
+                       : launch_gemm<64, true, true, kTerms, kToF32, false>(A, s);
 }
 dust_status gemm_dw(const void* dz, int64_t ld_dz, int terms, const void* x, int64_t ld_x, int64_t N, int32_t d_in,
                     int32_t d_out, float* dW, int accumulate, float* part, int late, JoinArgs& join, cudaStream_t s) {
