@@ -123,10 +123,10 @@ dust_status dust_noisy_linear_output(const void* x, const void* W, dust_dtype dt
  * Row strides (elements) at least the row and a multiple of 16 bytes; all pointers 16-byte
  * aligned.  y may be the residual's buffer (with the same stride); other overlaps are not allowed.
  * Sums in fp32, handed over every 512 products for fp32 outputs and beyond d_in = 16384 (the tensor cores
- * truncate as they add: up to 6e-9 of the sum for each product in between); each output is rounded once.  Rows behind N and columns behind d_out are not
- * written.  One and two tokens stream W through the CUDA cores, more go to the tensor cores, in forms
- * chosen by the sizes, so the last bits of a token's sums can depend on how many tokens the call has.
- * Deterministic.
+ * truncate as they add: up to 6e-9 of the sum for each product in between); each output is rounded
+ * once.  N >= 1.  Rows behind N and columns behind d_out are not written.  One and two tokens stream W
+ * through the CUDA cores, more go to the tensor cores, in forms chosen by the sizes, so the last bits of a
+ * token's sums can depend on how many tokens the call has.  Deterministic.
  *   DUST_ACT_GELU: z Phi(z);  DUST_ACT_GELU_TANH: z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2;
  *   DUST_ACT_SILU: z / (1 + exp(-z));  DUST_ACT_RELU: max(z, 0).
  */
@@ -182,7 +182,8 @@ dust_status dust_embedding(const int32_t* ids, const void* E, dust_dtype dt, int
  *   G[v] (+)= scale sum_{t: ids_t = v} g_t
  * g: [N, ld_g] of type dt, the gradient (or output-error estimate) at the embedding's output; G: fp32
  * [V, ld_G].  accumulate == 0 overwrites all V rows (rows without tokens with zeros), accumulate != 0
- * adds to the rows that have tokens and leaves the others (for a table shared with the output layer).
+ * adds to the rows that have tokens and leaves the others (for a table shared with the output layer);
+ * values of G and sums below 2^-126 in magnitude may count as zero there.
  * Tokens whose id is outside [0, V) add nothing.  Sums in fp32, in token order within runs of sorted
  * tokens: deterministic.  N <= 2^26, V < 2^31 - 1, d <= 2^31 - 1024.
  * workspace: dust_workspace_size(DUST_OP_EMBEDDING_GRAD, dt, N, V, d, 0) bytes (0 for up to

@@ -670,7 +670,8 @@ def dust_linear_backward(dy, x, W, act: str = "none", z=None, dx=True, dW=True, 
                          dx_dtype=None, workspace=None, stream=None, g_terms: int = G_TERMS):
     """(dx, dW, db) of dust_linear from dy [N, d_out] (bf16 or fp32) and the pre-activation z that it
     kept (not needed for act="none"): dx [N, d_in] bf16 (or dx_dtype=torch.float32), dW fp32
-    [d_out, d_in], db fp32 [d_out].  Each output is True (allocated), a tensor, or None (skipped);
+    [d_out, d_in], db fp32 [d_out].  dz = dy act'(z) goes to the tensor cores as g_terms bf16 terms in dW and in
+    an fp32 dx, as one in a bf16 dx (a bf16 dy without an activation is exact in one).  Each output is True (allocated), a tensor, or None (skipped);
     accumulate=True adds to the given dW and db."""
     torch = _torch()
     bf, f32 = torch.bfloat16, torch.float32

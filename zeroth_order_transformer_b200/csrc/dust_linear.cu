@@ -1246,8 +1246,8 @@ int choose_bn(int64_t m_tiles, int n_out, int k_blocks) {
 }
 
 // 256-column tiles of a bf16 output go to pairs of CTAs where the contraction is long enough to pay for
-// the pair's set-up (2304 columns over 8192 tokens, alone and in pairs: K = 256 15.5 and 18.5 us, 768 25.8 and
-// 23.9, 1536 43.1 and 40.9).  Sums that change hands every 512 products do so more slowly in a pair.
+// the pair's set-up (2304 columns over 8192 tokens, kernel times on one set of buffers after a pause, alone and in pairs:
+// K = 256 15.5 and 18.5 us, 768 25.8 and 23.9, 1536 43.1 and 40.9).  Sums that change hands every 512 products do so more slowly in a pair.
 bool in_pairs(int bn, int k_blocks, int out_bf16) { return bn == 256 && out_bf16 && k_blocks >= 12 && k_blocks <= kLongest; }
 
 template <bool kBmn, int kTerms, int kSums>
