@@ -544,7 +544,7 @@ _DT = {}  # torch dtype -> C code, filled at the first use
 def _dtypes() -> dict:
     if not _DT:
         torch = _torch()
-        _DT[torch.bfloat16], _DT[torch.float32] = DUST_BF16, DUST_F32
+        _DT.update({torch.bfloat16: DUST_BF16, torch.float32: DUST_F32})  # both at once: another thread may look now
     return _DT
 
 
