@@ -103,6 +103,7 @@ __global__ void __launch_bounds__(kFThreads) embedding_kernel(const int32_t* ids
     V8 r[kFItems];
     int64_t at[kFItems];
     int left[kFItems];
+    float by[kFItems];
 #pragma unroll
     for (int j = 0; j < kFItems; ++j) {
         const int64_t f = base + j * kFThreads;
@@ -113,7 +114,9 @@ __global__ void __launch_bounds__(kFThreads) embedding_kernel(const int32_t* ids
             const int32_t id = ids[t];
             left[j] = d - c;
             at[j] = t * ld_out + c;
+            by[j] = 1.0f;
             if (id >= 0 && id < V) {
+                by[j] = scale;
                 r[j] = load8(E + static_cast<int64_t>(id) * ld_E + c, left[j]);
             } else {
                 const float fill = id < 0 ? 0.f : __uint_as_float(0x7FC00000u);
@@ -126,7 +129,7 @@ __global__ void __launch_bounds__(kFThreads) embedding_kernel(const int32_t* ids
     for (int j = 0; j < kFItems; ++j)
         if (left[j] > 0) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) r[j].v[k] *= scale;
+            for (int k = 0; k < 8; ++k) r[j].v[k] *= by[j];
             store8(out + at[j], r[j], left[j]);
         }
 }
